@@ -109,7 +109,8 @@ typedef enum {
     MOE_ERR_WORKSPACE = 3,     /* workspace smaller than moe_workspace_size() */
     MOE_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed */
     MOE_ERR_BAD_INDEX = 5,     /* (device) an expert id outside [0, E): the dispatch that saw it
-                                * publishes no rows (see moe_dispatch) */
+                                * publishes no rows (see moe_dispatch); or a group's rows out of
+                                * range or out of order (see "Grouped products") */
     MOE_ERR_TIMEOUT = 6        /* (device) a bounded wait ran out; outputs of that call are invalid */
 } moe_status_t;
 
@@ -368,6 +369,81 @@ moe_status_t moe_layer_bwd(const moe_config_t* cfg, const moe_bf16* x, const flo
                            moe_bf16* dx, float* dW_r, float* db_r,
                            moe_bf16* dW_gate, moe_bf16* dW_up, moe_bf16* dW_down,
                            void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---- Grouped products --------------------------------------------------------------------------
+ * Matrix products over rows grouped by expert, group g having a weight of its own and any number of
+ * rows: for an expert FFN other than the layer's SwiGLU one (another activation, a bias, one matrix,
+ * adapters), on the layer's dispatched rows (moe_segments) or on rows laid out by the caller.
+ *   moe_grouped_mm      y_r  = W[g] x_r                       for every row r of every group g
+ *   moe_grouped_mm_dx   dx_r = W[g]^T dy_r
+ *   moe_grouped_mm_dw   dW[g] = sum over the group's rows of dy_r x_r^T
+ *   moe_grouped_mm_i8   y_r  = s_r (P[g] q_r) t[g]            8-bit integers q, P with their scales s, t
+ *
+ * Groups.  row_begin, row_end [groups] int32 on the device: group g is rows row_begin[g] ..
+ * row_end[g] - 1.  Groups come in row order and do not overlap (0 <= row_begin[g] <= row_end[g] <=
+ * row_begin[g + 1], row_end[groups - 1] <= rows); any of them may be empty, of any length, and start
+ * at any row, and rows between groups belong to none.  The offsets [groups + 1] of packed groups serve
+ * as both arrays (row_end = offsets + 1).  Rows of no group are not read into any product and their
+ * outputs are not written.  Values out of range or out of order record MOE_ERR_BAD_INDEX
+ * (moe_check_error) and the call writes nothing.
+ *
+ * Numerics.  Products are exact and summed in fp32, and each output is rounded once.  NaN and
+ * infinities stay within the rows (moe_grouped_mm, _dx, _i8) or the group (_dw) that hold them. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
+
+typedef struct {
+    int64_t rows;              /* rows of x, y, dx, dy (0 allowed), <= 2^28 */
+    int32_t n_in, n_out;       /* widths of x and y: multiples of 8, 8 .. 65536 */
+    int32_t groups;            /* 1 .. 1024 */
+    int32_t dtype;             /* MOE_BF16 or MOE_FP16: x, y, dx, dy and W (moe_grouped_mm_i8: y) */
+    int32_t dw_dtype;          /* type of dW: dtype or MOE_FP32 */
+    int32_t accumulate;        /* 1: dW += the gradient (MOE_FP32 only); 0: dW is overwritten, with
+                                * zeros for an empty group */
+    int64_t in_stride;         /* elements between the rows of x and dx (moe_grouped_mm_i8: of the */
+    int64_t out_stride;        /* codes), and of y and dy: multiples of 8 (codes: 16), at least the
+                                * width; 0: the width */
+} moe_grouped_t;
+
+/* Workspace bytes for any call of this description; its header is zeroed once with
+ * moe_grouped_workspace_init.  It must be 256-byte aligned; calls that share it must be ordered on one
+ * stream.  moe_check_error reads and clears the errors recorded in it. */
+moe_status_t moe_grouped_workspace_size(const moe_grouped_t* cfg, size_t* ws_bytes);
+moe_status_t moe_grouped_workspace_init(const moe_grouped_t* cfg, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The groups of the rows that the last moe_dispatch on ws laid out (x_perm, o_perm): row_begin,
+ * row_end [E + n_shared], the padded segments P_g and their ends P_g + n_g. */
+moe_status_t moe_segments(const moe_config_t* cfg, int32_t* row_begin, int32_t* row_end, void* ws, size_t ws_bytes,
+                          moe_stream_t stream);
+
+/* x [rows, n_in], W [groups, n_out, n_in] -> y [rows, n_out]. */
+moe_status_t moe_grouped_mm(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end, const void* x,
+                            const void* W, void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* dy [rows, n_out], W [groups, n_out, n_in] -> dx [rows, n_in].  (Also the forward product of weights
+ * stored [groups, in, out].) */
+moe_status_t moe_grouped_mm_dx(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
+                               const void* dy, const void* W, void* dx, void* ws, size_t ws_bytes,
+                               moe_stream_t stream);
+
+/* dy [rows, n_out], x [rows, n_in] -> dW [groups, n_out, n_in]. */
+moe_status_t moe_grouped_mm_dw(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
+                               const void* dy, const void* x, void* dW, void* ws, size_t ws_bytes,
+                               moe_stream_t stream);
+
+/* Rows of 8-bit integers: src [rows, cols] (dtype MOE_BF16 or MOE_FP16) -> codes [rows, cols] and
+ * scales [rows] fp32, scale = amax / 127 over the row (1 where that is zero) and code = v / scale
+ * rounded to nearest even, at most 127 in magnitude, all in fp32.  A NaN or an infinity in a row
+ * makes its scale NaN, and so its products.  For activations (one scale per token) and for the rows of
+ * weights (one per output channel).  cols a multiple of 16, at most 65536; 16-byte-aligned pointers. */
+moe_status_t moe_quantize_rows_i8(const void* src, int32_t dtype, int64_t rows, int32_t cols, int8_t* codes,
+                                  float* scales, moe_stream_t stream);
+
+/* codes [rows, n_in] int8, scales [rows] fp32, Wq [groups, n_out, n_in] int8, W_scale [groups, n_out]
+ * fp32 -> y [rows, n_out] (dtype).  n_in a multiple of 16.  One group is a dense product.  The sums of
+ * integer products are exact up to 2^24 in magnitude and rounded as fp32 sums beyond it. */
+moe_status_t moe_grouped_mm_i8(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
+                               const int8_t* codes, const float* scales, const int8_t* Wq, const float* W_scale,
+                               void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Synchronise `stream`, return the first device-side error recorded in ws since the last check
  * (MOE_OK if none) and clear it.  Returns MOE_ERR_CUDA if the stream itself reports an error. */

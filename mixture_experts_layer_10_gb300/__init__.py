@@ -28,7 +28,9 @@ EXPORTS = ("moe_workspace_size", "moe_perm_rows", "moe_workspace_init", "moe_rou
            "moe_debug_inject", "moe_profile_enable", "moe_profile_read", "moe_status_string",
            "moe_quantize_rows_e4m3", "moe_gate_up_fp8", "moe_down_fp8", "moe_layer_fwd_fp8",
            "moe_keep_rows_for_budget", "moe_keep_rows_for_free_memory", "moe_quantize_cols_e4m3",
-           "moe_layer_bwd_fp8", "moe_saved_layout", "moe_profile_sm_clock")
+           "moe_layer_bwd_fp8", "moe_saved_layout", "moe_profile_sm_clock", "moe_grouped_workspace_size",
+           "moe_grouped_workspace_init", "moe_segments", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
+           "moe_quantize_rows_i8", "moe_grouped_mm_i8")
 
 
 class moe_config_t(ctypes.Structure):
@@ -36,6 +38,16 @@ class moe_config_t(ctypes.Structure):
                 ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("n_shared", ctypes.c_int32),
                 ("renorm", ctypes.c_int32), ("capacity_factor", ctypes.c_float),
                 ("keep_rows", ctypes.c_int32), ("gather_in_gemm", ctypes.c_int32)]
+
+
+class moe_grouped_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("in_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
+# moe_dtype_t
+BF16, FP16, FP32 = 0, 1, 2
 
 
 class MoEError(RuntimeError):
@@ -59,6 +71,7 @@ def load(path: str | None = None):
         _build.build()
     lib = ctypes.CDLL(path)
     cfgp = ctypes.POINTER(moe_config_t)
+    grpp = ctypes.POINTER(moe_grouped_t)
     sig = {
         "moe_workspace_size": [cfgp, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)],
         "moe_perm_rows": [cfgp, ctypes.POINTER(ctypes.c_int64)],
@@ -92,6 +105,14 @@ def load(path: str | None = None):
         "moe_profile_sm_clock": [ctypes.c_int32, ctypes.POINTER(ctypes.c_double)],
         "moe_profile_read": [ctypes.c_int32, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_double),
                              ctypes.POINTER(ctypes.c_int32)],
+        "moe_grouped_workspace_size": [grpp, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_grouped_workspace_init": [grpp, _P, ctypes.c_size_t, _P],
+        "moe_segments": [cfgp, _P, _P, _P, ctypes.c_size_t, _P],
+        "moe_grouped_mm": [grpp, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+        "moe_grouped_mm_dx": [grpp, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+        "moe_grouped_mm_dw": [grpp, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+        "moe_quantize_rows_i8": [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P, _P, _P],
+        "moe_grouped_mm_i8": [grpp, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
         "moe_status_string": [ctypes.c_int],
     }
     for name, args in sig.items():
@@ -112,6 +133,34 @@ def config(T: int, d: int, f: int, E: int, k: int, S: int = 0, renorm: int = 0, 
                         int(gather_in_gemm))
 
 
+def dtype_code(t) -> int:
+    """moe_dtype_t of a torch dtype (or the code itself)."""
+    if isinstance(t, int):
+        return t
+    code = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}.get(str(t))
+    if code is None:
+        raise ValueError(f"no grouped product of {t}")
+    return code
+
+
+def grouped_config(rows: int, n_in: int, n_out: int, groups: int, dtype=BF16, dw_dtype=None, accumulate: int = 0,
+                   in_stride: int = 0, out_stride: int = 0) -> moe_grouped_t:
+    """Description of the grouped products of [rows, n_in] rows with weights [groups, n_out, n_in]; the
+    types are torch dtypes or moe_dtype_t codes, dW's the operands' unless given."""
+    code = dtype_code(dtype)
+    return moe_grouped_t(int(rows), int(n_in), int(n_out), int(groups), code,
+                         code if dw_dtype is None else dtype_code(dw_dtype), int(accumulate), int(in_stride),
+                         int(out_stride))
+
+
+def grouped_workspace(cfg: moe_grouped_t, device="cuda", stream=None):
+    """A device workspace for the grouped products of cfg, its header initialised."""
+    import torch
+    ws = torch.empty(moe_grouped_workspace_size(cfg), dtype=torch.uint8, device=device)
+    moe_grouped_workspace_init(cfg, ws, stream)
+    return ws
+
+
 def config_from(c: dict) -> moe_config_t:
     """From a workload dict with keys T, d, f, E, k, S, renorm, cf (and keep_rows, gather_in_gemm,
     default 0)."""
@@ -126,6 +175,26 @@ def _ptr(t):
         return t
     if not t.is_contiguous():
         raise ValueError("tensors passed to the MoE library must be contiguous")
+    return t.data_ptr()
+
+
+_HOLDS = {BF16: ("torch.bfloat16", "torch.int16", "torch.uint16"), FP16: ("torch.float16", "torch.int16", "torch.uint16"),
+          FP32: ("torch.float32",), "i32": ("torch.int32",), "i8": ("torch.int8",)}
+
+
+def _grouped_ptr(t, shape, kind, what, stride=0):
+    """Pointer of an operand of the grouped products: a CUDA tensor of this shape and type, contiguous
+    but for the rows of a matrix, which may be `stride` elements apart.  None and integers pass."""
+    if t is None or isinstance(t, int):
+        return t
+    if tuple(t.shape) != shape or str(t.dtype) not in _HOLDS[kind] or not t.is_cuda:
+        raise ValueError(f"{what}: CUDA tensor {shape} of {_HOLDS[kind][0]} expected, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    if stride and stride != shape[1]:
+        if t.numel() and (t.stride(1) != 1 or (shape[0] > 1 and t.stride(0) != stride)):
+            raise ValueError(f"{what}: rows {stride} elements apart expected, got strides {t.stride()}")
+    elif not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous tensor expected, got strides {t.stride()}")
     return t.data_ptr()
 
 
@@ -284,6 +353,72 @@ def moe_layer_bwd(cfg, x, W_r, b_r, W_gate, W_up, W_down, saved, dy, dx, dW_r, d
     _call("moe_layer_bwd", ctypes.byref(cfg), _ptr(x), _ptr(W_r), _ptr(b_r), _ptr(W_gate), _ptr(W_up),
           _ptr(W_down), _ptr(saved), _ptr(dy), _ptr(dx), _ptr(dW_r), _ptr(db_r), _ptr(dW_gate),
           _ptr(dW_up), _ptr(dW_down), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_segments(cfg, row_begin, row_end, ws, stream=None):
+    """begin and end [E + S] int32 of the padded segments of the last moe_dispatch on ws."""
+    n = (cfg.E + cfg.n_shared,)
+    _call("moe_segments", ctypes.byref(cfg), _grouped_ptr(row_begin, n, "i32", "row_begin"),
+          _grouped_ptr(row_end, n, "i32", "row_end"), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_grouped_workspace_size(cfg: moe_grouped_t) -> int:
+    n = ctypes.c_size_t()
+    _call("moe_grouped_workspace_size", ctypes.byref(cfg), ctypes.byref(n))
+    return n.value
+
+
+def moe_grouped_workspace_init(cfg, ws, stream=None):
+    _call("moe_grouped_workspace_init", ctypes.byref(cfg), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_grouped_mm(cfg, row_begin, row_end, x, W, y, ws, stream=None):
+    """y = x W[g]^T for the rows of every group g."""
+    c, n = cfg, (cfg.groups,)
+    _call("moe_grouped_mm", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin"),
+          _grouped_ptr(row_end, n, "i32", "row_end"), _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", c.in_stride),
+          _grouped_ptr(W, (c.groups, c.n_out, c.n_in), c.dtype, "W"),
+          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", c.out_stride), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_grouped_mm_dx(cfg, row_begin, row_end, dy, W, dx, ws, stream=None):
+    """dx = dy W[g] for the rows of every group g."""
+    c, n = cfg, (cfg.groups,)
+    _call("moe_grouped_mm_dx", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin"),
+          _grouped_ptr(row_end, n, "i32", "row_end"), _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", c.out_stride),
+          _grouped_ptr(W, (c.groups, c.n_out, c.n_in), c.dtype, "W"),
+          _grouped_ptr(dx, (c.rows, c.n_in), c.dtype, "dx", c.in_stride), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_grouped_mm_dw(cfg, row_begin, row_end, dy, x, dW, ws, stream=None):
+    """dW[g] = dy^T x over the rows of group g; with cfg.accumulate added to dW."""
+    c, n = cfg, (cfg.groups,)
+    _call("moe_grouped_mm_dw", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin"),
+          _grouped_ptr(row_end, n, "i32", "row_end"), _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", c.out_stride),
+          _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", c.in_stride),
+          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), c.dw_dtype, "dW"), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_quantize_rows_i8(src, codes, scales, stream=None):
+    """src [.., rows, cols] bf16 or fp16 -> codes of the same shape int8, scales [.., rows] fp32."""
+    cols = src.shape[-1]
+    rows = src.numel() // cols if cols else 0
+    code = dtype_code(src.dtype)
+    _call("moe_quantize_rows_i8", _grouped_ptr(src, tuple(src.shape), code, "src"), code, int(rows), int(cols),
+          _grouped_ptr(codes, tuple(src.shape), "i8", "codes"),
+          _grouped_ptr(scales, tuple(src.shape[:-1]), FP32, "scales"), _stream(stream))
+
+
+def moe_grouped_mm_i8(cfg, row_begin, row_end, codes, scales, Wq, W_scale, y, ws, stream=None):
+    """y = (codes Wq[g]^T) scaled by the rows' and the output channels' scales."""
+    c, n = cfg, (cfg.groups,)
+    _call("moe_grouped_mm_i8", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin"),
+          _grouped_ptr(row_end, n, "i32", "row_end"),
+          _grouped_ptr(codes, (c.rows, c.n_in), "i8", "codes", c.in_stride),
+          _grouped_ptr(scales, (c.rows,), FP32, "scales"),
+          _grouped_ptr(Wq, (c.groups, c.n_out, c.n_in), "i8", "Wq"),
+          _grouped_ptr(W_scale, (c.groups, c.n_out), FP32, "W_scale"),
+          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", c.out_stride), _ptr(ws), ws.numel(), _stream(stream))
 
 
 def moe_check_error(ws, stream=None) -> int:

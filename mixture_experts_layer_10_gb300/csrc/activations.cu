@@ -14,6 +14,7 @@
 // overwrite them in place, each element read before it is written, by the same thread.
 #include <algorithm>
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -252,7 +253,52 @@ __global__ void col_scales_kernel(const uint32_t* __restrict__ amax_bits, float*
   }
 }
 
+// ---- 8-bit integer rows: scale = amax / 127 over the row, code = v / scale to nearest even, one
+// block a row.
+__global__ void __launch_bounds__(256) quantize_rows_i8_kernel(const uint16_t* __restrict__ src, bool fp16, int64_t rows,
+                                                               int cols, int8_t* __restrict__ codes,
+                                                               float* __restrict__ scales) {
+  __shared__ float part[8];
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const uint16_t* row = src + r * cols;
+    auto value = [&](int i) {
+      return fp16 ? __half2float(__ushort_as_half(row[i])) : __uint_as_float((uint32_t)row[i] << 16);
+    };
+    float amax = 0.f;
+    for (int i = threadIdx.x; i < cols; i += 256) {
+      const float a = fabsf(value(i));
+      amax = (a > amax || a != a) ? a : amax;   // a NaN stays
+    }
+    for (int off = 16; off > 0; off >>= 1) {
+      const float a = __shfl_xor_sync(0xffffffffu, amax, off);
+      amax = (a > amax || a != a) ? a : amax;
+    }
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) amax = (part[w] > amax || part[w] != part[w]) ? part[w] : amax;
+    float scale = __fdiv_rn(amax, 127.f);
+    if (scale == 0.f) scale = 1.f;
+    if (!(scale <= 3.4028235e38f)) scale = __int_as_float(0x7fc00000);
+    if (threadIdx.x == 0) scales[r] = scale;
+    for (int i = threadIdx.x; i < cols; i += 256) {
+      const float q = rintf(__fdiv_rn(value(i), scale));
+      codes[r * cols + i] = q == q ? (int8_t)fmaxf(-127.f, fminf(127.f, q)) : (int8_t)0;
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_quantize_rows_i8(const uint16_t* src, bool fp16, int64_t rows, int cols, int8_t* codes,
+                                    float* scales, cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  prof_mark(kKQuantI8, s, true);
+  quantize_rows_i8_kernel<<<(int)std::min<int64_t>(rows, (int64_t)num_sms() * 8), 256, 0, s>>>(src, fp16, rows, cols,
+                                                                                             codes, scales);
+  prof_mark(kKQuantI8, s, false);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_quantize_rows_e4m3(const uint16_t* src, int64_t rows, int cols, uint8_t* codes, float* scales,
                                       cudaStream_t s, const Tables* tabs) {

@@ -234,7 +234,8 @@ const char* const kKernelNames[] = {
     "router_dlogits", "router_dwr", "router_reduce", "combine_bwd", "gemm_bwd_dgrad_down",
     "gemm_router_dx", "swiglu_bwd_kept", "gemm_gate_up_fp8", "quantize_e4m3", "gemm_down_fp8",
     "quantize_cols_e4m3", "gemm_bwd_dgrad_down_fp8", "gemm_bwd_recompute_swiglu_fp8", "gemm_dgrad_x_fp8",
-    "router_split_wr", "to_bf16_rows"};
+    "router_split_wr", "to_bf16_rows", "grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "grouped_mm_i8",
+    "quantize_i8"};
 static_assert(sizeof(kKernelNames) / sizeof(kKernelNames[0]) == kKCount, "a name for every kernel id");
 
 struct Profiler {
@@ -295,6 +296,38 @@ using namespace moe;
   } while (0)
 
 namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A validated description of grouped products.
+moe_status_t make_grouped(const moe_grouped_t* in, Grouped* c) {
+  if (in == nullptr) return MOE_ERR_INVALID_ARG;
+  const moe_grouped_t& m = *in;
+  MOE_NEED(m.rows >= 0 && m.rows <= (int64_t)1 << 28 && m.n_in >= 8 && m.n_in <= 65536 && m.n_in % 8 == 0 &&
+           m.n_out >= 8 && m.n_out <= 65536 && m.n_out % 8 == 0 && m.groups >= 1 && m.groups <= kMaxGroups);
+  MOE_NEED((m.dtype == MOE_BF16 || m.dtype == MOE_FP16) && (m.dw_dtype == m.dtype || m.dw_dtype == MOE_FP32));
+  MOE_NEED(m.accumulate == 0 || (m.accumulate == 1 && m.dw_dtype == MOE_FP32));
+  c->rows = m.rows;
+  c->K = m.n_in;
+  c->N = m.n_out;
+  c->G = m.groups;
+  c->ldi = m.in_stride != 0 ? m.in_stride : m.n_in;
+  c->ldo = m.out_stride != 0 ? m.out_stride : m.n_out;
+  // (2^31: the byte strides stay below the 2^40 a tensor map takes)
+  MOE_NEED(c->ldi >= c->K && c->ldi % 8 == 0 && c->ldi <= (int64_t)1 << 31 && c->ldo >= c->N && c->ldo % 8 == 0 &&
+           c->ldo <= (int64_t)1 << 31);
+  c->fp16 = m.dtype == MOE_FP16;
+  c->dw_fp32 = m.dw_dtype == MOE_FP32;
+  c->acc = m.accumulate == 1;
+  return MOE_OK;
+}
+
+moe_status_t get_grouped_ws(void* ws, size_t ws_bytes, Hdr** hdr) {
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(Hdr)) return MOE_ERR_WORKSPACE;
+  *hdr = static_cast<Hdr*>(ws);
+  return MOE_OK;
+}
 
 moe_status_t do_dispatch(const Cfg& c, const Ws& w, const int32_t* idx, const uint16_t* x,
                          const uint16_t* dy, const float* gates, int32_t* counts, int32_t* offsets,
@@ -954,6 +987,106 @@ moe_status_t moe_layer_bwd_fp8(const moe_config_t* cfg, const moe_bf16* x, const
       sv.logits_bytes ? reinterpret_cast<const float*>(static_cast<const char*>(saved) + sv.logits_off) : nullptr;
   MOE_TRY(do_router_bwd_saved(c, w, x, logits, idx, gates, dgates, dlogits, dW_r, db_r, stream));
   return do_combine_bwd(c, w, w.at<uint16_t>(w.L.buf_d1), dlogits, W_r, dx, stream, true);
+}
+
+moe_status_t moe_grouped_workspace_size(const moe_grouped_t* cfg, size_t* ws_bytes) {
+  Grouped c;
+  MOE_TRY(make_grouped(cfg, &c));
+  MOE_NEED(ws_bytes != nullptr);
+  *ws_bytes = sizeof(Hdr);
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_workspace_init(const moe_grouped_t* cfg, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Grouped c;
+  Hdr* hdr = nullptr;
+  MOE_TRY(make_grouped(cfg, &c));
+  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_CUDA(cudaMemsetAsync(hdr, 0, sizeof(Hdr), stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_segments(const moe_config_t* cfg, int32_t* row_begin, int32_t* row_end, void* ws, size_t ws_bytes,
+                          moe_stream_t stream) {
+  Cfg c;
+  MOE_TRY(make_cfg(cfg, &c));
+  MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
+  Ws w;
+  MOE_TRY(get_ws(c, ws, ws_bytes, &w));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_segments(w.tabs(), c.G, row_begin, row_end, stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_mm(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end, const void* x,
+                            const void* W, void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Grouped c;
+  Hdr* hdr = nullptr;
+  MOE_TRY(make_grouped(cfg, &c));
+  MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
+  MOE_NEED(W && aligned16(W) && (c.rows == 0 || (x && y)) && aligned16(x) && aligned16(y));
+  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_grouped_mm(c, row_begin, row_end, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(W),
+                             static_cast<uint16_t*>(y), hdr, stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_mm_dx(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
+                               const void* dy, const void* W, void* dx, void* ws, size_t ws_bytes,
+                               moe_stream_t stream) {
+  Grouped c;
+  Hdr* hdr = nullptr;
+  MOE_TRY(make_grouped(cfg, &c));
+  MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
+  MOE_NEED(W && aligned16(W) && (c.rows == 0 || (dy && dx)) && aligned16(dy) && aligned16(dx));
+  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_grouped_dx(c, row_begin, row_end, static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(W),
+                             static_cast<uint16_t*>(dx), hdr, stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_mm_dw(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
+                               const void* dy, const void* x, void* dW, void* ws, size_t ws_bytes,
+                               moe_stream_t stream) {
+  Grouped c;
+  Hdr* hdr = nullptr;
+  MOE_TRY(make_grouped(cfg, &c));
+  MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
+  MOE_NEED(dW && aligned16(dW) && (c.rows == 0 || (dy && x)) && aligned16(dy) && aligned16(x));
+  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_grouped_dw(c, row_begin, row_end, static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
+                             dW, hdr, stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_rows_i8(const void* src, int32_t dtype, int64_t rows, int32_t cols, int8_t* codes,
+                                  float* scales, moe_stream_t stream) {
+  MOE_NEED((dtype == MOE_BF16 || dtype == MOE_FP16) && rows >= 0 && cols >= 16 && cols <= 65536 && cols % 16 == 0);
+  MOE_NEED(rows == 0 || (src && codes && scales && aligned16(src) && aligned16(codes) && aligned16(scales)));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_quantize_rows_i8(static_cast<const uint16_t*>(src), dtype == MOE_FP16, rows, cols, codes, scales,
+                                   stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_mm_i8(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
+                               const int8_t* codes, const float* scales, const int8_t* Wq, const float* W_scale,
+                               void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Grouped c;
+  Hdr* hdr = nullptr;
+  MOE_TRY(make_grouped(cfg, &c));
+  MOE_NEED(c.K % 16 == 0 && c.ldi % 16 == 0);
+  MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
+  MOE_NEED(Wq && W_scale && aligned16(Wq) && aligned16(W_scale) && (c.rows == 0 || (codes && scales && y)) &&
+           aligned16(codes) && aligned16(scales) && aligned16(y));
+  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_grouped_i8(c, row_begin, row_end, codes, scales, Wq, W_scale, static_cast<uint16_t*>(y), hdr,
+                             stream));
+  return MOE_OK;
 }
 
 moe_status_t moe_check_error(void* ws, moe_stream_t stream) {

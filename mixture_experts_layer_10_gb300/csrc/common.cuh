@@ -28,6 +28,11 @@ enum Site : int32_t {
   kSiteGemmProducer = 10,
   kSiteGemmMma = 11,
   kSiteGemmEpilogue = 12,
+  kSiteGroups = 20,
+  kSiteGroupedProducer = 21,
+  kSiteGroupedMma = 22,
+  kSiteGroupedEpilogue = 23,
+  kSiteGroupedStage = 24,
 };
 
 // Header at workspace offset 0.  `status`..`timeout_ns` persist across calls (cleared by
@@ -142,7 +147,7 @@ enum KernelId : int {
   kKRoute = 0, kKScan, kKGather, kKGateUp, kKDown, kKCombine, kKBwdFused, kKWgrad, kKDgradX,
   kKDgates, kKRouterDlogits, kKRouterDwr, kKRouterReduce, kKCombineBwd, kKBwdDh, kKRouterDx, kKSwigluKept,
   kKGateUpFp8, kKQuantE4m3, kKDownFp8, kKQuantCols, kKBwdDhFp8, kKBwdFusedFp8, kKDgradXFp8, kKSplitWr,
-  kKToBf16, kKCount
+  kKToBf16, kKGroupedMm, kKGroupedDx, kKGroupedDw, kKGroupedI8, kKQuantI8, kKCount
 };
 void prof_mark(int id, cudaStream_t s, bool begin);
 // In-kernel SM clock of the GEMM kernels (gemm.cu): per kernel id, summed clock64 cycles and
@@ -326,5 +331,26 @@ struct DownFp8Args {
   const Tables* tabs;
 };
 cudaError_t launch_down_fp8(const Cfg& c, const Layout& L, const DownFp8Args& a, cudaStream_t s);
+
+// Grouped products (grouped.cu): rows of group g times its weight, or the rows' outer products.
+struct Grouped {           // validated description
+  int64_t rows, ldi, ldo;  // row strides of the n_in-wide and the n_out-wide operand, in elements
+  int K, N, G;             // n_in, n_out, groups
+  bool fp16, dw_fp32, acc;
+};
+constexpr int kMaxGroups = 1024;
+cudaError_t launch_grouped_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
+                              const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s);
+cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* dy,
+                              const uint16_t* W, uint16_t* dx, Hdr* hdr, cudaStream_t s);
+cudaError_t launch_grouped_dw(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* dy,
+                              const uint16_t* x, void* dW, Hdr* hdr, cudaStream_t s);
+cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,
+                              const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr,
+                              cudaStream_t s);
+cudaError_t launch_segments(const Tables* tabs, int G, int32_t* begin, int32_t* end, cudaStream_t s);
+// 8-bit integer rows: codes [rows, cols] and one fp32 scale per row (amax / 127)
+cudaError_t launch_quantize_rows_i8(const uint16_t* src, bool fp16, int64_t rows, int cols, int8_t* codes,
+                                    float* scales, cudaStream_t s);
 
 }  // namespace moe
