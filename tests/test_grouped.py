@@ -341,6 +341,35 @@ def test_repeats_streams_and_graphs(moe, sizes):
     assert moe.moe_check_error(ws) == 0
 
 
+@pytest.mark.parametrize("op", ["mm", "dx", "dw", "i8"])
+def test_a_wait_that_runs_out_is_reported(moe, op):
+    """A fill of the operand ring that never comes ends in MOE_ERR_TIMEOUT, and the next call runs."""
+    sizes, K, N = [600, 70], 256, 256
+    begin, end, rows = layout(sizes)
+    cfg = moe.grouped_config(rows, K, N, 2)
+    ws = moe.grouped_workspace(cfg)
+    b, e = dev_i32(begin), dev_i32(end)
+    x, W = rand((rows, K), torch.bfloat16, 1), rand((2, N, K), torch.bfloat16, 2)
+    q, qs = torch.ones(rows, K, dtype=torch.int8, device="cuda"), torch.ones(rows, device="cuda")
+    Wq, Ws = torch.ones(2, N, K, dtype=torch.int8, device="cuda"), torch.ones(2, N, device="cuda")
+    out = torch.zeros((2, N, K) if op == "dw" else (rows, K), dtype=torch.bfloat16, device="cuda")
+    call = {"mm": lambda: moe.moe_grouped_mm(cfg, b, e, x, W, out, ws),
+            "dx": lambda: moe.moe_grouped_mm_dx(cfg, b, e, x, W, out, ws),
+            "dw": lambda: moe.moe_grouped_mm_dw(cfg, b, e, x, x, out, ws),
+            "i8": lambda: moe.moe_grouped_mm_i8(cfg, b, e, q, qs, Wq, Ws, out, ws)}[op]
+    call()
+    assert moe.moe_check_error(ws) == 0
+    good = out.clone()
+    moe.moe_debug_inject(ws, -1, 20_000_000, stall_fill=1)
+    call()
+    assert moe.moe_check_error(ws) == 6
+    moe.moe_debug_inject(ws, -1, 0)
+    out.zero_()
+    call()
+    assert moe.moe_check_error(ws) == 0
+    assert torch.equal(out, good)
+
+
 def test_far_rows(moe):
     """Element offsets past 32 bits: rows far apart in a large buffer."""
     rows, K, N, stride = 300, 64, 72, 1 << 24   # 300 rows x 16 Mi elements
