@@ -253,38 +253,92 @@ __global__ void col_scales_kernel(const uint32_t* __restrict__ amax_bits, float*
   }
 }
 
-// ---- 8-bit integer rows: scale = amax / 127 over the row, code = v / scale to nearest even, one
-// block a row.
-__global__ void __launch_bounds__(256) quantize_rows_i8_kernel(const uint16_t* __restrict__ src, bool fp16, int64_t rows,
-                                                               int cols, int8_t* __restrict__ codes,
-                                                               float* __restrict__ scales) {
-  __shared__ float part[8];
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const uint16_t* row = src + r * cols;
-    auto value = [&](int i) {
-      return fp16 ? __half2float(__ushort_as_half(row[i])) : __uint_as_float((uint32_t)row[i] << 16);
-    };
+// ---- 8-bit integer rows: per row, amax over the row, scale = amax / 127 in fp32 (1 where that is
+// zero), codes = v / scale rounded to the nearest integer.  A block takes a row and
+// keeps it in registers between the maximum and the codes; many blocks an SM keep rows in flight.  The quotient from the row's reciprocal (div_by_scale) is the
+// correctly rounded one wherever the code is not zero.  A row with a NaN or an infinity gets a NaN scale and zero
+// codes, which make its products NaN.
+
+__device__ __forceinline__ void unpack8(const uint4& u, bool fp16, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    if (fp16) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[m]));
+      f[2 * m] = v.x;
+      f[2 * m + 1] = v.y;
+    } else {
+      f[2 * m] = bf16_lo(w[m]);
+      f[2 * m + 1] = bf16_hi(w[m]);
+    }
+  }
+}
+
+// The larger of two magnitudes; a NaN stays.
+__device__ __forceinline__ float amax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight values to eight codes: the quotient plus 1.5 x 2^23 leaves the nearest integer (ties to even)
+// in the low bits of the sum.
+template <bool kRecip>
+__device__ __forceinline__ uint2 encode8_i8(const float (&f)[8], float scale, float y) {
+  uint32_t c[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float q = kRecip ? div_by_scale(f[i], scale, y) : __fdiv_rn(f[i], scale);
+    q = fminf(127.f, fmaxf(-127.f, q));
+    c[i / 4] |= (__float_as_uint(q + 12582912.f) & 0xFFu) << (8 * (i % 4));
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+template <int kThreads, int NV>
+__global__ void __launch_bounds__(kThreads) quantize_rows_i8_kernel(const uint16_t* __restrict__ src, bool fp16,
+                                                                   int64_t rows, int cols, int8_t* __restrict__ codes,
+                                                                   float* __restrict__ scales) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float part[2][kWarps];   // per-warp maxima, double-buffered across rows
+  const int nvec = cols / 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int buf = 0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, buf ^= 1) {
+    uint4 v[NV];
+    load_row<NV>(src, cols, nullptr, 0, r, nvec, nvec, kThreads, v);
     float amax = 0.f;
-    for (int i = threadIdx.x; i < cols; i += 256) {
-      const float a = fabsf(value(i));
-      amax = (a > amax || a != a) ? a : amax;   // a NaN stays
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[8];
+      unpack8(v[i], fp16, f);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) amax = amax_nan(amax, fabsf(f[m]));
     }
-    for (int off = 16; off > 0; off >>= 1) {
-      const float a = __shfl_xor_sync(0xffffffffu, amax, off);
-      amax = (a > amax || a != a) ? a : amax;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if (kWarps > 1) {
+      if (lane == 0) part[buf][warp] = amax;
+      __syncthreads();   // also orders the previous row's reads of part[buf ^ 1] before its next writes
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) amax = amax_nan(amax, part[buf][w]);
     }
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    for (int w = 0; w < 8; ++w) amax = (part[w] > amax || part[w] != part[w]) ? part[w] : amax;
+    const bool finite = amax <= 3.4028235e38f;
     float scale = __fdiv_rn(amax, 127.f);
     if (scale == 0.f) scale = 1.f;
-    if (!(scale <= 3.4028235e38f)) scale = __int_as_float(0x7fc00000);
-    if (threadIdx.x == 0) scales[r] = scale;
-    for (int i = threadIdx.x; i < cols; i += 256) {
-      const float q = rintf(__fdiv_rn(value(i), scale));
-      codes[r * cols + i] = q == q ? (int8_t)fmaxf(-127.f, fminf(127.f, q)) : (int8_t)0;
+    if (threadIdx.x == 0) scales[r] = finite ? scale : __int_as_float(0x7fffffff);
+    uint2* out = reinterpret_cast<uint2*>(codes + r * cols);
+    const bool recip = e4m3_recip_ok(scale);
+    const float y = __frcp_rn(scale);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int q = threadIdx.x + i * kThreads;
+      if (q >= nvec) continue;
+      float f[8];
+      unpack8(v[i], fp16, f);
+      if (!finite) out[q] = make_uint2(0u, 0u);
+      else out[q] = recip ? encode8_i8<true>(f, scale, y) : encode8_i8<false>(f, scale, y);
     }
-    __syncthreads();
   }
 }
 
@@ -294,8 +348,14 @@ cudaError_t launch_quantize_rows_i8(const uint16_t* src, bool fp16, int64_t rows
                                     float* scales, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
   prof_mark(kKQuantI8, s, true);
-  quantize_rows_i8_kernel<<<(int)std::min<int64_t>(rows, (int64_t)num_sms() * 8), 256, 0, s>>>(src, fp16, rows, cols,
-                                                                                             codes, scales);
+  // up to four vectors of eight values a thread; past 32768 values, eight
+  const int nvec = cols / 8, blocks = (int)std::min<int64_t>(rows, 1 << 30);
+  if (nvec <= 4 * 32) quantize_rows_i8_kernel<32, 4><<<blocks, 32, 0, s>>>(src, fp16, rows, cols, codes, scales);
+  else if (nvec <= 4 * 64) quantize_rows_i8_kernel<64, 4><<<blocks, 64, 0, s>>>(src, fp16, rows, cols, codes, scales);
+  else if (nvec <= 4 * 128) quantize_rows_i8_kernel<128, 4><<<blocks, 128, 0, s>>>(src, fp16, rows, cols, codes, scales);
+  else if (nvec <= 4 * 256) quantize_rows_i8_kernel<256, 4><<<blocks, 256, 0, s>>>(src, fp16, rows, cols, codes, scales);
+  else if (nvec <= 4 * 1024) quantize_rows_i8_kernel<1024, 4><<<blocks, 1024, 0, s>>>(src, fp16, rows, cols, codes, scales);
+  else quantize_rows_i8_kernel<1024, 8><<<blocks, 1024, 0, s>>>(src, fp16, rows, cols, codes, scales);
   prof_mark(kKQuantI8, s, false);
   return cudaGetLastError();
 }

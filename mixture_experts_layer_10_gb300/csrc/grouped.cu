@@ -119,8 +119,8 @@ constexpr uint32_t kEpiBox = 32 * 64;        // a staging box: 32 rows of 64 byt
 
 template <int kOp>
 struct Shape {
-  static constexpr int kStages = kOp == kI8 ? 3 : 6;       // 16-bit K blocks
-  static constexpr int kRaw = kOp == kI8 ? 3 : 0;          // 8-bit blocks, 128 codes deep
+  static constexpr int kStages = kOp == kI8 ? 4 : 6;       // 16-bit K blocks
+  static constexpr int kRaw = kOp == kI8 ? 2 : 0;          // 8-bit blocks, 128 codes deep
   static constexpr int kWiden = 8;                         // warps that widen codes
   static constexpr int kExtra = kOp == kI8 ? kWiden : (kOp == kDw ? 1 : 0);
   static constexpr int kThreads = 32 * (6 + kExtra);
@@ -433,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
-      mbar_init(&full[s], kOp == kI8 ? 2 * S::kWiden : 1);
+      mbar_init(&full[s], kOp == kI8 ? S::kWiden : 1);
       mbar_init(&empty[s], 1);
       mbar_init(&raw[s], 1);
       mbar_init(&rempty[s], S::kWiden);
@@ -685,50 +685,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     }
   } else if constexpr (kOp == kI8) {
     // Widen: an octet of rows at a time, a lane a row and 16 codes -- in the 128-byte swizzle the eight
-    // lanes of a phase touch distinct banks on both sides.  A raw stage holds two K blocks.
-    const int w = warp - 6, r = lane & 7, cq = lane >> 3;
-    int slot = 0, rslot = 0;
-    uint32_t phase = 0, rphase = 0;
+    // lanes of a phase touch distinct banks on both sides.  A raw stage holds two K blocks; four warps
+    // take each, so that the latency of one block's widening runs under the other's.
+    constexpr int kTeam = S::kWiden / 2;
+    const int team = (warp - 6) / kTeam, w = (warp - 6) % kTeam, r = lane & 7, cq = lane >> 3;
+    int block = 0, rblock = 0;   // K blocks and raw stages before this job
     bool ok = true;
     while (ok && walk.next(j)) {
       const int half = ((j.n + 31) / 32 * 32) / 2;
       const int octets = 16 + half / 8;   // of the weight's 128 rows, then of the token rows
-      for (int kit = 0; kit < j.kits; ++kit) {
-        if ((kit & 1) == 0) ok = mbar_wait(&raw[rslot], rphase, limit, abort_flag);
-        ok = ok && mbar_wait(&empty[slot], phase ^ 1, limit, abort_flag);
+      const int kits = j.kits, rkits = (kits + 1) / 2;
+      for (int rk = 0; rk < rkits; ++rk) {
+        const int rs = (rblock + rk) % kRaw, kit = 2 * rk + team;
+        const int at = block + kit, slot = at % kStages;
+        // (a team without a block in this raw stage waits for it too, so that its release of the stage
+        // counts towards this fill)
+        ok = mbar_wait(&raw[rs], (uint32_t)((rblock + rk) / kRaw) & 1u, limit, abort_flag) &&
+             (kit >= kits || mbar_wait(&empty[slot], ((uint32_t)(at / kStages) & 1u) ^ 1u, limit, abort_flag));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           if (lane == 0) fail(kSiteGroupedStage);
           break;
         }
-        const uint8_t* src = raws + (size_t)rslot * kStage;
-        uint8_t* dst = stages + (size_t)slot * kStage;
-        const int c = (kit & 1) * 4 + cq;
-#pragma unroll 4
-        for (int o = w; o < octets; o += S::kWiden) {
-          // the weight's octets fill the first half of both stages, the rows' the second
-          const uint32_t at = (uint32_t)(o * 8 + r) * 128u;
-          uint4 lo, hi;
-          widen(*reinterpret_cast<const uint4*>(src + at + ((c ^ r) << 4)), lo, hi);
-          *reinterpret_cast<uint4*>(dst + at + (((2 * cq) ^ r) << 4)) = lo;
-          *reinterpret_cast<uint4*>(dst + at + (((2 * cq + 1) ^ r) << 4)) = hi;
+        if (kit < kits) {
+          const uint8_t* src = raws + (size_t)rs * kStage + r * 128 + (((team * 4 + cq) ^ r) << 4);
+          uint8_t* dst = stages + (size_t)slot * kStage + r * 128;
+#pragma unroll 1
+          for (int o = w; o < octets; o += 4 * kTeam) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (o + i * kTeam < octets) v[i] = *reinterpret_cast<const uint4*>(src + (o + i * kTeam) * 1024);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (o + i * kTeam >= octets) break;
+              uint4 lo, hi;
+              widen(v[i], lo, hi);
+              uint8_t* d = dst + (o + i * kTeam) * 1024;
+              *reinterpret_cast<uint4*>(d + (((2 * cq) ^ r) << 4)) = lo;
+              *reinterpret_cast<uint4*>(d + (((2 * cq + 1) ^ r) << 4)) = hi;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[slot], 0));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        const bool last = (kit & 1) != 0 || kit == j.kits - 1;
-        if (lane == 0) {
-          mbar_arrive_cluster(cluster_addr(&full[slot], 0));
-          if (last) mbar_arrive(&rempty[rslot]);
-        }
-        if (++slot == kStages) {
-          slot = 0;
-          phase ^= 1;
-        }
-        if (last && ++rslot == kRaw) {
-          rslot = 0;
-          rphase ^= 1;
-        }
+        if (lane == 0) mbar_arrive(&rempty[rs]);
       }
+      block += kits;
+      rblock += rkits;
     }
   }
   tc_fence_before();
