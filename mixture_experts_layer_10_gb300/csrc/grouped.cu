@@ -10,7 +10,8 @@
 //   warp 0      TMA producer: operand tiles into a ring of shared-memory stages (64 deep in K)
 //   warp 1      MMA issuer (the even CTA's one thread)
 //   warps 2-5   epilogue: tcgen05.ld of the accumulator, scales, rounding, stores
-//   warps 6..   8-bit integers: eight warps that widen the codes to fp16 (below);
+//   warps 6..   8-bit integers: twelve warps that fetch the codes and widen them to fp16 (below), in the
+//               producer's place;
 //               weight gradient: one warp that clears the rows past the end of a group
 //
 // Rows times a weight.  The weight's 256 features are the M side of the tile and up to 256 rows of one
@@ -29,8 +30,9 @@
 //
 // 8-bit integers.  sm_103a has no integer product at tensor rates, but every code is exact in fp16 and a
 // product of two in fp32, so fp16 tensor products of widened codes are the integer products, and their
-// fp32 sums are exact up to 2^24.  Codes travel as bytes; eight warps widen them between the ring that
-// TMA fills and the ring that the tensor cores read.
+// fp32 sums are exact up to 2^24.  Codes travel as bytes as far as the registers of the warps that widen
+// them into the stages.  (A ring of raw stages that TMA fills, read and widened from there, took the
+// room of half the stages and a third more shared-memory traffic: PERF_I8.)
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -119,13 +121,15 @@ constexpr uint32_t kEpiBox = 32 * 64;        // a staging box: 32 rows of 64 byt
 
 template <int kOp>
 struct Shape {
-  static constexpr int kStages = kOp == kI8 ? 4 : 6;       // 16-bit K blocks
-  static constexpr int kRaw = kOp == kI8 ? 2 : 0;          // 8-bit blocks, 128 codes deep
-  static constexpr int kWiden = 8;                         // warps that widen codes
-  static constexpr int kExtra = kOp == kI8 ? kWiden : (kOp == kDw ? 1 : 0);
+  static constexpr int kDepth = kOp == kI8 ? 2 * kBK : kBK;   // K of a stage
+  static constexpr int kStages = kOp == kI8 ? 3 : 6;
+  static constexpr int kRing = kOp == kDw ? 5 : kStages;      // weight gradient: the last stage is set apart
+  static constexpr uint32_t kStageBytes = 2 * kHalf * (kDepth / kBK);
+  static constexpr int kTeams = 2, kTeam = 8;   // 8-bit integers: teams of warps that widen codes
+  static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : (kOp == kDw ? 1 : 0);
   static constexpr int kThreads = 32 * (6 + kExtra);
   static constexpr uint32_t kEpi = kOp == kDw ? 4 * 2 * kEpiBox : 0;
-  static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kEpi + 512 + sizeof(GroupTab);
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kEpi + 512 + sizeof(GroupTab);
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
@@ -135,8 +139,9 @@ struct Params {
   CUtensorMap out;            // weight gradient: dW in boxes
   const int32_t *begin, *end;
   void* y;
-  const float *qs, *ws;       // scales of the rows and of the output channels (8-bit integers)
-  int64_t rows, ldy;
+  const int8_t *q, *wq;       // 8-bit integers: codes of the rows (ldq apart) and of the weights, and
+  const float *qs, *ws;       // the scales of the rows and of the output channels
+  int64_t rows, ldy, ldq;
   int depth;                  // contraction length (rows times a weight)
   int width;                  // features of the output row; weight gradient: columns of dW (n_in)
   int M;                      // weight gradient: rows of dW (n_out)
@@ -200,14 +205,14 @@ __device__ __forceinline__ Job dw_job(const Params& p, const GroupTab& s, int t,
 // The rows' box for a half of n rows: 0 (128 rows), 1 (64) or 2 (32).
 __device__ __forceinline__ int box_of(int half) { return half > 64 ? 0 : (half > 32 ? 1 : 2); }
 
-// 16 codes (four words) to 16 fp16 values: a code with its sign bit flipped is u = code + 128, the fp16
-// number with that byte under 0x64 is 1024 + u, and 1152 less is the code, exactly.
-__device__ __forceinline__ void widen(const uint4& v, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[8];
+// Eight codes (two words) to eight fp16 values: a code with its sign bit flipped is u = code + 128, the
+// fp16 number with that byte under 0x64 is 1024 + u, and 1152 less is the code, exactly.
+__device__ __forceinline__ uint4 widen(uint32_t w0, uint32_t w1) {
+  const uint32_t w[2] = {w0, w1};
+  uint32_t o[4];
   const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const uint32_t u = w[i] ^ 0x80808080u;
     const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
     const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
@@ -215,9 +220,11 @@ __device__ __forceinline__ void widen(const uint4& v, uint4& lo, uint4& hi) {
     o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
     o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
+
+// Whether the run's last K block takes the stage set apart (below).
+__device__ __forceinline__ bool early_last(const Job& j) { return j.tail % 16 != 0 && j.kits >= 4; }
 
 // One pair's walk over its tiles, the same in every role of both CTAs: rows times a weight has one job a
 // tile, the weight gradient one a run of rows.
@@ -232,7 +239,7 @@ struct Walk {
     if (kOp != kDw) {
       if (t >= ntiles) return false;
       j = row_job(p, s, t);
-      j.kits = (p.depth + kBK - 1) / kBK;
+      j.kits = (p.depth + Shape<kOp>::kDepth - 1) / Shape<kOp>::kDepth;
       t += step;
       return true;
     }
@@ -249,6 +256,13 @@ struct Walk {
     return true;
   }
 };
+
+// A store under a predicate rather than a branch, so that a run of them needs no reconvergence.
+__device__ __forceinline__ void store_if(uint16_t* at, uint32_t w, bool yes) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(at), "r"(w),
+               "r"((int)yes)
+               : "memory");
+}
 
 // ---- epilogues -----------------------------------------------------------------------------------
 
@@ -270,16 +284,23 @@ __device__ __forceinline__ void store_rows(const Params& p, const Job& j, int ra
     float qs = 0.f;
     if (kOp == kI8) qs = c + lane < j.n ? p.qs[j.row + c + lane] : 0.f;
     tmem_ld_wait();
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
+    for (int i = 0; i < 16; ++i) {
+      float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
       if (kOp == kI8) {
-        a = a * ws * __shfl_sync(0xffffffffu, qs, i);
-        b = b * ws * __shfl_sync(0xffffffffu, qs, i + 1);
+        a = a * ws * __shfl_sync(0xffffffffu, qs, 2 * i);
+        b = b * ws * __shfl_sync(0xffffffffu, qs, 2 * i + 1);
       }
       const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-      const uint32_t w = odd ? pack16(got, b, p.fp16) : pack16(a, got, p.fp16);
-      if (live && c + i + odd < j.n) *reinterpret_cast<uint32_t*>(out + (int64_t)(c + i) * p.ldy) = w;
+      w[i] = odd ? pack16(got, b, p.fp16) : pack16(a, got, p.fp16);
+    }
+    const int left = live ? j.n - c - odd : 0;   // this lane's rows from c on
+    uint16_t* at = out + (int64_t)c * p.ldy;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      store_if(at, w[i], 2 * i < left);
+      at += 2 * p.ldy;
     }
   }
 }
@@ -372,56 +393,70 @@ __device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
       : "memory");
 }
 
-// True once the phase with parity `parity` has completed; acquires at cluster scope, for barriers on
+// Bounded wait with naps of kNap ns between polls.  kCluster acquires at cluster scope: for barriers on
 // which the peer CTA's threads arrive after writing shared memory.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
-                                                  volatile int* abort) {
-  const uint64_t t0 = global_ns();
+template <bool kCluster>
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  if (!kCluster) return mbar_try_wait(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+template <int kNap, bool kCluster = false>
+__device__ __forceinline__ bool wait_nap(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort) {
+  if (try_wait<kCluster>(bar, parity)) return true;
+  uint64_t t0 = 0;
   while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
-      uint32_t ok;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity)
-          : "memory");
-      if (ok) return true;
+    for (int i = 0; i < 64; ++i) {
+      if (kNap > 0) __nanosleep(kNap);
+      if (try_wait<kCluster>(bar, parity)) return true;
     }
-    if (*abort || global_ns() - t0 > limit_ns) return false;
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (*abort || t - t0 > limit_ns) return false;
   }
 }
 
+// The same for a whole warp: lane 0 polls.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_nap<20>(bar, parity, limit_ns, abort);
+  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+}
+
 // Barriers (the same offsets in both CTAs; who uses which copy):
-//   full[s]     even CTA: the stage's operands of both CTAs are in place (TMA bytes; 8-bit integers: the
-//               widening warps of both CTAs; a cleared K block: the clearing warps)
+//   full[s]     even CTA: the stage's operands of both CTAs are in place (TMA bytes; 8-bit integers, and
+//               a cleared K block: an arrival from each CTA)
 //   empty[s]    stage free: committed to the even CTA, whose producer forwards it to the odd one when it
 //               refills the stage (8-bit integers: committed to both, the widening warps wait)
 //   tfull[a]    each CTA: accumulator a is complete
 //   tempty[a]   even CTA: both CTAs' epilogues have read it
-//   raw[s]      own CTA: bytes of a raw stage (8-bit integers), or of a K block that needs clearing
-//   rempty[s]   8-bit integers, own CTA: the widening warps have read raw stage s
-//   peer[s]     weight gradient, even CTA: the odd CTA has cleared its share of stage s
+//   raw[s]      own CTA: bytes of a K block that needs clearing (weight gradient); codes widened to the
+//               stage (8-bit integers)
 // Every wait is bounded; whatever happens, both CTAs meet at the last cluster barrier before TMEM is
 // freed, with their own copies landed.
 template <int kOp>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads, 1)
     grouped_kernel(const __grid_constant__ Params p) {
   using S = Shape<kOp>;
-  constexpr int kStages = S::kStages, kRaw = S::kRaw;
-  constexpr uint32_t kStage = 2 * kHalf;
+  constexpr int kStages = S::kStages;
+  constexpr int kRing = S::kRing;
+  constexpr uint32_t kStage = S::kStageBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = smem;
-  uint8_t* raws = stages + kStages * kStage;
-  uint8_t* boxes = raws + kRaw * kStage;
+  uint8_t* boxes = stages + kStages * kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(boxes + S::kEpi);
   uint64_t* empty = full + 6;
   uint64_t* raw = empty + 6;
-  uint64_t* rempty = raw + 6;
-  uint64_t* peer = rempty + 6;
-  uint64_t* tfull = peer + 6;
+  uint64_t* tfull = raw + 6;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -433,11 +468,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
-      mbar_init(&full[s], kOp == kI8 ? S::kWiden : 1);
+      mbar_init(&full[s], kOp == kI8 || kOp == kDw ? 2 : 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&raw[s], 1);
-      mbar_init(&rempty[s], S::kWiden);
-      mbar_init(&peer[s], 1);
+      mbar_init(&raw[s], kOp == kI8 ? S::kTeam : 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -446,8 +479,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch(&p.a);
-    for (int i = 0; i < (kOp == kDw ? 1 : kBoxes); ++i) tma_prefetch(&p.b[i]);
+    if (kOp != kI8) {
+      tma_prefetch(&p.a);
+      for (int i = 0; i < (kOp == kDw ? 1 : kBoxes); ++i) tma_prefetch(&p.b[i]);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
@@ -472,99 +507,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   if (warp == 0) {
     if (lane == 0) {
       int slot = 0, uses = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, phase_apart = 0;   // ring; the stage set apart
+      int uses_apart = 0;
       bool ok = true;
       // test hook: the first pair skips one fill, so that the wait for it runs out
       const int skip = pair == 0 ? *((volatile const int32_t*)&p.hdr->stall_fill_p1) - 1 : -1;
       uint32_t raw_used = 0, raw_next = 0;   // weight gradient, a bit per stage: own barrier used, next phase
       if constexpr (kOp == kI8) {
-        while (ok && !*abort_flag && walk.next(j)) {
-          const int half = ((j.n + 31) / 32 * 32) / 2, bx = box_of(half);
-          const uint32_t bytes = kHalf + (128u >> bx) * 128u;
-          const int kits = (p.depth + 127) / 128;
-          for (int kit = 0; kit < kits; ++kit) {
-            if (!mbar_wait(&rempty[slot], phase ^ 1, limit, abort_flag)) {
+        // tells the even CTA's MMA thread of every widened stage: one thread with nothing else in flight,
+        // because a release at cluster scope waits for all of a thread's memory operations
+        while (ok && walk.next(j)) {
+          for (int kit = 0; kit < j.kits; ++kit) {
+            if (!wait_nap<20>(&raw[slot], phase, limit, abort_flag)) {
               fail(kSiteGroupedProducer);
               ok = false;
               break;
             }
-            if (uses != skip) {
-              uint8_t* st = raws + (size_t)slot * kStage;
-              mbar_arrive_expect_tx(&raw[slot], bytes);
-              tma_load_3d(st, &p.a, &raw[slot], kit * 128, j.f0 + kBM * rank, j.g);
-              tma_load_2d(st + kHalf, &p.b[bx], &raw[slot], kit * 128, j.row + half * rank);
-            }
-            ++uses;
-            if (++slot == kRaw) {
+            mbar_arrive_cluster(cluster_addr(&full[slot], 0));
+            if (++slot == kRing) {
               slot = 0;
               phase ^= 1;
             }
           }
         }
-        drain_fills(raw, kRaw, slot, phase, uses, limit);
       } else {
         while (ok && !*abort_flag && walk.next(j)) {
           const int half = ((j.n + 31) / 32 * 32) / 2, bx = kOp == kDw ? 0 : box_of(half);
           const uint32_t bytes = kHalf + (kOp == kDw ? kHalf : (128u >> bx) * 128u);
-          for (int kit = 0; kit < j.kits; ++kit) {
-            if (!mbar_wait(&empty[slot], phase ^ 1, limit, abort_flag)) {
+          // K block kit to stage s, which is free
+          auto fill = [&](int kit, int s) {
+            uint8_t* st = stages + (size_t)s * kStage;
+            if constexpr (kOp == kDw) {
+              // a K block that needs clearing lands on this CTA's own barrier, for its clearing warp
+              const bool clear = j.tail % 16 != 0 && kit == j.kits - 1;
+              uint32_t bar = cluster_addr(&full[s], 0);
+              if (clear) {
+                mbar_arrive_expect_tx(&raw[s], bytes);
+                bar = cluster_addr(&raw[s], (uint32_t)rank);
+                raw_used |= 1u << s;
+                raw_next ^= 1u << s;
+              } else if (rank == 0) {
+                mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                mbar_arrive(&full[s]);
+              }
+              const int row = j.row + kit * kBK, ca = j.m0 + kBM * rank, cb = j.f0 + kBM * rank;
+              if (p.wide_a) {
+                tma_load_3d_pair(st, &p.a, bar, 0, row, ca / 64);
+              } else {
+                tma_load_2d_pair(st, &p.a, bar, ca, row);
+                tma_load_2d_pair(st + kBox, &p.a, bar, ca + 64, row);
+              }
+              if (p.wide_b) {
+                tma_load_3d_pair(st + kHalf, &p.b[0], bar, 0, row, cb / 64);
+              } else {
+                tma_load_2d_pair(st + kHalf, &p.b[0], bar, cb, row);
+                tma_load_2d_pair(st + kHalf + kBox, &p.b[0], bar, cb + 64, row);
+              }
+            } else {
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+              const uint32_t bar = cluster_addr(&full[s], 0);
+              const int f = j.f0 + kBM * rank;
+              if (kOp == kMm) {
+                tma_load_3d_pair(st, &p.a, bar, kit * kBK, f, j.g);
+              } else if (p.wide_a) {
+                tma_load_4d_pair(st, &p.a, bar, 0, kit * kBK, f / 64, j.g);
+              } else {
+                tma_load_3d_pair(st, &p.a, bar, f, kit * kBK, j.g);
+                tma_load_3d_pair(st + kBox, &p.a, bar, f + 64, kit * kBK, j.g);
+              }
+              tma_load_2d_pair(st + kHalf, &p.b[bx], bar, kit * kBK, j.row + half * rank);
+            }
+          };
+          const bool apart = kOp == kDw && early_last(j);
+          auto fill_apart = [&] {
+            fill(j.kits - 1, kRing);
+            if (rank == 0 && uses_apart > 0) mbar_arrive_cluster_relaxed(cluster_addr(&empty[kRing], 1));
+            ++uses_apart;
+            phase_apart ^= 1;
+          };
+          bool pending = apart;
+          for (int kit = 0; kit < j.kits - (int)apart; ++kit) {
+            if (pending && mbar_try_wait(&empty[kRing], phase_apart ^ 1)) {
+              fill_apart();
+              pending = false;
+            }
+            if (!wait_nap<20>(&empty[slot], phase ^ 1, limit, abort_flag)) {
               fail(kSiteGroupedProducer);
               ok = false;
               break;
             }
-            if (uses != skip) {
-              uint8_t* st = stages + (size_t)slot * kStage;
-              if constexpr (kOp == kDw) {
-                // a K block that needs clearing lands on this CTA's own barrier, for its clearing warp
-                const bool clear = j.tail != 0 && kit == j.kits - 1;
-                uint32_t bar = cluster_addr(&full[slot], 0);
-                if (clear) {
-                  mbar_arrive_expect_tx(&raw[slot], bytes);
-                  bar = cluster_addr(&raw[slot], (uint32_t)rank);
-                  raw_used |= 1u << slot;
-                  raw_next ^= 1u << slot;
-                } else if (rank == 0) {
-                  mbar_arrive_expect_tx(&full[slot], 2 * bytes);
-                }
-                const int row = j.row + kit * kBK, ca = j.m0 + kBM * rank, cb = j.f0 + kBM * rank;
-                if (p.wide_a) {
-                  tma_load_3d_pair(st, &p.a, bar, 0, row, ca / 64);
-                } else {
-                  tma_load_2d_pair(st, &p.a, bar, ca, row);
-                  tma_load_2d_pair(st + kBox, &p.a, bar, ca + 64, row);
-                }
-                if (p.wide_b) {
-                  tma_load_3d_pair(st + kHalf, &p.b[0], bar, 0, row, cb / 64);
-                } else {
-                  tma_load_2d_pair(st + kHalf, &p.b[0], bar, cb, row);
-                  tma_load_2d_pair(st + kHalf + kBox, &p.b[0], bar, cb + 64, row);
-                }
-              } else {
-                if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * bytes);
-                const uint32_t bar = cluster_addr(&full[slot], 0);
-                const int f = j.f0 + kBM * rank;
-                if (kOp == kMm) {
-                  tma_load_3d_pair(st, &p.a, bar, kit * kBK, f, j.g);
-                } else if (p.wide_a) {
-                  tma_load_4d_pair(st, &p.a, bar, 0, kit * kBK, f / 64, j.g);
-                } else {
-                  tma_load_3d_pair(st, &p.a, bar, f, kit * kBK, j.g);
-                  tma_load_3d_pair(st + kBox, &p.a, bar, f + 64, kit * kBK, j.g);
-                }
-                tma_load_2d_pair(st + kHalf, &p.b[bx], bar, kit * kBK, j.row + half * rank);
-              }
-            }
-            if (rank == 0 && uses >= kStages) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 1));
+            if (uses != skip) fill(kit, slot);
+            if (rank == 0 && uses >= kRing) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 1));
             ++uses;
-            if (++slot == kStages) {
+            if (++slot == kRing) {
               slot = 0;
               phase ^= 1;
             }
           }
+          if (ok && pending) {
+            ok = wait_nap<20>(&empty[kRing], phase_apart ^ 1, limit, abort_flag);
+            if (ok) fill_apart();
+            else fail(kSiteGroupedProducer);
+          }
         }
         // every load of the pair lands before either CTA's shared memory is released: the even CTA's
         // full barriers complete after both CTAs' bytes, and the odd CTA waits at the cluster barrier
-        if (rank == 0) drain_fills(full, kStages, slot, phase, uses, limit);
+        if (rank == 0) {
+          drain_fills(full, kRing, slot, phase, uses, limit);
+          if (uses_apart > 0) mbar_wait_drain(&full[kRing], phase_apart ^ 1, limit);
+        }
         for (int s = 0; s < kStages; ++s)
           if ((raw_used >> s) & 1) mbar_wait_drain(&raw[s], ((raw_next >> s) & 1) ^ 1u, limit);
       }
@@ -572,39 +623,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       int slot = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t phase = 0, acc_phase = 0, phase_apart = 0;
       bool ok = true, more = walk.next(j);
       while (ok && more && !*abort_flag) {
         const int kits = j.kits;
+        const bool apart = kOp == kDw && early_last(j);
+        // steps of 16 in the last K block: the rest of it holds no rows of the group (weight gradient), or
+        // no codes (8-bit integers: the depth is a multiple of 16)
+        int last = S::kDepth / 16;
+        if (kOp == kDw && j.tail != 0) last = (j.tail + 15) / 16;
+        if (kOp == kI8) last = p.depth / 16 - (kits - 1) * (S::kDepth / 16);
         const int n = kOp == kDw ? kTile : (j.n + 31) / 32 * 32;
         const uint32_t idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(n >> 3) << 17);
         more = walk.next(j);   // the next job, worked out while this one's products run
         if (kits == 0) continue;
         const uint32_t dt = tmem_base + (uint32_t)(acc * kTile);
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1, limit, abort_flag)) {
+        if (!wait_nap<20>(&tempty[acc], acc_phase ^ 1, limit, abort_flag)) {
           fail(kSiteGroupedMma);
           break;
         }
         tc_fence_after();
         for (int kit = 0; kit < kits; ++kit) {
-          const bool there = kOp == kI8 || kOp == kDw ? mbar_wait_cluster(&full[slot], phase, limit, abort_flag)
-                                                      : mbar_wait(&full[slot], phase, limit, abort_flag);
-          if (!there) {
+          const bool set_apart = apart && kit == kits - 1;
+          const int s = set_apart ? kRing : slot;
+          if (!wait_nap<20, kOp == kI8 || kOp == kDw>(&full[s], set_apart ? phase_apart : phase, limit, abort_flag)) {
             fail(kSiteGroupedMma);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(stages + (size_t)slot * kStage);
+          const uint32_t sa = smem_u32(stages + (size_t)s * kStage);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            const uint64_t da = kOp == kMm || kOp == kI8 ? sdesc_kmajor(sa + kk * 32) : sdesc_mnmajor(sa + kk * 2048, kBox);
-            const uint64_t db = kOp == kDw ? sdesc_mnmajor(sa + kHalf + kk * 2048, kBox) : sdesc_kmajor(sa + kHalf + kk * 32);
+          for (int kk = 0; kk < S::kDepth / 16; ++kk) {
+            if ((kOp == kDw || kOp == kI8) && kit == kits - 1 && kk >= last) break;
+            const uint32_t at = sa + (kk / 4) * 2 * kHalf;   // (8-bit integers: two blocks of 64)
+            const uint64_t da = kOp == kMm || kOp == kI8 ? sdesc_kmajor(at + kk % 4 * 32) : sdesc_mnmajor(at + kk * 2048, kBox);
+            const uint64_t db = kOp == kDw ? sdesc_mnmajor(at + kHalf + kk * 2048, kBox) : sdesc_kmajor(at + kHalf + kk % 4 * 32);
             umma_bf16_pair(dt, da, db, idesc, (kit | kk) != 0);
           }
-          if (kOp == kI8) umma_commit_both(&empty[slot]);
-          else umma_commit_pair(smem_u32(&empty[slot]));
-          if (++slot == kStages) {
+          if (kOp == kI8) umma_commit_both(&empty[s]);
+          else umma_commit_pair(smem_u32(&empty[s]));
+          if (set_apart) {
+            phase_apart ^= 1;
+          } else if (++slot == kRing) {
             slot = 0;
             phase ^= 1;
           }
@@ -648,92 +709,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     }
     if (kOp == kDw && lane == 0) bulk_wait_all();   // this warp's output stores have landed
   } else if constexpr (kOp == kDw) {
-    // the rows past the end of the group in its last K block, in both operands' boxes of this CTA
+    // the rows past the end of the group in its last step of 16 rows, in both operands' boxes of this CTA
     int slot = 0;
-    uint32_t raw_phase = 0, peer_phase = 0;   // a bit per stage: only cleared blocks use these barriers
+    uint32_t raw_phase = 0;   // a bit per stage: only cleared blocks use these barriers
     bool ok = true;
     while (ok && walk.next(j)) {
-      if (j.tail != 0) {
-        const int s = (slot + j.kits - 1) % kStages;
-        if (!mbar_wait(&raw[s], (raw_phase >> s) & 1, limit, abort_flag)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
+      const int from = j.tail, to = (j.tail + 15) / 16 * 16;
+      if (from != to) {
+        const int s = early_last(j) ? kRing : (slot + j.kits - 1) % kRing;
+        ok = wait_warp(&raw[s], (raw_phase >> s) & 1, limit, abort_flag);
         if (!ok) {
           if (lane == 0) fail(kSiteGroupedStage);
           break;
         }
         raw_phase ^= 1u << s;
-        uint8_t* st = stages + (size_t)s * kStage;
-#pragma unroll 1
-        for (int box = 0; box < 4; ++box)
-          for (int o = j.tail * 128 + lane * 16; o < (int)kBox; o += 32 * 16)
-            *reinterpret_cast<uint4*>(st + box * kBox + o) = make_uint4(0, 0, 0, 0);
+        uint8_t* at = stages + (size_t)s * kStage + (lane >> 3) * kBox + (lane & 7) * 16;   // eight lanes a box
+        for (int r = from; r < to; ++r) *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (rank == 1) {
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(&peer[s], 0));
-        } else {
-          if (lane == 0) {
-            ok = mbar_wait_cluster(&peer[s], (peer_phase >> s) & 1, limit, abort_flag);
-            if (ok) mbar_arrive_cluster(cluster_addr(&full[s], 0));
-            else fail(kSiteGroupedStage);
-          }
-          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-          peer_phase ^= 1u << s;
-        }
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[s], 0));
       }
-      slot = (slot + j.kits) % kStages;
+      slot = (slot + j.kits - (int)early_last(j)) % kRing;
     }
   } else if constexpr (kOp == kI8) {
-    // Widen: an octet of rows at a time, a lane a row and 16 codes -- in the 128-byte swizzle the eight
-    // lanes of a phase touch distinct banks on both sides.  A raw stage holds two K blocks; four warps
-    // take each, so that the latency of one block's widening runs under the other's.
-    constexpr int kTeam = S::kWiden / 2;
-    const int team = (warp - 6) / kTeam, w = (warp - 6) % kTeam, r = lane & 7, cq = lane >> 3;
-    int block = 0, rblock = 0;   // K blocks and raw stages before this job
+    // Widen: the teams take turns at the stages, 128 codes deep; a warp takes every eighth four rows (of
+    // the weight's 128, then of up to 128 token rows), a lane 16 codes of a row: an instruction reads
+    // whole 128-byte lines of four rows.  A lane's codes belong to one of the stage's two 64-deep
+    // blocks; the lanes of the second block store their halves in the other order, which with the
+    // 128-byte swizzle keeps the banks of each eight lanes distinct.  Rows past the last are read as the
+    // last one: nothing stores their products.
+    constexpr int kRows = 4;   // rows an instruction reads
+    constexpr int kPer = kBM / kRows / S::kTeam;
+    const int team = (warp - 6) / S::kTeam, w = (warp - 6) % S::kTeam;
+    const int r0 = w * kRows + (lane >> 3), second = (lane >> 2) & 1, cq = lane & 3;
+    const int skip = pair == 0 ? *((volatile const int32_t*)&p.hdr->stall_fill_p1) - 1 : -1;
+    uint8_t* const dst = stages + second * 2 * kHalf + r0 * 128;
+    const int o0 = ((2 * cq + second) ^ (r0 & 7)) << 4, o1 = ((2 * cq + 1 - second) ^ (r0 & 7)) << 4;
+    int fill = 0;
     bool ok = true;
     while (ok && walk.next(j)) {
       const int half = ((j.n + 31) / 32 * 32) / 2;
-      const int octets = 16 + half / 8;   // of the weight's 128 rows, then of the token rows
-      const int kits = j.kits, rkits = (kits + 1) / 2;
-      for (int rk = 0; rk < rkits; ++rk) {
-        const int rs = (rblock + rk) % kRaw, kit = 2 * rk + team;
-        const int at = block + kit, slot = at % kStages;
-        // (a team without a block in this raw stage waits for it too, so that its release of the stage
-        // counts towards this fill)
-        ok = mbar_wait(&raw[rs], (uint32_t)((rblock + rk) / kRaw) & 1u, limit, abort_flag) &&
-             (kit >= kits || mbar_wait(&empty[slot], ((uint32_t)(at / kStages) & 1u) ^ 1u, limit, abort_flag));
-        ok = __all_sync(0xffffffffu, ok);
+      const int f = j.f0 + kBM * rank + r0, row = j.row + half * rank + r0;
+      const int8_t* wq = p.wq + (int64_t)j.g * p.width * p.depth;
+      for (int kit = 0; kit < j.kits; ++kit, ++fill) {
+        if (fill % S::kTeams != team) continue;
+        const int k = min(kit * S::kDepth + (lane & 7) * 16, p.depth - 16);
+        uint4 a[kPer], b[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          a[i] = __ldg(reinterpret_cast<const uint4*>(wq + (int64_t)min(f + i * kRows * S::kTeam, p.width - 1) * p.depth + k));
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if ((i * S::kTeam + w) * kRows < half)
+            b[i] = __ldg(reinterpret_cast<const uint4*>(
+                p.q + min((int64_t)row + i * kRows * S::kTeam, p.rows - 1) * p.ldq + k));
+        const int slot = fill % kRing;
+        ok = __all_sync(0xffffffffu, wait_nap<0>(&empty[slot], ((uint32_t)(fill / kRing) & 1u) ^ 1u, limit, abort_flag));
         if (!ok) {
           if (lane == 0) fail(kSiteGroupedStage);
           break;
         }
-        if (kit < kits) {
-          const uint8_t* src = raws + (size_t)rs * kStage + r * 128 + (((team * 4 + cq) ^ r) << 4);
-          uint8_t* dst = stages + (size_t)slot * kStage + r * 128;
-#pragma unroll 1
-          for (int o = w; o < octets; o += 4 * kTeam) {
-            uint4 v[4];
+        uint8_t* st = dst + (size_t)slot * kStage;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (o + i * kTeam < octets) v[i] = *reinterpret_cast<const uint4*>(src + (o + i * kTeam) * 1024);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (o + i * kTeam >= octets) break;
-              uint4 lo, hi;
-              widen(v[i], lo, hi);
-              uint8_t* d = dst + (o + i * kTeam) * 1024;
-              *reinterpret_cast<uint4*>(d + (((2 * cq) ^ r) << 4)) = lo;
-              *reinterpret_cast<uint4*>(d + (((2 * cq + 1) ^ r) << 4)) = hi;
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[slot], 0));
+        for (int i = 0; i < 2 * kPer; ++i) {
+          if (i >= kPer && ((i - kPer) * S::kTeam + w) * kRows >= half) break;
+          const uint4 v = i < kPer ? a[i % kPer] : b[i % kPer];
+          uint8_t* d = st + (i < kPer ? 0 : kHalf) + (i % kPer) * kRows * S::kTeam * 128;
+          *reinterpret_cast<uint4*>(d + o0) = second ? widen(v.z, v.w) : widen(v.x, v.y);
+          *reinterpret_cast<uint4*>(d + o1) = second ? widen(v.x, v.y) : widen(v.z, v.w);
         }
-        if (lane == 0) mbar_arrive(&rempty[rs]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && fill != skip) mbar_arrive(&raw[slot]);
       }
-      block += kits;
-      rblock += rkits;
     }
   }
   tc_fence_before();
@@ -763,25 +811,24 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base
                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr CUtensorMapDataType k16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+constexpr CUtensorMapDataType k16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;   // (fp16 values too: bits are copied)
 constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B, kSw64 = CU_TENSOR_MAP_SWIZZLE_64B;
 
-// Rows [rows, width] as K-major boxes of 128 bytes x 128, 64 and 32 rows.
-bool map_rows(CUtensorMap* m, const void* base, bool codes, uint64_t rows, uint64_t width, uint64_t ld) {
-  const cuuint64_t dims[2] = {width, rows}, strides[1] = {ld * (codes ? 1 : 2)};
+// Rows [rows, width] as K-major boxes of 64 columns x 128, 64 and 32 rows.
+bool map_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t width, uint64_t ld) {
+  const cuuint64_t dims[2] = {width, rows}, strides[1] = {ld * 2};
   for (int i = 0; i < kBoxes; ++i) {
-    const cuuint32_t box[2] = {codes ? 128u : 64u, 128u >> i};
-    if (!encode(&m[i], codes ? k8 : k16, 2, base, dims, strides, box, kSw128)) return false;
+    const cuuint32_t box[2] = {64, 128u >> i};
+    if (!encode(&m[i], k16, 2, base, dims, strides, box, kSw128)) return false;
   }
   return true;
 }
 
-// Weights [G, N, K], K-major: boxes of 128 bytes x 128 rows.
-bool map_weight(CUtensorMap* m, const void* base, bool codes, uint64_t G, uint64_t N, uint64_t K) {
-  const uint64_t size = codes ? 1 : 2;
-  const cuuint64_t dims[3] = {K, N, G}, strides[2] = {K * size, K * N * size};
-  const cuuint32_t box[3] = {codes ? 128u : 64u, 128, 1};
-  return encode(m, codes ? k8 : k16, 3, base, dims, strides, box, kSw128);
+// Weights [G, N, K], K-major: boxes of 64 columns x 128 rows.
+bool map_weight(CUtensorMap* m, const void* base, uint64_t G, uint64_t N, uint64_t K) {
+  const cuuint64_t dims[3] = {K, N, G}, strides[2] = {K * 2, K * N * 2};
+  const cuuint32_t box[3] = {64, 128, 1};
+  return encode(m, k16, 3, base, dims, strides, box, kSw128);
 }
 
 // Weights [G, N, K] read MN-major (K contiguous): 64 x 64 boxes, two at a time when K allows (the columns
@@ -863,7 +910,7 @@ cudaError_t launch_grouped_mm(const Grouped& c, const int32_t* begin, const int3
                               const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s) {
   if (c.rows == 0) return cudaSuccess;
   Params p = params_of(c, begin, end, hdr);
-  if (!map_weight(&p.a, W, false, c.G, c.N, c.K) || !map_rows(p.b, x, false, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
+  if (!map_weight(&p.a, W, c.G, c.N, c.K) || !map_rows(p.b, x, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
   p.y = y;
   p.ldy = c.ldo;
   p.depth = c.K;
@@ -878,7 +925,7 @@ cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int3
   if (c.rows == 0) return cudaSuccess;
   Params p = params_of(c, begin, end, hdr);
   p.wide_a = c.K % 64 == 0;
-  if (!map_weight_mn(&p.a, W, c.G, c.N, c.K, p.wide_a) || !map_rows(p.b, dy, false, c.rows, c.N, c.ldo))
+  if (!map_weight_mn(&p.a, W, c.G, c.N, c.K, p.wide_a) || !map_rows(p.b, dy, c.rows, c.N, c.ldo))
     return cudaErrorInvalidValue;
   p.y = dx;
   p.ldy = c.ldi;
@@ -916,9 +963,11 @@ cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int3
                               cudaStream_t s) {
   if (c.rows == 0) return cudaSuccess;
   Params p = params_of(c, begin, end, hdr);
-  if (!map_weight(&p.a, Wq, true, c.G, c.N, c.K) || !map_rows(p.b, q, true, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
   p.y = y;
   p.ldy = c.ldo;
+  p.q = q;
+  p.wq = Wq;
+  p.ldq = c.ldi;
   p.qs = qs;
   p.ws = Ws;
   p.depth = c.K;
