@@ -348,6 +348,12 @@ cudaError_t launch_grouped_dw(const Grouped& c, const int32_t* begin, const int3
 cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,
                               const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr,
                               cudaStream_t s);
+// The same for few rows a group (grouped_stream.cu): y = x W[g]^T, or with 8-bit integers.
+bool stream_eligible(const Grouped& c);
+cudaError_t launch_stream_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
+                             const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s);
+cudaError_t launch_stream_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,
+                             const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr, cudaStream_t s);
 cudaError_t launch_segments(const Tables* tabs, int G, int32_t* begin, int32_t* end, cudaStream_t s);
 // 8-bit integer rows: codes [rows, cols] and one fp32 scale per row (amax / 127)
 cudaError_t launch_quantize_rows_i8(const uint16_t* src, bool fp16, int64_t rows, int cols, int8_t* codes,

@@ -35,76 +35,14 @@
 // room of half the stages and a third more shared-memory traffic: PERF_I8.)
 #include <algorithm>
 
-#include <cuda_fp16.h>
-
 #include "common.cuh"
+#include "grouped.cuh"
 #include "ptx.cuh"
 #include "tmap.cuh"
 
 namespace moe {
 
 namespace {
-
-// The groups and the exclusive sum of their row tiles.
-struct GroupTab {
-  int begin[kMaxGroups];
-  int end[kMaxGroups];
-  int first[kMaxGroups + 1];   // first tile of every group
-  int part[32];
-};
-
-// Whole block: read the groups, check them, and number the row tiles of `tile` rows.  Returns the
-// number of row tiles, or -1 (recorded in the error word by block 0) when the groups are out of range
-// or out of order; every block reads the same values and answers the same.
-__device__ int load_groups(GroupTab& t, const int32_t* begin, const int32_t* end, int G, int64_t rows, int tile,
-                           Hdr* hdr) {
-  const int n = blockDim.x, per = (G + n - 1) / n;
-  const int g0 = min(G, (int)threadIdx.x * per), g1 = min(G, g0 + per);
-  bool bad = false;
-  int sum = 0;
-  for (int g = g0; g < g1; ++g) {
-    const int b = begin[g], e = end[g];
-    const int prev = g == 0 ? 0 : end[g - 1];
-    bad |= b < prev || e < b || (int64_t)e > rows;
-    t.begin[g] = b;
-    t.end[g] = e;
-    sum += bad ? 0 : (e - b) / tile + ((e - b) % tile != 0);
-  }
-  if (__syncthreads_or(bad)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(hdr, MOE_ERR_BAD_INDEX, kSiteGroups);
-    return -1;
-  }
-  // exclusive sum over the threads
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) t.part[warp] = inc;
-  __syncthreads();
-  int at = inc - sum;
-  for (int w = 0; w < warp; ++w) at += t.part[w];
-  for (int g = g0; g < g1; ++g) {
-    t.first[g] = at;
-    const int len = t.end[g] - t.begin[g];
-    at += len / tile + (len % tile != 0);
-  }
-  if (threadIdx.x == 0) {
-    int total = 0;
-    for (int w = 0; w < n / 32; ++w) total += t.part[w];
-    t.first[G] = total;
-  }
-  __syncthreads();
-  return t.first[G];
-}
-
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
-  if (!fp16) return pack_bf16(lo, hi);
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 enum Op { kMm, kDx, kDw, kI8 };
 
@@ -204,24 +142,6 @@ __device__ __forceinline__ Job dw_job(const Params& p, const GroupTab& s, int t,
 
 // The rows' box for a half of n rows: 0 (128 rows), 1 (64) or 2 (32).
 __device__ __forceinline__ int box_of(int half) { return half > 64 ? 0 : (half > 32 ? 1 : 2); }
-
-// Eight codes (two words) to eight fp16 values: a code with its sign bit flipped is u = code + 128, the
-// fp16 number with that byte under 0x64 is 1024 + u, and 1152 less is the code, exactly.
-__device__ __forceinline__ uint4 widen(uint32_t w0, uint32_t w1) {
-  const uint32_t w[2] = {w0, w1};
-  uint32_t o[4];
-  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t u = w[i] ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-    o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
-    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
 
 // Whether the run's last K block takes the stage set apart (below).
 __device__ __forceinline__ bool early_last(const Job& j) { return j.tail % 16 != 0 && j.kits >= 4; }
@@ -909,6 +829,7 @@ int64_t most_row_tiles(const Grouped& c) { return c.rows / kTile + std::min<int6
 cudaError_t launch_grouped_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
                               const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s) {
   if (c.rows == 0) return cudaSuccess;
+  if (stream_eligible(c)) return launch_stream_mm(c, begin, end, x, W, y, hdr, s);
   Params p = params_of(c, begin, end, hdr);
   if (!map_weight(&p.a, W, c.G, c.N, c.K) || !map_rows(p.b, x, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
   p.y = y;
@@ -962,6 +883,7 @@ cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int3
                               const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr,
                               cudaStream_t s) {
   if (c.rows == 0) return cudaSuccess;
+  if (stream_eligible(c)) return launch_stream_i8(c, begin, end, q, qs, Wq, Ws, y, hdr, s);
   Params p = params_of(c, begin, end, hdr);
   p.y = y;
   p.ldy = c.ldo;

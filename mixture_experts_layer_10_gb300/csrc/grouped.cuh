@@ -1,0 +1,89 @@
+// What the kernels of the grouped products share: the table of the groups and the 16-bit roundings.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+// The groups and the exclusive sum of their row tiles.
+struct GroupTab {
+  int begin[kMaxGroups];
+  int end[kMaxGroups];
+  int first[kMaxGroups + 1];   // first tile of every group
+  int part[32];
+};
+
+// Whole block: read the groups, check them, and number the row tiles of `tile` rows.  Returns the
+// number of row tiles, or -1 (recorded in the error word by block 0) when the groups are out of range
+// or out of order; every block reads the same values and answers the same.
+__device__ __forceinline__ int load_groups(GroupTab& t, const int32_t* begin, const int32_t* end, int G, int64_t rows, int tile,
+                           Hdr* hdr) {
+  const int n = blockDim.x, per = (G + n - 1) / n;
+  const int g0 = min(G, (int)threadIdx.x * per), g1 = min(G, g0 + per);
+  bool bad = false;
+  int sum = 0;
+  for (int g = g0; g < g1; ++g) {
+    const int b = begin[g], e = end[g];
+    const int prev = g == 0 ? 0 : end[g - 1];
+    bad |= b < prev || e < b || (int64_t)e > rows;
+    t.begin[g] = b;
+    t.end[g] = e;
+    sum += bad ? 0 : (e - b) / tile + ((e - b) % tile != 0);
+  }
+  if (__syncthreads_or(bad)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(hdr, MOE_ERR_BAD_INDEX, kSiteGroups);
+    return -1;
+  }
+  // exclusive sum over the threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) t.part[warp] = inc;
+  __syncthreads();
+  int at = inc - sum;
+  for (int w = 0; w < warp; ++w) at += t.part[w];
+  for (int g = g0; g < g1; ++g) {
+    t.first[g] = at;
+    const int len = t.end[g] - t.begin[g];
+    at += len / tile + (len % tile != 0);
+  }
+  if (threadIdx.x == 0) {
+    int total = 0;
+    for (int w = 0; w < n / 32; ++w) total += t.part[w];
+    t.first[G] = total;
+  }
+  __syncthreads();
+  return t.first[G];
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
+  if (!fp16) return pack_bf16(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight codes (two words) to eight fp16 values: a code with its sign bit flipped is u = code + 128, the
+// fp16 number with that byte under 0x64 is 1024 + u, and 1152 less is the code, exactly.
+__device__ __forceinline__ uint4 widen(uint32_t w0, uint32_t w1) {
+  const uint32_t w[2] = {w0, w1};
+  uint32_t o[4];
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = w[i] ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+}  // namespace moe
