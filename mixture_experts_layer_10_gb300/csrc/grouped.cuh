@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -84,6 +85,37 @@ __device__ __forceinline__ uint4 widen(uint32_t w0, uint32_t w1) {
     o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Bounded wait with naps of kNap ns between polls.  kCluster acquires at cluster scope: for barriers on
+// which the peer CTA's threads arrive after writing shared memory.
+template <bool kCluster>
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  if (!kCluster) return mbar_try_wait(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+template <int kNap, bool kCluster = false>
+__device__ __forceinline__ bool wait_nap(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort) {
+  if (try_wait<kCluster>(bar, parity)) return true;
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+      if (kNap > 0) __nanosleep(kNap);
+      if (try_wait<kCluster>(bar, parity)) return true;
+    }
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (*abort || t - t0 > limit_ns) return false;
+  }
 }
 
 }  // namespace moe
