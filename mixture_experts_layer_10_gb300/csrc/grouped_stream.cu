@@ -2,10 +2,12 @@
 // integers.  Such a product is one read of the weights of the groups that have rows, so the kernel is
 // built around that read.  A tile is 128 features of one group and up to 8 or 32 of its rows; one thread
 // of a block streams the tiles' W and x as TMA boxes, 128 bytes of every row, into a ring of stages,
-// across tile borders, and eight warps multiply 16 features each with mma.sync.  (Register fragments: at
-// a few rows a weight the tensor rate is not what counts, and 8-bit codes widen to fp16 on their way
-// from shared memory to the fragment.)  The order in which the products of a sum are taken is free, so
-// lane (r, c) of a fragment holds 16 consecutive bytes of rows r and r + 8, as one load delivers them.
+// across tile borders, and eight warps multiply with mma.sync: two teams of four, 32 features a warp and
+// every other 16 bytes of a row a team.  (Register fragments: at a few rows a weight the tensor rate is not what counts, and 8-bit
+// codes widen to fp16 on their way from shared memory to the fragment.  32 features a warp halve the
+// codes of x that are widened more than once.)  The order in which the products of a sum are taken is
+// free, so lane (r, c) of a fragment holds 16 consecutive bytes of rows r and r + 8, as one load delivers
+// them.  The teams' sums meet in shared memory.
 //
 // Where the tiles are fewer than the blocks that fit (one token's 8 experts x 768 features are 48), a
 // cluster of 2, 4 or 8 blocks splits the contraction of a tile, and each block adds up its share of the
@@ -24,8 +26,9 @@ namespace {
 
 enum Type { kBf16, kFp16, kCodes };
 
-constexpr int kWarps = 8;                  // that multiply
-constexpr int kFeat = 16 * kWarps;         // features of a tile
+constexpr int kTeams = 2, kTeam = 4;       // warps that multiply
+constexpr int kWarps = kTeams * kTeam;
+constexpr int kFeat = 32 * kTeam;          // features of a tile
 constexpr int kCols = 128;                 // bytes of a row in a stage
 constexpr int kPitch = kFeat + 4;          // floats between the rows of the partial sums
 
@@ -78,10 +81,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
   constexpr uint32_t kWBytes = kFeat * kCols, kStage = kWBytes + kRows * kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* red = reinterpret_cast<float*>(ring + kDepth * kStage);   // partial sums [kRows][kPitch]
+  float* red = reinterpret_cast<float*>(ring + kDepth * kStage);   // partial sums [kTeams][kRows][kPitch]
   __shared__ GroupTab tab;
   __shared__ uint64_t full[kDepth], empty[kDepth];
-  __shared__ uint64_t sums, read;   // every block's partial sums are in place; have been read
+  __shared__ uint64_t sums, read;   // the cluster's partial sums are in place; have been read
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
@@ -161,73 +164,70 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
       drain_fills(full, kDepth, slot, phase, uses, limit);   // every copy lands before the block exits
     }
   }
-  uint32_t turn = 0;   // parity of the tile, for the cluster's sums
+  const int team = warp / kTeam, f32 = warp % kTeam * 32;
+  uint32_t turn = 0;   // parity of the tile, for the sums
   for (int t = first; warp < kWarps && t < ntiles; t += stride, turn ^= 1) {
     const Tile j = tile_of(t);
-    float acc[NT][4];
-    {
-      const int nt = (j.n + 7) / 8;
+    const int nt = (j.n + 7) / 8;
+    float acc[2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[k][v] = 0.f;
+        for (int v = 0; v < 4; ++v) acc[i][k][v] = 0.f;
 #pragma unroll 1
-      for (int s = s0; s < s1 && ok; ++s) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, limit, abort_flag));
-        if (!ok) {   // still arrives at the cluster's barriers below, so that no block waits for it in vain
-          if (lane == 0) {
-            record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedMma);
-            *abort_flag = 1;
-          }
-          break;
+    for (int s = s0; s < s1 && ok; ++s) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, limit, abort_flag));
+      if (!ok) {   // still arrives at the barriers below, so that no block waits for it in vain
+        if (lane == 0) {
+          record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedMma);
+          *abort_flag = 1;
         }
-        // chunk 2 c + u of a row: with the 128-byte swizzle eight lanes read distinct banks
-        const uint8_t* wst = ring + (size_t)slot * kStage + (warp * 16 + r) * kCols;
-        const uint8_t* xst = ring + (size_t)slot * kStage + kWBytes + r * kCols;
+        break;
+      }
+      // this team's chunks 2 c + team of a row: with the 128-byte swizzle eight lanes read distinct banks
+      const int at = ((2 * c + team) ^ r) << 4;
+      const uint8_t* wst = ring + (size_t)slot * kStage + (f32 + r) * kCols + at;
+      const uint8_t* xst = ring + (size_t)slot * kStage + kWBytes + r * kCols + at;
+      uint4 w[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int at = ((2 * c + u) ^ r) << 4;
-          const uint4 lo = *reinterpret_cast<const uint4*>(wst + at);
-          const uint4 hi = *reinterpret_cast<const uint4*>(wst + 8 * kCols + at);
-          if (kType == kCodes) {
-            const uint4 lo0 = widen(lo.x, lo.y), lo1 = widen(lo.z, lo.w);
-            const uint4 hi0 = widen(hi.x, hi.y), hi1 = widen(hi.z, hi.w);
+      for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint4*>(wst + e * 8 * kCols);
+      if (kType == kCodes) {
+        uint4 a[4][2];
 #pragma unroll
-            for (int k = 0; k < NT; ++k) {
-              if (k >= nt) break;
-              const uint4 x = *reinterpret_cast<const uint4*>(xst + k * 8 * kCols + at);
-              step<kFp16>(acc[k], lo0, hi0, widen(x.x, x.y));
-              step<kFp16>(acc[k], lo1, hi1, widen(x.z, x.w));
-            }
-          } else {
+        for (int e = 0; e < 4; ++e) {
+          a[e][0] = widen(w[e].x, w[e].y);
+          a[e][1] = widen(w[e].z, w[e].w);
+        }
 #pragma unroll
-            for (int k = 0; k < NT; ++k) {
-              if (k >= nt) break;
-              step<kType>(acc[k], lo, hi, *reinterpret_cast<const uint4*>(xst + k * 8 * kCols + at));
-            }
+        for (int k = 0; k < NT; ++k) {
+          if (k >= nt) break;
+          const uint4 x = *reinterpret_cast<const uint4*>(xst + k * 8 * kCols);
+          const uint4 x0 = widen(x.x, x.y), x1 = widen(x.z, x.w);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            step<kFp16>(acc[i][k], a[2 * i][0], a[2 * i + 1][0], x0);
+            step<kFp16>(acc[i][k], a[2 * i][1], a[2 * i + 1][1], x1);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);
-        if (++slot == kDepth) {
-          slot = 0;
-          phase ^= 1;
+      } else {
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+          if (k >= nt) break;
+          const uint4 x = *reinterpret_cast<const uint4*>(xst + k * 8 * kCols);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) step<kType>(acc[i][k], w[2 * i], w[2 * i + 1], x);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      if (++slot == kDepth) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
-    auto put = [&](int f, int row, float v) {
-      if (f >= p.N || row >= j.n) return;
-      if (kType == kCodes) v = v * p.ws[(int64_t)j.g * p.N + f] * p.xs[j.row0 + row];
-      p.y[(j.row0 + row) * p.ldy + f] = (uint16_t)pack16(v, 0.f, p.fp16);
-    };
-    if (p.split == 1) {
-      if (!ok) break;
-#pragma unroll
-      for (int k = 0; k < NT; ++k)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) put(j.f0 + warp * 16 + r + 8 * (v >> 1), 8 * k + 2 * c + (v & 1), acc[k][v]);
-      continue;
-    }
+
     auto wait_sums = [&](uint64_t* bar, uint32_t parity) {
       if (!ok) return;
       ok = __all_sync(0xffffffffu, wait_nap<0, true>(bar, parity, limit, abort_flag));
@@ -236,24 +236,41 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
         *abort_flag = 1;
       }
     };
+    // every block of the cluster (or the one block) hears of this warp's sums, or of its having read
+    auto tell = [&](uint64_t* bar) {
+      __syncwarp();
+      if (p.split == 1) {
+        if (lane == 0) mbar_arrive(bar);
+      } else if (lane < p.split) {
+        mbar_arrive_cluster(cluster_addr(bar, lane));
+      }
+    };
     if (t != first) wait_sums(&read, turn ^ 1);
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) red[(8 * k + 2 * c + (v & 1)) * kPitch + warp * 16 + r + 8 * (v >> 1)] = acc[k][v];
-    __syncwarp();
-    if (lane < p.split) mbar_arrive_cluster(cluster_addr(&sums, lane));
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          red[(team * kRows + 8 * k + 2 * c + (v & 1)) * kPitch + f32 + 16 * i + r + 8 * (v >> 1)] = acc[i][k][v];
+    tell(&sums);
     wait_sums(&sums, turn);
     if (ok) {
       for (int e = rank * 32 * kWarps + threadIdx.x; e < j.n * kFeat; e += p.split * 32 * kWarps) {
-        const int fl = e % kFeat, row = e / kFeat;
+        const int fl = e % kFeat, row = e / kFeat, f = j.f0 + fl;
+        if (f >= p.N) continue;
+        const float* from = red + row * kPitch + fl;
         float v = 0.f;
-        for (int s = 0; s < p.split; ++s) v += load_peer(red + row * kPitch + fl, s);
-        put(j.f0 + fl, row, v);
+        if (p.split == 1) {
+          v = from[0] + from[kRows * kPitch];
+        } else {
+          for (int s = 0; s < p.split; ++s) v += load_peer(from, s) + load_peer(from + kRows * kPitch, s);
+        }
+        if (kType == kCodes) v = v * p.ws[(int64_t)j.g * p.N + f] * p.xs[j.row0 + row];
+        p.y[(j.row0 + row) * p.ldy + f] = (uint16_t)pack16(v, 0.f, p.fp16);
       }
     }
-    __syncwarp();
-    if (lane < p.split) mbar_arrive_cluster(cluster_addr(&read, lane));
+    tell(&read);
   }
   __syncwarp();
   if (p.split > 1) cluster_sync();   // no block ends while another may read its sums or arrive at its barriers
@@ -262,7 +279,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
 template <int kType, int NT, int kDepth>
 cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, const void* W, int size, int id,
                           cudaStream_t s) {
-  constexpr int smem = 1024 + kDepth * (kFeat + 8 * NT) * kCols + 8 * NT * kPitch * 4;
+  constexpr int smem = 1024 + kDepth * (kFeat + 8 * NT) * kCols + kTeams * 8 * NT * kPitch * 4;
   static_assert(smem + sizeof(GroupTab) + 256 <= 232448 / 2 - 1024, "shared memory of an SM");
   auto fn = encode_fn();
   const cuuint64_t row = (cuuint64_t)c.K * size;
@@ -279,11 +296,12 @@ cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, cons
     return cudaErrorInvalidValue;
   p.nst = (int)((row + kCols - 1) / kCols);
   p.nf = (c.N + kFeat - 1) / kFeat;
-  const int64_t tiles = std::min<int64_t>(c.G, c.rows) * p.nf, slots = 2 * (int64_t)num_sms();
+  // the most tiles if the rows spread evenly over the groups, and at all
+  const int64_t live = std::min<int64_t>(c.G, c.rows), slots = 2 * (int64_t)num_sms();
+  const int64_t tiles = (live + (c.rows - live) / (8 * NT)) * p.nf;
   p.split = 1;
   while (p.split < 8 && 2 * p.split * tiles <= slots && 2 * p.split <= p.nst) p.split *= 2;
-  const int64_t most = (c.rows / (8 * NT)) * p.nf + tiles;
-  const int grid = p.split * (int)std::min<int64_t>(most, slots / p.split);
+  const int grid = p.split * (int)std::min<int64_t>((live + c.rows / (8 * NT)) * p.nf, slots / p.split);
   auto kernel = stream_kernel<kType, NT, kDepth>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -309,7 +327,7 @@ template <int kType>
 cudaError_t launch_type(const Grouped& c, StreamParams& p, const void* x, const void* W, int id, cudaStream_t s) {
   constexpr int size = kType == kCodes ? 1 : 2;
   return c.rows <= 8 ? launch_stream<kType, 1, 5>(c, p, x, W, size, id, s)
-                     : launch_stream<kType, 4, 4>(c, p, x, W, size, id, s);
+                     : launch_stream<kType, 4, 3>(c, p, x, W, size, id, s);
 }
 
 StreamParams stream_params(const Grouped& c, const int32_t* begin, const int32_t* end, uint16_t* y, Hdr* hdr) {
