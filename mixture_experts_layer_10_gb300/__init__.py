@@ -178,17 +178,21 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_HOLDS = {BF16: ("torch.bfloat16", "torch.int16", "torch.uint16"), FP16: ("torch.float16", "torch.int16", "torch.uint16"),
-          FP32: ("torch.float32",), "i32": ("torch.int32",), "i8": ("torch.int8",)}
+_holds = None   # kind -> the torch dtypes that hold it
 
 
 def _grouped_ptr(t, shape, kind, what, stride=0):
     """Pointer of an operand of the grouped products: a CUDA tensor of this shape and type, contiguous
     but for the rows of a matrix, which may be `stride` elements apart.  None and integers pass."""
+    global _holds
     if t is None or isinstance(t, int):
         return t
-    if tuple(t.shape) != shape or str(t.dtype) not in _HOLDS[kind] or not t.is_cuda:
-        raise ValueError(f"{what}: CUDA tensor {shape} of {_HOLDS[kind][0]} expected, got {tuple(t.shape)} {t.dtype} "
+    if _holds is None:
+        import torch
+        _holds = {BF16: (torch.bfloat16, torch.int16, torch.uint16), FP16: (torch.float16, torch.int16, torch.uint16),
+                  FP32: (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,)}
+    if t.shape != shape or t.dtype not in _holds[kind] or not t.is_cuda:
+        raise ValueError(f"{what}: CUDA tensor {shape} of {_holds[kind][0]} expected, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
     if stride and stride != shape[1]:
         if t.numel() and (t.stride(1) != 1 or (shape[0] > 1 and t.stride(0) != stride)):
@@ -201,7 +205,8 @@ def _grouped_ptr(t, shape, kind, what, stride=0):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # (the raw handle: a Stream object costs more than the rest of a call's marshalling)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -769,7 +769,8 @@ template <int kOp>
 cudaError_t launch(const Params& p, int64_t most_tiles, int id, cudaStream_t s) {
   using S = Shape<kOp>;
   static int most = 0;   // pairs that run at once, per process (all devices here are alike)
-  cudaError_t e = cudaFuncSetAttribute(grouped_kernel<kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  static SmemOnce once;
+  cudaError_t e = once.set(reinterpret_cast<const void*>(grouped_kernel<kOp>), S::kSmem);
   if (e != cudaSuccess) return e;
   if (most == 0) {
     cudaLaunchConfig_t cfg = {};

@@ -1,6 +1,8 @@
 // What the kernels of the grouped products share: the table of the groups and the 16-bit roundings.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -86,6 +88,21 @@ __device__ __forceinline__ uint4 widen(uint32_t w0, uint32_t w1) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
+
+// A kernel's dynamic shared memory, set once a device rather than at every launch.
+struct SmemOnce {
+  std::atomic<uint64_t> done{0};
+  cudaError_t set(const void* kernel, size_t bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 // Bounded wait with naps of kNap ns between polls.  kCluster acquires at cluster scope: for barriers on
 // which the peer CTA's threads arrive after writing shared memory.

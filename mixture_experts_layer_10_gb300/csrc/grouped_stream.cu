@@ -1,18 +1,15 @@
 // Grouped products of few rows a group (decode steps, small batches): y = x W[g]^T, 16-bit or with 8-bit
 // integers.  Such a product is one read of the weights of the groups that have rows, so the kernel is
-// built around that read.  A tile is 128 features of one group and up to 8 or 32 of its rows; one thread
-// of a block streams the tiles' W and x as TMA boxes, 128 bytes of every row, into a ring of stages,
-// across tile borders, and eight warps multiply with mma.sync: two teams of four, 32 features a warp and
-// every other 16 bytes of a row a team.  (Register fragments: at a few rows a weight the tensor rate is not what counts, and 8-bit
-// codes widen to fp16 on their way from shared memory to the fragment.  32 features a warp halve the
-// codes of x that are widened more than once.)  The order in which the products of a sum are taken is
-// free, so lane (r, c) of a fragment holds 16 consecutive bytes of rows r and r + 8, as one load delivers
-// them.  The teams' sums meet in shared memory.
-//
-// Where the tiles are fewer than the blocks that fit (one token's 8 experts x 768 features are 48), a
-// cluster of 2, 4 or 8 blocks splits the contraction of a tile, and each block adds up its share of the
-// tile's partial sums, in the order of the blocks, from the others' shared memory.  Rows of a group past
-// those of a tile make another tile, whose weights come from L2.
+// built around that read.  A tile is 32 features of one group and up to 8 or 32 of its rows: small enough
+// that one token's 8 experts x 768 features (192 tiles) keep every SM reading, where the 256-feature
+// tiles of the tensor-memory kernel occupy 48.  One thread of a block streams the tiles' weights as TMA
+// boxes, 512 bytes of every row, into a ring of stages, across tile borders; eight warps multiply with
+// mma.sync, each its own 64 bytes of the stage's rows, and add up through shared memory in a fixed order
+// at the end of a tile.  (Register fragments: at a few rows a weight the tensor rate is not what counts, and
+// 8-bit codes widen to fp16 on their way from shared memory to the fragment.)  The order in which the
+// products of a sum are taken is free, so lane (r, c) of a fragment holds 16 consecutive bytes of rows
+// r and r + 8, as one load delivers them.  x comes from L2 straight into fragments, on its way while the
+// stage is waited for.  Rows of a group past those of a tile make another tile, whose weights come from L2.
 #include <algorithm>
 
 #include "common.cuh"
@@ -26,20 +23,23 @@ namespace {
 
 enum Type { kBf16, kFp16, kCodes };
 
-constexpr int kTeams = 2, kTeam = 4;       // warps that multiply
-constexpr int kWarps = kTeams * kTeam;
-constexpr int kFeat = 32 * kTeam;          // features of a tile
-constexpr int kCols = 128;                 // bytes of a row in a stage
+constexpr int kWarps = 8;                  // that multiply
+constexpr int kFeat = 32;                  // features of a tile
+constexpr int kBoxCols = 128;              // bytes of a row in a box
+constexpr int kBoxes = kWarps / 2;         // boxes of a stage, side by side
+constexpr uint32_t kBoxBytes = kFeat * kBoxCols, kStage = kBoxes * kBoxBytes;
+constexpr int kCols = kBoxes * kBoxCols;   // bytes of a row in a stage
 constexpr int kPitch = kFeat + 4;          // floats between the rows of the partial sums
 
 struct StreamParams {
-  CUtensorMap W, x;         // bytes: [G, N, row_bytes] in boxes of 128 rows, [rows, row_bytes] in boxes of 8 NT
+  CUtensorMap W;            // bytes: [G, N, row_bytes] in boxes of 128 bytes x 32 rows
   const int32_t *begin, *end;
+  const uint8_t* x;         // rows ldx bytes apart
   const float *xs, *ws;     // scales (8-bit integers)
   uint16_t* y;
-  int64_t rows, ldy;
-  int nst, N, G, nf;        // stages of a tile; feature tiles of a group
-  int split;                // blocks of a cluster
+  int64_t rows, ldx, ldy;   // ldx in bytes, ldy in elements
+  int row_bytes;            // of a row of W or x
+  int N, G, nf;             // nf: feature tiles of a group
   bool fp16;                // y's type
   Hdr* hdr;
 };
@@ -68,23 +68,29 @@ __device__ __forceinline__ void step(float (&d)[4], const uint4& lo, const uint4
   mma<kType>(d, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
 }
 
-__device__ __forceinline__ float load_peer(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(p, rank)) : "memory");
+// 16 bytes of x, zero where not `in`.
+__device__ __forceinline__ uint4 load_x(const uint8_t* at, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "mov.u32 %3, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(at), "r"((int)in));
   return v;
 }
+
+// A barrier of the eight multiplying warps.
+__device__ __forceinline__ void bar_warps() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 // NT: 8-row tiles.
 template <int kType, int NT, int kDepth>
 __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __grid_constant__ StreamParams p) {
   constexpr int kRows = 8 * NT;
-  constexpr uint32_t kWBytes = kFeat * kCols, kStage = kWBytes + kRows * kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* red = reinterpret_cast<float*>(ring + kDepth * kStage);   // partial sums [kTeams][kRows][kPitch]
+  float* red = reinterpret_cast<float*>(ring + kDepth * kStage);   // partial sums [kWarps][kRows][kPitch]
   __shared__ GroupTab tab;
   __shared__ uint64_t full[kDepth], empty[kDepth];
-  __shared__ uint64_t sums, read;   // the cluster's partial sums are in place; have been read
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
@@ -93,20 +99,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kWarps);
     }
-    mbar_init(&sums, kWarps * p.split);
-    mbar_init(&read, kWarps * p.split);
     abort_word = 0;
     fence_mbar_init();
     tma_prefetch(&p.W);
-    tma_prefetch(&p.x);
   }
   const int tiles = load_groups(tab, p.begin, p.end, p.G, p.rows, kRows, p.hdr);   // (a barrier of the block, too)
-  if (p.split > 1) cluster_sync();   // all blocks' barriers exist before any remote arrival
   const int ntiles = max(tiles, 0) * p.nf;
-  const int rank = p.split > 1 ? (int)cluster_rank() : 0;
-  const int first = blockIdx.x / p.split, stride = gridDim.x / p.split;
-  const int per = (p.nst + p.split - 1) / p.split;                    // this block's stages of a tile
-  const int s0 = min(p.nst, rank * per), s1 = min(p.nst, s0 + per);
+  const int nst = (p.row_bytes + kCols - 1) / kCols;
   const uint64_t limit = wait_limit_ns(p.hdr);
 
   struct Tile {
@@ -139,9 +138,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
       int uses = 0;
       // test hook: the first block skips one fill, so that the wait for it runs out
       const int skip = blockIdx.x == 0 ? *((volatile const int32_t*)&p.hdr->stall_fill_p1) - 1 : -1;
-      for (int t = first; ok && t < ntiles; t += stride) {
+      for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
         const Tile j = tile_of(t);
-        for (int s = s0; s < s1; ++s) {
+        for (int s = 0; s < nst; ++s) {
           ok = mbar_wait(&empty[slot], phase ^ 1, limit, abort_flag);
           if (!ok) {
             record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedProducer);
@@ -150,9 +149,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
           }
           if (uses != skip) {
             uint8_t* st = ring + (size_t)slot * kStage;
-            mbar_arrive_expect_tx(&full[slot], kStage);
-            tma_load_3d(st, &p.W, &full[slot], s * kCols, j.f0, j.g);
-            tma_load_2d(st + kWBytes, &p.x, &full[slot], s * kCols, j.row0);
+            const int boxes = min(kBoxes, (p.row_bytes - s * kCols + kBoxCols - 1) / kBoxCols);
+            mbar_arrive_expect_tx(&full[slot], boxes * kBoxBytes);
+            for (int b = 0; b < boxes; ++b)
+              tma_load_3d(st + b * kBoxBytes, &p.W, &full[slot], s * kCols + b * kBoxCols, j.f0, j.g);
           }
           ++uses;
           if (++slot == kDepth) {
@@ -163,10 +163,14 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
       }
       drain_fills(full, kDepth, slot, phase, uses, limit);   // every copy lands before the block exits
     }
+    return;
   }
-  const int team = warp / kTeam, f32 = warp % kTeam * 32;
-  uint32_t turn = 0;   // parity of the tile, for the sums
-  for (int t = first; warp < kWarps && t < ntiles; t += stride, turn ^= 1) {
+
+  // this warp's 64 bytes: the even or odd 16-byte chunks of a box, which in the 128-byte swizzle keep the
+  // banks of eight lanes distinct
+  const int chunk = 2 * c + (warp & 1), col = warp / 2 * kBoxCols + chunk * 16;
+  const uint32_t wat = warp / 2 * kBoxBytes + r * kBoxCols + ((chunk ^ r) << 4);
+  for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
     const Tile j = tile_of(t);
     const int nt = (j.n + 7) / 8;
     float acc[2][NT][4];
@@ -176,48 +180,51 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
       for (int k = 0; k < NT; ++k)
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][k][v] = 0.f;
+    const uint8_t* xrow = p.x + j.row0 * p.ldx + col;
 #pragma unroll 1
-    for (int s = s0; s < s1 && ok; ++s) {
+    for (int s = 0; s < nst && ok; ++s) {
+      // (rows past the tile's last are read as that: nothing stores their products)
+      uint4 x[NT];
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+        x[k] = load_x(xrow + min(8 * k + r, j.n - 1) * p.ldx + s * kCols, k < nt && s * kCols + col < p.row_bytes);
       ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, limit, abort_flag));
-      if (!ok) {   // still arrives at the barriers below, so that no block waits for it in vain
+      if (!ok) {   // keeps to the barriers below, so that no warp waits for it in vain
         if (lane == 0) {
           record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedMma);
           *abort_flag = 1;
         }
         break;
       }
-      // this team's chunks 2 c + team of a row: with the 128-byte swizzle eight lanes read distinct banks
-      const int at = ((2 * c + team) ^ r) << 4;
-      const uint8_t* wst = ring + (size_t)slot * kStage + (f32 + r) * kCols + at;
-      const uint8_t* xst = ring + (size_t)slot * kStage + kWBytes + r * kCols + at;
-      uint4 w[4];
+      if (s * kCols + warp / 2 * kBoxCols < p.row_bytes) {   // the stage has this warp's box
+        const uint8_t* st = ring + (size_t)slot * kStage + wat;
+        uint4 w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint4*>(wst + e * 8 * kCols);
-      if (kType == kCodes) {
-        uint4 a[4][2];
+        for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint4*>(st + e * 8 * kBoxCols);
+        if (kType == kCodes) {
+          uint4 a[4][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e][0] = widen(w[e].x, w[e].y);
-          a[e][1] = widen(w[e].z, w[e].w);
-        }
-#pragma unroll
-        for (int k = 0; k < NT; ++k) {
-          if (k >= nt) break;
-          const uint4 x = *reinterpret_cast<const uint4*>(xst + k * 8 * kCols);
-          const uint4 x0 = widen(x.x, x.y), x1 = widen(x.z, x.w);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            step<kFp16>(acc[i][k], a[2 * i][0], a[2 * i + 1][0], x0);
-            step<kFp16>(acc[i][k], a[2 * i][1], a[2 * i + 1][1], x1);
+          for (int e = 0; e < 4; ++e) {
+            a[e][0] = widen(w[e].x, w[e].y);
+            a[e][1] = widen(w[e].z, w[e].w);
           }
-        }
-      } else {
 #pragma unroll
-        for (int k = 0; k < NT; ++k) {
-          if (k >= nt) break;
-          const uint4 x = *reinterpret_cast<const uint4*>(xst + k * 8 * kCols);
+          for (int k = 0; k < NT; ++k) {
+            if (k >= nt) break;
+            const uint4 x0 = widen(x[k].x, x[k].y), x1 = widen(x[k].z, x[k].w);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) step<kType>(acc[i][k], w[2 * i], w[2 * i + 1], x);
+            for (int i = 0; i < 2; ++i) {
+              step<kFp16>(acc[i][k], a[2 * i][0], a[2 * i + 1][0], x0);
+              step<kFp16>(acc[i][k], a[2 * i][1], a[2 * i + 1][1], x1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < NT; ++k) {
+            if (k >= nt) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) step<kType>(acc[i][k], w[2 * i], w[2 * i + 1], x[k]);
+          }
         }
       }
       __syncwarp();
@@ -228,115 +235,78 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) stream_kernel(const __gr
       }
     }
 
-    auto wait_sums = [&](uint64_t* bar, uint32_t parity) {
-      if (!ok) return;
-      ok = __all_sync(0xffffffffu, wait_nap<0, true>(bar, parity, limit, abort_flag));
-      if (!ok && lane == 0) {
-        record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedEpilogue);
-        *abort_flag = 1;
-      }
-    };
-    // every block of the cluster (or the one block) hears of this warp's sums, or of its having read
-    auto tell = [&](uint64_t* bar) {
-      __syncwarp();
-      if (p.split == 1) {
-        if (lane == 0) mbar_arrive(bar);
-      } else if (lane < p.split) {
-        mbar_arrive_cluster(cluster_addr(bar, lane));
-      }
-    };
-    if (t != first) wait_sums(&read, turn ^ 1);
+    bar_warps();   // the previous tile's sums have been read
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int k = 0; k < NT; ++k)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          red[(team * kRows + 8 * k + 2 * c + (v & 1)) * kPitch + f32 + 16 * i + r + 8 * (v >> 1)] = acc[i][k][v];
-    tell(&sums);
-    wait_sums(&sums, turn);
-    if (ok) {
-      for (int e = rank * 32 * kWarps + threadIdx.x; e < j.n * kFeat; e += p.split * 32 * kWarps) {
-        const int fl = e % kFeat, row = e / kFeat, f = j.f0 + fl;
-        if (f >= p.N) continue;
-        const float* from = red + row * kPitch + fl;
-        float v = 0.f;
-        if (p.split == 1) {
-          v = from[0] + from[kRows * kPitch];
-        } else {
-          for (int s = 0; s < p.split; ++s) v += load_peer(from, s) + load_peer(from + kRows * kPitch, s);
-        }
-        if (kType == kCodes) v = v * p.ws[(int64_t)j.g * p.N + f] * p.xs[j.row0 + row];
-        p.y[(j.row0 + row) * p.ldy + f] = (uint16_t)pack16(v, 0.f, p.fp16);
+          red[(warp * kRows + 8 * k + 2 * c + (v & 1)) * kPitch + 16 * i + r + 8 * (v >> 1)] = acc[i][k][v];
+    bar_warps();
+    // two features of a row a thread
+    for (int e = threadIdx.x; e < j.n * (kFeat / 2); e += 32 * kWarps) {
+      const int fl = e % (kFeat / 2) * 2, row = e / (kFeat / 2), f = j.f0 + fl;
+      if (f >= p.N) continue;   // N is a multiple of 8
+      const float* from = red + row * kPitch + fl;
+      float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 part = *reinterpret_cast<const float2*>(from + k * kRows * kPitch);
+        v0 += part.x;
+        v1 += part.y;
       }
+      if (kType == kCodes) {
+        const float2 ws = __ldg(reinterpret_cast<const float2*>(p.ws + (int64_t)j.g * p.N + f));
+        const float xs = p.xs[j.row0 + row];
+        v0 = v0 * ws.x * xs;
+        v1 = v1 * ws.y * xs;
+      }
+      *reinterpret_cast<uint32_t*>(p.y + (j.row0 + row) * p.ldy + f) = pack16(v0, v1, p.fp16);
     }
-    tell(&read);
   }
-  __syncwarp();
-  if (p.split > 1) cluster_sync();   // no block ends while another may read its sums or arrive at its barriers
 }
 
 template <int kType, int NT, int kDepth>
-cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, const void* W, int size, int id,
-                          cudaStream_t s) {
-  constexpr int smem = 1024 + kDepth * (kFeat + 8 * NT) * kCols + kTeams * 8 * NT * kPitch * 4;
+cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* W, int id, cudaStream_t s) {
+  constexpr int smem = 1024 + kDepth * kStage + kWarps * 8 * NT * kPitch * 4;
   static_assert(smem + sizeof(GroupTab) + 256 <= 232448 / 2 - 1024, "shared memory of an SM");
   auto fn = encode_fn();
-  const cuuint64_t row = (cuuint64_t)c.K * size;
-  const cuuint64_t wdims[3] = {row, (cuuint64_t)c.N, (cuuint64_t)c.G}, wstrides[2] = {row, row * c.N};
-  const cuuint64_t xdims[2] = {row, (cuuint64_t)c.rows}, xstrides[1] = {(cuuint64_t)c.ldi * size};
-  const cuuint32_t wbox[3] = {kCols, kFeat, 1}, xbox[2] = {kCols, 8 * NT}, es[3] = {1, 1, 1};
-  if (!fn ||
-      fn(&p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(W), wdims, wstrides, wbox, es,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-      fn(&p.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(x), xdims, xstrides, xbox, es,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  const cuuint64_t row = (cuuint64_t)p.row_bytes;
+  const cuuint64_t dims[3] = {row, (cuuint64_t)c.N, (cuuint64_t)c.G}, strides[2] = {row, row * c.N};
+  const cuuint32_t box[3] = {kBoxCols, kFeat, 1}, es[3] = {1, 1, 1};
+  if (!fn || fn(&p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(W), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  p.nst = (int)((row + kCols - 1) / kCols);
   p.nf = (c.N + kFeat - 1) / kFeat;
-  // the most tiles if the rows spread evenly over the groups, and at all
-  const int64_t live = std::min<int64_t>(c.G, c.rows), slots = 2 * (int64_t)num_sms();
-  const int64_t tiles = (live + (c.rows - live) / (8 * NT)) * p.nf;
-  p.split = 1;
-  while (p.split < 8 && 2 * p.split * tiles <= slots && 2 * p.split <= p.nst) p.split *= 2;
-  const int grid = p.split * (int)std::min<int64_t>((live + c.rows / (8 * NT)) * p.nf, slots / p.split);
+  const int64_t tiles = (std::min<int64_t>(c.G, c.rows) + c.rows / (8 * NT)) * p.nf;   // at most
   auto kernel = stream_kernel<kType, NT, kDepth>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemOnce once;
+  cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(32 * (kWarps + 1));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
   prof_mark(id, s, true);
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  kernel<<<(int)std::min<int64_t>(tiles, 2 * (int64_t)num_sms()), 32 * (kWarps + 1), smem, s>>>(p);
   prof_mark(id, s, false);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return cudaGetLastError();
 }
 
 template <int kType>
-cudaError_t launch_type(const Grouped& c, StreamParams& p, const void* x, const void* W, int id, cudaStream_t s) {
-  constexpr int size = kType == kCodes ? 1 : 2;
-  return c.rows <= 8 ? launch_stream<kType, 1, 5>(c, p, x, W, size, id, s)
-                     : launch_stream<kType, 4, 3>(c, p, x, W, size, id, s);
+cudaError_t launch_type(const Grouped& c, StreamParams& p, const void* W, int id, cudaStream_t s) {
+  return c.rows <= 8 ? launch_stream<kType, 1, 5>(c, p, W, id, s) : launch_stream<kType, 4, 3>(c, p, W, id, s);
 }
 
-StreamParams stream_params(const Grouped& c, const int32_t* begin, const int32_t* end, uint16_t* y, Hdr* hdr) {
+StreamParams stream_params(const Grouped& c, const int32_t* begin, const int32_t* end, const void* x, uint16_t* y,
+                           int size, Hdr* hdr) {
   StreamParams p{};
   p.begin = begin;
   p.end = end;
+  p.x = static_cast<const uint8_t*>(x);
   p.y = y;
   p.rows = c.rows;
+  p.ldx = c.ldi * size;
   p.ldy = c.ldo;
+  p.row_bytes = c.K * size;
   p.N = c.N;
   p.G = c.G;
   p.fp16 = c.fp16;
@@ -350,17 +320,17 @@ bool stream_eligible(const Grouped& c) { return c.rows <= 32 * (int64_t)c.G || c
 
 cudaError_t launch_stream_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
                              const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s) {
-  StreamParams p = stream_params(c, begin, end, y, hdr);
-  return c.fp16 ? launch_type<kFp16>(c, p, x, W, kKGroupedMm, s) : launch_type<kBf16>(c, p, x, W, kKGroupedMm, s);
+  StreamParams p = stream_params(c, begin, end, x, y, 2, hdr);
+  return c.fp16 ? launch_type<kFp16>(c, p, W, kKGroupedMm, s) : launch_type<kBf16>(c, p, W, kKGroupedMm, s);
 }
 
 cudaError_t launch_stream_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,
                              const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr,
                              cudaStream_t s) {
-  StreamParams p = stream_params(c, begin, end, y, hdr);
+  StreamParams p = stream_params(c, begin, end, q, y, 1, hdr);
   p.xs = qs;
   p.ws = Ws;
-  return launch_type<kCodes>(c, p, q, Wq, kKGroupedI8, s);
+  return launch_type<kCodes>(c, p, Wq, kKGroupedI8, s);
 }
 
 }  // namespace moe
