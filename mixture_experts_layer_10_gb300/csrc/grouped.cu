@@ -83,7 +83,8 @@ struct Params {
   int depth;                  // contraction length (rows times a weight)
   int width;                  // features of the output row; weight gradient: columns of dW (n_in)
   int M;                      // weight gradient: rows of dW (n_out)
-  int G, nf, mf;              // tiles across width; weight gradient: tiles across M
+  int G, nf, mf;              // whole tiles across width; weight gradient: all tiles across width and M
+  bool narrow;                // rows times a weight: there is a last, narrower tile across width
   bool fp16, wide_a, wide_b;  // wide: one copy fetches two 64-column boxes (columns a multiple of 64)
   bool dw_fp32, acc;
   uint32_t idesc;             // N and M as of a full tile
@@ -100,22 +101,28 @@ struct Job {
 // chunks of up to 16 row tiles x all feature tiles with the row tile fastest, so that the pairs at work
 // share a panel of each operand in L2.
 __device__ __forceinline__ Job row_job(const Params& p, const GroupTab& s, int t) {
-  const int m = t / p.nf;
+  // the tiles of the last, narrower feature tile (if there is one) come after all others: what is
+  // left to do while the last pairs finish is then short
+  const int full = s.first[p.G] * p.nf;
+  const bool narrow = t >= full;
+  const int nf = narrow ? 1 : p.nf;
+  if (narrow) t -= full;
+  const int m = t / nf;
   int lo = 0, hi = p.G - 1;   // the last group whose first tile <= m
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (s.first[mid] <= m) lo = mid; else hi = mid - 1;
   }
   const int first = s.first[lo], mt = s.first[lo + 1] - first;
-  const int local = t - first * p.nf;
-  const int c = local / (kChunkM * p.nf);
+  const int local = t - first * nf;
+  const int c = local / (kChunkM * nf);
   const int cm = min(kChunkM, mt - c * kChunkM);
-  const int r = local - c * kChunkM * p.nf;
+  const int r = local - c * kChunkM * nf;
   Job j{};
   j.g = lo;
   j.row = s.begin[lo] + (c * kChunkM + r % cm) * kTile;
   j.n = min(kTile, s.end[lo] - j.row);
-  j.f0 = r / cm * kTile;
+  j.f0 = narrow ? p.nf * kTile : r / cm * kTile;
   return j;
 }
 
@@ -384,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t limit = wait_limit_ns(p.hdr);
-  const int ntiles = rtiles < 0 ? 0 : (kOp == kDw ? p.G * p.mf * p.nf : rtiles * p.nf);
+  const int ntiles = rtiles < 0 ? 0 : (kOp == kDw ? p.G * p.mf * p.nf : rtiles * (p.nf + (int)p.narrow));
   Walk<kOp> walk(p, tab, pair, npairs, ntiles);
   Job j;
 
@@ -806,9 +813,10 @@ cudaError_t launch_grouped_mm(const Grouped& c, const int32_t* begin, const int3
   p.ldy = c.ldo;
   p.depth = c.K;
   p.width = c.N;
-  p.nf = (c.N + kTile - 1) / kTile;
+  p.nf = c.N / kTile;
+  p.narrow = c.N % kTile != 0;
   p.idesc = idesc_of(c.fp16, false, false);
-  return launch<kMm>(p, most_row_tiles(c) * p.nf, kKGroupedMm, s);
+  return launch<kMm>(p, most_row_tiles(c) * (p.nf + p.narrow), kKGroupedMm, s);
 }
 
 cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* dy,
@@ -822,9 +830,10 @@ cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int3
   p.ldy = c.ldi;
   p.depth = c.N;
   p.width = c.K;
-  p.nf = (c.K + kTile - 1) / kTile;
+  p.nf = c.K / kTile;
+  p.narrow = c.K % kTile != 0;
   p.idesc = idesc_of(c.fp16, true, false);
-  return launch<kDx>(p, most_row_tiles(c) * p.nf, kKGroupedDx, s);
+  return launch<kDx>(p, most_row_tiles(c) * (p.nf + p.narrow), kKGroupedDx, s);
 }
 
 cudaError_t launch_grouped_dw(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* dy,
@@ -864,9 +873,10 @@ cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int3
   p.ws = Ws;
   p.depth = c.K;
   p.width = c.N;
-  p.nf = (c.N + kTile - 1) / kTile;
+  p.nf = c.N / kTile;
+  p.narrow = c.N % kTile != 0;
   p.idesc = idesc_of(true, false, false);   // widened codes are fp16, whatever y's type
-  return launch<kI8>(p, most_row_tiles(c) * p.nf, kKGroupedI8, s);
+  return launch<kI8>(p, most_row_tiles(c) * (p.nf + p.narrow), kKGroupedI8, s);
 }
 
 cudaError_t launch_segments(const Tables* tabs, int G, int32_t* begin, int32_t* end, cudaStream_t s) {

@@ -341,11 +341,11 @@ def test_repeats_streams_and_graphs(moe, sizes):
     assert moe.moe_check_error(ws) == 0
 
 
-@pytest.mark.parametrize("sizes,op", [([600, 70], "mm"), ([600, 70], "dx"), ([600, 70], "dw"), ([600, 70], "i8"),
-                                      ([9, 3], "mm"), ([5, 2], "mm"), ([9, 3], "i8"), ([1, 1], "i8")])
-def test_a_wait_that_runs_out_is_reported(moe, sizes, op):
-    """A fill of the operand ring that never comes ends in MOE_ERR_TIMEOUT, and the next call runs."""
-    K = N = 2048 if sizes[0] < 10 else 256
+@pytest.mark.parametrize("op", ["mm", "dx", "dw", "i8"])
+def test_a_wait_that_runs_out_is_reported(moe, op):
+    """A fill of the operand ring that never comes ends in MOE_ERR_TIMEOUT, and the next call runs.  (Few
+    rows a group take a kernel that waits for nothing.)"""
+    sizes, K, N = [600, 70], 256, 256
     begin, end, rows = layout(sizes)
     cfg = moe.grouped_config(rows, K, N, 2)
     ws = moe.grouped_workspace(cfg)
