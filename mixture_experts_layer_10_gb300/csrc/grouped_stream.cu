@@ -1,18 +1,22 @@
 // Grouped products of few rows a group (decode steps, small batches): y = x W[g]^T, 16-bit or with 8-bit
 // integers.  Such a product is one read of the weights of the groups that have rows, so the kernel is
-// built around that read.  A warp takes 16 or 32 features of one group and streams their rows of W from
-// global memory straight into the registers of mma.sync fragments: the order in which the products of a
-// sum are taken is free, so lane (r, c) of a fragment may hold 16 consecutive bytes of rows r and r + 8,
-// as one load delivers them, if the lanes of the x fragment hold the same places of a row of x.  No
-// shared memory, barrier or tensor map stands between HBM and the tensor cores, and any number of
-// warps can be at work: where the features are few, up to eight warps split K and add up through
-// shared memory in a fixed order.  (tcgen05's 128-row tiles leave most SMs without work here: one token's
-// 8 experts x 768 features are 48 of them.)  x is read from L1 and L2; rows of a group past the
-// 8 NT of a tile make another tile, whose weights come from L2.
+// built around that read.  A tile is 128 features of one group and up to 8 or 32 of its rows; one thread
+// of a block streams the tiles' W and x as TMA boxes, 128 bytes of every row, into a ring of stages,
+// across tile borders, and eight warps multiply 16 features each with mma.sync.  (Register fragments: at
+// a few rows a weight the tensor rate is not what counts, and 8-bit codes widen to fp16 on their way
+// from shared memory to the fragment.)  The order in which the products of a sum are taken is free, so
+// lane (r, c) of a fragment holds 16 consecutive bytes of rows r and r + 8, as one load delivers them.
+//
+// Where the tiles are fewer than the blocks that fit (one token's 8 experts x 768 features are 48), a
+// cluster of 2, 4 or 8 blocks splits the contraction of a tile, and each block adds up its share of the
+// tile's partial sums, in the order of the blocks, from the others' shared memory.  Rows of a group past
+// those of a tile make another tile, whose weights come from L2.
 #include <algorithm>
 
 #include "common.cuh"
 #include "grouped.cuh"
+#include "ptx.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 
@@ -20,40 +24,23 @@ namespace {
 
 enum Type { kBf16, kFp16, kCodes };
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;                  // that multiply
+constexpr int kFeat = 16 * kWarps;         // features of a tile
+constexpr int kCols = 128;                 // bytes of a row in a stage
+constexpr int kMaxSplit = 8;               // blocks of a cluster
+constexpr int kPitch = kFeat + 4;          // floats between the rows of the partial sums
 
 struct StreamParams {
+  CUtensorMap W, x;         // bytes: [G, N, row_bytes] in boxes of 128 rows, [rows, row_bytes] in boxes of 8 NT
   const int32_t *begin, *end;
-  const uint8_t *x, *W;     // rows ldx bytes apart; weights [G, N, K]
   const float *xs, *ws;     // scales (8-bit integers)
   uint16_t* y;
-  int64_t rows, ldx, ldy;   // ldx in bytes, ldy in elements
-  int row_bytes;            // of a row of W or x
-  int N, G, nf, wk_log2;    // feature tiles of a group; log2 of the warps that split K
+  int64_t rows, ldy;
+  int nst, N, G, nf;        // stages of a tile; feature tiles of a group
+  int split;                // blocks of a cluster
   bool fp16;                // y's type
   Hdr* hdr;
 };
-
-// 16 bytes under a predicate (else zero): of a weight, which no other block reads, or of x.
-__device__ __forceinline__ uint4 load_once(const uint8_t* at, bool in) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
-      "mov.u32 %3, 0;\n\t@p ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(at), "r"((int)in));
-  return v;
-}
-
-__device__ __forceinline__ uint4 load_shared(const uint8_t* at, bool in) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
-      "mov.u32 %3, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(at), "r"((int)in));
-  return v;
-}
 
 template <int kType>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -79,22 +66,55 @@ __device__ __forceinline__ void step(float (&d)[4], const uint4& lo, const uint4
   mma<kType>(d, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
 }
 
-// MT: 16-feature tiles of a warp; NT: 8-row tiles; a chunk is 64 KC bytes of every row.  A warp has one
-// chunk of W and x in flight, with nothing between the loads that waits; what hides their latency
-// is the kBlocks x 8 warps of an SM, each at its own place.
-template <int kType, int MT, int NT, int KC, int kBlocks>
-__global__ void __launch_bounds__(32 * kWarps, kBlocks) stream_kernel(const __grid_constant__ StreamParams p) {
+__device__ __forceinline__ float2 load_peer(const float* p, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(cluster_addr(p, rank))
+               : "memory");
+  return v;
+}
+
+// NT: 8-row tiles.
+template <int kType, int NT, int kDepth, int kBlocks>
+__global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(const __grid_constant__ StreamParams p) {
+  constexpr int kRows = 8 * NT;
+  constexpr uint32_t kWBytes = kFeat * kCols, kStage = kWBytes + kRows * kCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* red = reinterpret_cast<float*>(ring + kDepth * kStage);   // partial sums [kRows][kPitch]
   __shared__ GroupTab tab;
-  extern __shared__ float red[];   // partial sums, [warp][MT][NT][4][32]
-  constexpr int kFeat = 16 * MT, kRows = 8 * NT, kVals = MT * NT * 128;
-  const int tiles = load_groups(tab, p.begin, p.end, p.G, p.rows, kRows, p.hdr);
-  if (tiles < 0) return;
+  __shared__ uint64_t full[kDepth], empty[kDepth];
+  __shared__ uint64_t sums, read;   // every block's partial sums are in place; have been read
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-  const int wk = 1 << p.wk_log2, part = warp & (wk - 1), fw = warp >> p.wk_log2, nfw = kWarps >> p.wk_log2;
-  const int nchunk = (p.row_bytes + 64 * KC - 1) / (64 * KC);
-  const int ntiles = tiles * p.nf;
-  for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
-    // the group of row tile t / nf; within a group the row tiles of a feature tile follow each other
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kDepth; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    mbar_init(&sums, kWarps * p.split);
+    mbar_init(&read, kWarps * p.split);
+    abort_word = 0;
+    fence_mbar_init();
+    tma_prefetch(&p.W);
+    tma_prefetch(&p.x);
+  }
+  const int tiles = load_groups(tab, p.begin, p.end, p.G, p.rows, kRows, p.hdr);   // (a barrier of the block, too)
+  if (p.split > 1) cluster_sync();   // all blocks' barriers exist before any remote arrival
+  const int ntiles = max(tiles, 0) * p.nf;
+  const int rank = p.split > 1 ? (int)cluster_rank() : 0;
+  const int first = blockIdx.x / p.split, stride = gridDim.x / p.split;
+  const int per = (p.nst + p.split - 1) / p.split;                    // this block's stages of a tile
+  const int s0 = min(p.nst, rank * per), s1 = min(p.nst, s0 + per);
+  const uint64_t limit = wait_limit_ns(p.hdr);
+
+  struct Tile {
+    int g, f0, row0, n;
+  };
+  // the group of row tile t / nf; within a group the row tiles of a feature tile follow each other
+  auto tile_of = [&](int t) {
     const int m = t / p.nf;
     int lo = 0, hi = p.G - 1;
     while (lo < hi) {
@@ -104,151 +124,228 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) stream_kernel(const __gr
     const int mt = tab.first[lo + 1] - tab.first[lo];
     const int local = t - tab.first[lo] * p.nf;
     const int ft = mt == 1 ? local : local / mt;
-    const int row0 = tab.begin[lo] + (local - ft * mt) * kRows;
-    const int n = min(kRows, tab.end[lo] - row0);
-    const int f0 = (ft * nfw + fw) * kFeat;
-    const int nt = (n + 7) / 8;
+    Tile j;
+    j.g = lo;
+    j.f0 = ft * kFeat;
+    j.row0 = tab.begin[lo] + (local - ft * mt) * kRows;
+    j.n = min(kRows, tab.end[lo] - j.row0);
+    return j;
+  };
 
-    float acc[MT][NT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
+  int slot = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  if (warp == kWarps) {
+    if (lane == 0) {
+      int uses = 0;
+      // test hook: the first block skips one fill, so that the wait for it runs out
+      const int skip = blockIdx.x == 0 ? *((volatile const int32_t*)&p.hdr->stall_fill_p1) - 1 : -1;
+      for (int t = first; ok && t < ntiles; t += stride) {
+        const Tile j = tile_of(t);
+        for (int s = s0; s < s1; ++s) {
+          ok = wait_nap<20>(&empty[slot], phase ^ 1, limit, abort_flag);
+          if (!ok) {
+            record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedProducer);
+            *abort_flag = 1;
+            break;
+          }
+          if (uses != skip) {
+            uint8_t* st = ring + (size_t)slot * kStage;
+            mbar_arrive_expect_tx(&full[slot], kStage);
+            tma_load_3d(st, &p.W, &full[slot], s * kCols, j.f0, j.g);
+            tma_load_2d(st + kWBytes, &p.x, &full[slot], s * kCols, j.row0);
+          }
+          ++uses;
+          if (++slot == kDepth) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      drain_fills(full, kDepth, slot, phase, uses, limit);   // every copy lands before the block exits
+    }
+  }
+  uint32_t turn = 0;   // parity of the tile, for the cluster's sums
+  for (int t = first; warp < kWarps && t < ntiles; t += stride, turn ^= 1) {
+    const Tile j = tile_of(t);
+    float acc[NT][4];
+    {
+      const int nt = (j.n + 7) / 8;
 #pragma unroll
       for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][k][v] = 0.f;
-
-    if (f0 < p.N) {
-      // rows past the last feature are read as the last, rows past the group's last as that: nothing
-      // stores their products
-      const uint8_t* wrow[MT][2];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          wrow[i][h] = p.W + ((int64_t)lo * p.N + min(f0 + 16 * i + 8 * h + r, p.N - 1)) * p.row_bytes + c * 16;
-      const uint8_t* xrow = p.x + row0 * p.ldx + c * 16;
+        for (int v = 0; v < 4; ++v) acc[k][v] = 0.f;
 #pragma unroll 1
-      for (int ch = part; ch < nchunk; ch += wk) {
-        uint4 w[KC][MT][2], x[KC][NT];
-#pragma unroll
-        for (int u = 0; u < KC; ++u) {
-          const int at = (ch * KC + u) * 64;
-          const bool in = at + c * 16 < p.row_bytes;
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) w[u][i][h] = load_once(wrow[i][h] + at, in);
-#pragma unroll
-          for (int k = 0; k < NT; ++k) x[u][k] = load_shared(xrow + min(8 * k + r, n - 1) * p.ldx + at, in && k < nt);
+      for (int s = s0; s < s1 && ok; ++s) {
+        ok = __all_sync(0xffffffffu, wait_nap<0>(&full[slot], phase, limit, abort_flag));
+        if (!ok) {   // still arrives at the cluster's barriers below, so that no block waits for it in vain
+          if (lane == 0) {
+            record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedMma);
+            *abort_flag = 1;
+          }
+          break;
         }
+        // chunk 2 c + u of a row: with the 128-byte swizzle eight lanes read distinct banks
+        const uint8_t* wst = ring + (size_t)slot * kStage + (warp * 16 + r) * kCols;
+        const uint8_t* xst = ring + (size_t)slot * kStage + kWBytes + r * kCols;
 #pragma unroll
-        for (int u = 0; u < KC; ++u) {
+        for (int u = 0; u < 2; ++u) {
+          const int at = ((2 * c + u) ^ r) << 4;
+          const uint4 lo = *reinterpret_cast<const uint4*>(wst + at);
+          const uint4 hi = *reinterpret_cast<const uint4*>(wst + 8 * kCols + at);
           if (kType == kCodes) {
-            uint4 a[MT][2][2];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                a[i][h][0] = widen(w[u][i][h].x, w[u][i][h].y);
-                a[i][h][1] = widen(w[u][i][h].z, w[u][i][h].w);
-              }
+            const uint4 lo0 = widen(lo.x, lo.y), lo1 = widen(lo.z, lo.w);
+            const uint4 hi0 = widen(hi.x, hi.y), hi1 = widen(hi.z, hi.w);
 #pragma unroll
             for (int k = 0; k < NT; ++k) {
               if (k >= nt) break;
-              const uint4 x0 = widen(x[u][k].x, x[u][k].y), x1 = widen(x[u][k].z, x[u][k].w);
-#pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                step<kFp16>(acc[i][k], a[i][0][0], a[i][1][0], x0);
-                step<kFp16>(acc[i][k], a[i][0][1], a[i][1][1], x1);
-              }
+              const uint4 x = *reinterpret_cast<const uint4*>(xst + k * 8 * kCols + at);
+              step<kFp16>(acc[k], lo0, hi0, widen(x.x, x.y));
+              step<kFp16>(acc[k], lo1, hi1, widen(x.z, x.w));
             }
           } else {
 #pragma unroll
             for (int k = 0; k < NT; ++k) {
               if (k >= nt) break;
-#pragma unroll
-              for (int i = 0; i < MT; ++i) step<kType>(acc[i][k], w[u][i][0], w[u][i][1], x[u][k]);
+              step<kType>(acc[k], lo, hi, *reinterpret_cast<const uint4*>(xst + k * 8 * kCols + at));
             }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        if (++slot == kDepth) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
     }
-
-    auto put = [&](int f, int row, float v) {
-      if (f >= p.N || row >= n) return;
-      if (kType == kCodes) v = v * p.ws[(int64_t)lo * p.N + f] * p.xs[row0 + row];
-      p.y[(row0 + row) * p.ldy + f] = (uint16_t)pack16(v, 0.f, p.fp16);
+    if (p.split == 1) {
+      if (!ok) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int f = j.f0 + warp * 16 + r + 8 * h;
+        if (f >= p.N) continue;
+        const float ws = kType == kCodes ? p.ws[(int64_t)j.g * p.N + f] : 1.f;
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const int row = 8 * k + 2 * c + v;
+            if (row >= j.n) continue;
+            float out = acc[k][2 * h + v];
+            if (kType == kCodes) out = out * ws * p.xs[j.row0 + row];
+            p.y[(j.row0 + row) * p.ldy + f] = (uint16_t)pack16(out, 0.f, p.fp16);
+          }
+      }
+      continue;
+    }
+    auto wait_sums = [&](uint64_t* bar, uint32_t parity) {
+      if (!ok) return;
+      ok = __all_sync(0xffffffffu, wait_nap<0, true>(bar, parity, limit, abort_flag));
+      if (!ok && lane == 0) {
+        record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedEpilogue);
+        *abort_flag = 1;
+      }
     };
-    if (wk == 1) {
+    if (t != first) wait_sums(&read, turn ^ 1);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int k = 0; k < NT; ++k)
+      for (int v = 0; v < 4; ++v) red[(8 * k + 2 * c + (v & 1)) * kPitch + warp * 16 + r + 8 * (v >> 1)] = acc[k][v];
+    __syncwarp();
+    if (lane < p.split) mbar_arrive_cluster(cluster_addr(&sums, lane));
+    wait_sums(&sums, turn);
+    if (ok) {
+      // two features of a row a thread
+#pragma unroll 1
+      for (int e = rank * 32 * kWarps + threadIdx.x; e < j.n * (kFeat / 2); e += p.split * 32 * kWarps) {
+        const int fl = e % (kFeat / 2) * 2, row = e / (kFeat / 2), f = j.f0 + fl;
+        if (f >= p.N) continue;   // N is a multiple of 8
+        float2 part[kMaxSplit];   // all on their way before the first sum
 #pragma unroll
-          for (int v = 0; v < 4; ++v) put(f0 + 16 * i + r + 8 * (v >> 1), 8 * k + 2 * c + (v & 1), acc[i][k][v]);
-    } else {
-      float* mine = red + warp * kVals + lane;
+        for (int s = 0; s < kMaxSplit; ++s)
+          if (s < p.split) part[s] = load_peer(red + row * kPitch + fl, s);
+        float2 v = part[0];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int k = 0; k < NT; ++k)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) mine[((i * NT + k) * 4 + v) * 32] = acc[i][k][v];
-      __syncthreads();
-      // feature fastest, so that a warp stores runs of a row; the parts of a sum in their order
-      for (int e = threadIdx.x; e < nfw * n * kFeat; e += 32 * kWarps) {
-        const int f = e % kFeat, wr = e / kFeat, w0 = nfw == 1 ? 0 : wr / n, row = wr - w0 * n;
-        const int at = ((f / 16 * NT + row / 8) * 4 + (f % 16 / 8) * 2 + row % 2) * 32 + f % 8 * 4 + row % 8 / 2;
-        const float* from = red + (w0 << p.wk_log2) * kVals + at;
-        float v = 0.f;
-        for (int k = 0; k < wk; ++k) v += from[k * kVals];
-        put((ft * nfw + w0) * kFeat + f, row, v);
+        for (int s = 1; s < kMaxSplit; ++s)
+          if (s < p.split) v = make_float2(v.x + part[s].x, v.y + part[s].y);
+        if (kType == kCodes) {
+          const float2 ws = __ldg(reinterpret_cast<const float2*>(p.ws + (int64_t)j.g * p.N + f));
+          const float xs = p.xs[j.row0 + row];
+          v = make_float2(v.x * ws.x * xs, v.y * ws.y * xs);
+        }
+        *reinterpret_cast<uint32_t*>(p.y + (j.row0 + row) * p.ldy + f) = pack16(v.x, v.y, p.fp16);
       }
-      __syncthreads();
     }
+    __syncwarp();
+    if (lane < p.split) mbar_arrive_cluster(cluster_addr(&read, lane));
   }
+  __syncwarp();
+  if (p.split > 1) cluster_sync();   // no block ends while another may read its sums or arrive at its barriers
 }
 
-template <int kType, int MT, int NT, int KC, int kBlocks>
-cudaError_t launch_stream(const Grouped& c, StreamParams p, int id, cudaStream_t s) {
-  constexpr int smem = kWarps * MT * NT * 128 * 4;
-  static_assert(smem + sizeof(GroupTab) <= 232448 / kBlocks - 1024, "shared memory of an SM");
-  const int64_t live = std::min<int64_t>(c.G, c.rows);
-  const int per = (c.N + 16 * MT - 1) / (16 * MT);   // features of a group, in warps
-  // warps that split K: enough for sixteen warps an SM
-  p.wk_log2 = 0;
-  while (p.wk_log2 < 3 && ((live * per) << p.wk_log2) < (int64_t)num_sms() * 16) ++p.wk_log2;
-  p.nf = ((per << p.wk_log2) + kWarps - 1) / kWarps;
-  const int64_t tiles = (c.rows / (8 * NT) + live) * p.nf;
+template <int kType, int NT, int kDepth, int kBlocks>
+cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, const void* W, int size, int id,
+                          cudaStream_t s) {
+  constexpr int smem = 1024 + kDepth * (kFeat + 8 * NT) * kCols + 8 * NT * kPitch * 4;
+  static_assert(smem + sizeof(GroupTab) + 256 <= 232448 / kBlocks - 1024, "shared memory of an SM");
+  auto fn = encode_fn();
+  const cuuint64_t row = (cuuint64_t)c.K * size;
+  const cuuint64_t wdims[3] = {row, (cuuint64_t)c.N, (cuuint64_t)c.G}, wstrides[2] = {row, row * c.N};
+  const cuuint64_t xdims[2] = {row, (cuuint64_t)c.rows}, xstrides[1] = {(cuuint64_t)c.ldi * size};
+  const cuuint32_t wbox[3] = {kCols, kFeat, 1}, xbox[2] = {kCols, 8 * NT}, es[3] = {1, 1, 1};
+  if (!fn ||
+      fn(&p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(W), wdims, wstrides, wbox, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+      fn(&p.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(x), xdims, xstrides, xbox, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  p.nst = (int)((row + kCols - 1) / kCols);
+  p.nf = (c.N + kFeat - 1) / kFeat;
+  // the tiles if the rows spread evenly over the groups; at most (live + c.rows / (8 NT)) nf
+  const int64_t live = std::min<int64_t>(c.G, c.rows), slots = kBlocks * (int64_t)num_sms();
+  const int64_t tiles = (live + (c.rows - live) / (8 * NT)) * p.nf;
+  p.split = 1;
+  while (p.split < kMaxSplit && 2 * p.split * tiles <= slots && 2 * p.split <= p.nst) p.split *= 2;
+  const int grid = p.split * (int)std::min<int64_t>((live + c.rows / (8 * NT)) * p.nf, slots / p.split);
+  auto kernel = stream_kernel<kType, NT, kDepth, kBlocks>;
   static SmemOnce once;
-  cudaError_t e = once.set(reinterpret_cast<const void*>(stream_kernel<kType, MT, NT, KC, kBlocks>), smem);
+  cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(32 * (kWarps + 1));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
   prof_mark(id, s, true);
-  stream_kernel<kType, MT, NT, KC, kBlocks>
-      <<<(int)std::min<int64_t>(tiles, kBlocks * (int64_t)num_sms()), 32 * kWarps, smem, s>>>(p);
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   prof_mark(id, s, false);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int kType>
-cudaError_t launch_type(const Grouped& c, const StreamParams& p, int id, cudaStream_t s) {
-  if (c.rows <= 8) return launch_stream<kType, 1, 1, 4, 3>(c, p, id, s);
-  if (c.rows <= 16 * (int64_t)c.G) return launch_stream<kType, 2, 4, 1, 2>(c, p, id, s);
-  return launch_stream<kType, 2, 8, 1, 1>(c, p, id, s);
+cudaError_t launch_type(const Grouped& c, StreamParams& p, const void* x, const void* W, int id, cudaStream_t s) {
+  constexpr int size = kType == kCodes ? 1 : 2;
+  return c.rows <= 8 ? launch_stream<kType, 1, 3, 3>(c, p, x, W, size, id, s)
+                     : launch_stream<kType, 4, 4, 2>(c, p, x, W, size, id, s);
 }
 
-StreamParams stream_params(const Grouped& c, const int32_t* begin, const int32_t* end, const void* x, const void* W,
-                           uint16_t* y, int size, Hdr* hdr) {
+StreamParams stream_params(const Grouped& c, const int32_t* begin, const int32_t* end, uint16_t* y, Hdr* hdr) {
   StreamParams p{};
   p.begin = begin;
   p.end = end;
-  p.x = static_cast<const uint8_t*>(x);
-  p.W = static_cast<const uint8_t*>(W);
   p.y = y;
   p.rows = c.rows;
-  p.ldx = c.ldi * size;
   p.ldy = c.ldo;
-  p.row_bytes = c.K * size;
   p.N = c.N;
   p.G = c.G;
   p.fp16 = c.fp16;
@@ -262,17 +359,17 @@ bool stream_eligible(const Grouped& c) { return c.rows <= 32 * (int64_t)c.G || c
 
 cudaError_t launch_stream_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
                              const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s) {
-  const StreamParams p = stream_params(c, begin, end, x, W, y, 2, hdr);
-  return c.fp16 ? launch_type<kFp16>(c, p, kKGroupedMm, s) : launch_type<kBf16>(c, p, kKGroupedMm, s);
+  StreamParams p = stream_params(c, begin, end, y, hdr);
+  return c.fp16 ? launch_type<kFp16>(c, p, x, W, kKGroupedMm, s) : launch_type<kBf16>(c, p, x, W, kKGroupedMm, s);
 }
 
 cudaError_t launch_stream_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,
                              const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr,
                              cudaStream_t s) {
-  StreamParams p = stream_params(c, begin, end, q, Wq, y, 1, hdr);
+  StreamParams p = stream_params(c, begin, end, y, hdr);
   p.xs = qs;
   p.ws = Ws;
-  return launch_type<kCodes>(c, p, kKGroupedI8, s);
+  return launch_type<kCodes>(c, p, q, Wq, kKGroupedI8, s);
 }
 
 }  // namespace moe
