@@ -59,15 +59,14 @@ constexpr uint32_t kEpiBox = 32 * 64;        // a staging box: 32 rows of 64 byt
 
 template <int kOp>
 struct Shape {
-  static constexpr int kDepth = kOp == kI8 ? 2 * kBK : kBK;   // K of a stage
-  static constexpr int kStages = kOp == kI8 ? 3 : 6;
-  static constexpr int kRing = kOp == kDw ? 5 : kStages;      // weight gradient: the last stage is set apart
-  static constexpr uint32_t kStageBytes = 2 * kHalf * (kDepth / kBK);
-  static constexpr int kTeams = 2, kTeam = 8;   // 8-bit integers: teams of warps that widen codes
+  static constexpr int kStages = kOp == kI8 ? 4 : 6;
+  static constexpr int kRing = kOp == kDw ? 5 : kStages;   // weight gradient: the last stage is set apart
+  static constexpr int kRaw = kOp == kI8 ? 2 : 0;          // 8-bit integers: stages of codes, two K blocks each,
+  static constexpr int kTeams = 4, kTeam = 4;              // and the teams of warps that widen them
   static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : (kOp == kDw ? 1 : 0);
   static constexpr int kThreads = 32 * (6 + kExtra);
   static constexpr uint32_t kEpi = kOp == kDw ? 4 * 2 * kEpiBox : 0;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kEpi + 512 + sizeof(GroupTab);
+  static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kEpi + 512 + sizeof(GroupTab);
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
@@ -77,9 +76,8 @@ struct Params {
   CUtensorMap out;            // weight gradient: dW in boxes
   const int32_t *begin, *end;
   void* y;
-  const int8_t *q, *wq;       // 8-bit integers: codes of the rows (ldq apart) and of the weights, and
-  const float *qs, *ws;       // the scales of the rows and of the output channels
-  int64_t rows, ldy, ldq;
+  const float *qs, *ws;       // scales of the rows and of the output channels (8-bit integers)
+  int64_t rows, ldy;
   int depth;                  // contraction length (rows times a weight)
   int width;                  // features of the output row; weight gradient: columns of dW (n_in)
   int M;                      // weight gradient: rows of dW (n_out)
@@ -166,7 +164,7 @@ struct Walk {
     if (kOp != kDw) {
       if (t >= ntiles) return false;
       j = row_job(p, s, t);
-      j.kits = (p.depth + Shape<kOp>::kDepth - 1) / Shape<kOp>::kDepth;
+      j.kits = (p.depth + kBK - 1) / kBK;
       t += step;
       return true;
     }
@@ -216,11 +214,16 @@ __device__ __forceinline__ void store_rows(const Params& p, const Job& j, int ra
     for (int i = 0; i < 16; ++i) {
       float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
       if (kOp == kI8) {
-        a = a * ws * __shfl_sync(0xffffffffu, qs, 2 * i);
-        b = b * ws * __shfl_sync(0xffffffffu, qs, 2 * i + 1);
+        a *= ws;
+        b *= ws;
       }
       const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-      w[i] = odd ? pack16(got, b, p.fp16) : pack16(a, got, p.fp16);
+      if (kOp == kI8) {   // this lane now has two features of row c + 2 i + odd
+        const float s = __shfl_sync(0xffffffffu, qs, 2 * i + odd);
+        w[i] = odd ? pack16(got * s, b * s, p.fp16) : pack16(a * s, got * s, p.fp16);
+      } else {
+        w[i] = odd ? pack16(got, b, p.fp16) : pack16(a, got, p.fp16);
+      }
     }
     const int left = live ? j.n - c - odd : 0;   // this lane's rows from c on
     uint16_t* at = out + (int64_t)c * p.ldy;
@@ -344,15 +347,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   using S = Shape<kOp>;
   constexpr int kStages = S::kStages;
   constexpr int kRing = S::kRing;
-  constexpr uint32_t kStage = S::kStageBytes;
+  constexpr uint32_t kStage = 2 * kHalf;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = smem;
-  uint8_t* boxes = stages + kStages * kStage;
+  uint8_t* raws = stages + kStages * kStage;
+  uint8_t* boxes = raws + S::kRaw * kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(boxes + S::kEpi);
   uint64_t* empty = full + 6;
   uint64_t* raw = empty + 6;
-  uint64_t* tfull = raw + 6;
+  uint64_t* rempty = raw + 6;
+  uint64_t* tfull = rempty + 6;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -364,9 +369,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
-      mbar_init(&full[s], kOp == kI8 || kOp == kDw ? 2 : 1);
+      mbar_init(&full[s], kOp == kI8 ? 2 * S::kTeam : (kOp == kDw ? 2 : 1));
       mbar_init(&empty[s], 1);
-      mbar_init(&raw[s], kOp == kI8 ? S::kTeam : 1);
+      mbar_init(&raw[s], 1);
+      mbar_init(&rempty[s], S::kTeams * S::kTeam);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -375,10 +381,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    if (kOp != kI8) {
-      tma_prefetch(&p.a);
-      for (int i = 0; i < (kOp == kDw ? 1 : kBoxes); ++i) tma_prefetch(&p.b[i]);
-    }
+    tma_prefetch(&p.a);
+    for (int i = 0; i < (kOp == kDw ? 1 : kBoxes); ++i) tma_prefetch(&p.b[i]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
@@ -410,22 +414,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       const int skip = pair == 0 ? *((volatile const int32_t*)&p.hdr->stall_fill_p1) - 1 : -1;
       uint32_t raw_used = 0, raw_next = 0;   // weight gradient, a bit per stage: own barrier used, next phase
       if constexpr (kOp == kI8) {
-        // tells the even CTA's MMA thread of every widened stage: one thread with nothing else in flight,
-        // because a release at cluster scope waits for all of a thread's memory operations
-        while (ok && walk.next(j)) {
-          for (int kit = 0; kit < j.kits; ++kit) {
-            if (!wait_nap<20>(&raw[slot], phase, limit, abort_flag)) {
+        while (ok && !*abort_flag && walk.next(j)) {
+          const int half = ((j.n + 31) / 32 * 32) / 2, bx = box_of(half);
+          for (int kit = 0; kit < (j.kits + 1) / 2; ++kit) {
+            if (!wait_nap<20>(&rempty[slot], phase ^ 1, limit, abort_flag)) {
               fail(kSiteGroupedProducer);
               ok = false;
               break;
             }
-            mbar_arrive_cluster(cluster_addr(&full[slot], 0));
-            if (++slot == kRing) {
+            if (uses != skip) {
+              uint8_t* st = raws + (size_t)slot * kStage;
+              mbar_arrive_expect_tx(&raw[slot], kHalf + (128u >> bx) * 128u);
+              tma_load_3d(st, &p.a, &raw[slot], kit * 2 * kBK, j.f0 + kBM * rank, j.g);
+              tma_load_2d(st + kHalf, &p.b[bx], &raw[slot], kit * 2 * kBK, j.row + half * rank);
+            }
+            ++uses;
+            if (++slot == S::kRaw) {
               slot = 0;
               phase ^= 1;
             }
           }
         }
+        drain_fills(raw, S::kRaw, slot, phase, uses, limit);
       } else {
         while (ok && !*abort_flag && walk.next(j)) {
           const int half = ((j.n + 31) / 32 * 32) / 2, bx = kOp == kDw ? 0 : box_of(half);
@@ -524,11 +534,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       while (ok && more && !*abort_flag) {
         const int kits = j.kits;
         const bool apart = kOp == kDw && early_last(j);
-        // steps of 16 in the last K block: the rest of it holds no rows of the group (weight gradient), or
-        // no codes (8-bit integers: the depth is a multiple of 16)
-        int last = S::kDepth / 16;
+        // steps of 16 in the last K block (weight gradient: the rest of it holds no rows of the group)
+        int last = kBK / 16;
         if (kOp == kDw && j.tail != 0) last = (j.tail + 15) / 16;
-        if (kOp == kI8) last = p.depth / 16 - (kits - 1) * (S::kDepth / 16);
         const int n = kOp == kDw ? kTile : (j.n + 31) / 32 * 32;
         const uint32_t idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(n >> 3) << 17);
         more = walk.next(j);   // the next job, worked out while this one's products run
@@ -550,11 +558,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
           tc_fence_after();
           const uint32_t sa = smem_u32(stages + (size_t)s * kStage);
 #pragma unroll
-          for (int kk = 0; kk < S::kDepth / 16; ++kk) {
-            if ((kOp == kDw || kOp == kI8) && kit == kits - 1 && kk >= last) break;
-            const uint32_t at = sa + (kk / 4) * 2 * kHalf;   // (8-bit integers: two blocks of 64)
-            const uint64_t da = kOp == kMm || kOp == kI8 ? sdesc_kmajor(at + kk % 4 * 32) : sdesc_mnmajor(at + kk * 2048, kBox);
-            const uint64_t db = kOp == kDw ? sdesc_mnmajor(at + kHalf + kk * 2048, kBox) : sdesc_kmajor(at + kHalf + kk % 4 * 32);
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            if (kOp == kDw && kit == kits - 1 && kk >= last) break;
+            const uint64_t da = kOp == kMm || kOp == kI8 ? sdesc_kmajor(sa + kk * 32) : sdesc_mnmajor(sa + kk * 2048, kBox);
+            const uint64_t db = kOp == kDw ? sdesc_mnmajor(sa + kHalf + kk * 2048, kBox) : sdesc_kmajor(sa + kHalf + kk * 32);
             umma_bf16_pair(dt, da, db, idesc, (kit | kk) != 0);
           }
           if (kOp == kI8) umma_commit_both(&empty[s]);
@@ -628,56 +635,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       slot = (slot + j.kits - (int)early_last(j)) % kRing;
     }
   } else if constexpr (kOp == kI8) {
-    // Widen: the teams take turns at the stages, 128 codes deep; a warp takes every eighth four rows (of
-    // the weight's 128, then of up to 128 token rows), a lane 16 codes of a row: an instruction reads
-    // whole 128-byte lines of four rows.  A lane's codes belong to one of the stage's two 64-deep
-    // blocks; the lanes of the second block store their halves in the other order, which with the
-    // 128-byte swizzle keeps the banks of each eight lanes distinct.  Rows past the last are read as the
-    // last one: nothing stores their products.
-    constexpr int kRows = 4;   // rows an instruction reads
-    constexpr int kPer = kBM / kRows / S::kTeam;
-    const int team = (warp - 6) / S::kTeam, w = (warp - 6) % S::kTeam;
-    const int r0 = w * kRows + (lane >> 3), second = (lane >> 2) & 1, cq = lane & 3;
-    const int skip = pair == 0 ? *((volatile const int32_t*)&p.hdr->stall_fill_p1) - 1 : -1;
-    uint8_t* const dst = stages + second * 2 * kHalf + r0 * 128;
-    const int o0 = ((2 * cq + second) ^ (r0 & 7)) << 4, o1 = ((2 * cq + 1 - second) ^ (r0 & 7)) << 4;
-    int fill = 0;
+    // Widen: the teams take turns at the K blocks (a raw stage holds two), each with a stage of its own; a
+    // warp takes every fourth octet of rows (of the weight's 128, then of up to 128 token rows), a lane a
+    // row and 16 of its codes: in the 128-byte swizzle the eight lanes of a phase touch distinct banks
+    // on both sides.  Four teams, because the arrival that the even CTA's MMA thread waits for (a release
+    // at cluster scope) takes about as long as a block's products: with two it was 1.3 times the time.
+    static_assert(kStages == S::kTeams, "a stage a team");
+    constexpr int kPer = kBM / 8 / S::kTeam;
+    const int team = (warp - 6) / S::kTeam, w = (warp - 6) % S::kTeam, r = lane & 7, cq = lane >> 3;
+    const uint32_t to = (w * 8 + r) * 128;
+    const uint32_t o0 = ((2 * cq) ^ r) << 4, o1 = ((2 * cq + 1) ^ r) << 4;
+    int block = 0, rblock = 0;   // K blocks and raw stages before this job
     bool ok = true;
     while (ok && walk.next(j)) {
       const int half = ((j.n + 31) / 32 * 32) / 2;
-      const int f = j.f0 + kBM * rank + r0, row = j.row + half * rank + r0;
-      const int8_t* wq = p.wq + (int64_t)j.g * p.width * p.depth;
-      for (int kit = 0; kit < j.kits; ++kit, ++fill) {
-        if (fill % S::kTeams != team) continue;
-        const int k = min(kit * S::kDepth + (lane & 7) * 16, p.depth - 16);
-        uint4 a[kPer], b[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          a[i] = __ldg(reinterpret_cast<const uint4*>(wq + (int64_t)min(f + i * kRows * S::kTeam, p.width - 1) * p.depth + k));
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if ((i * S::kTeam + w) * kRows < half)
-            b[i] = __ldg(reinterpret_cast<const uint4*>(
-                p.q + min((int64_t)row + i * kRows * S::kTeam, p.rows - 1) * p.ldq + k));
-        const int slot = fill % kRing;
-        ok = __all_sync(0xffffffffu, wait_nap<0>(&empty[slot], ((uint32_t)(fill / kRing) & 1u) ^ 1u, limit, abort_flag));
+      const int kits = j.kits, rkits = (kits + 1) / 2;
+      for (int rk = 0; rk < rkits; ++rk) {
+        // every warp waits for every raw stage and releases it: a barrier's phase must not pass a waiter by
+        const int rs = (rblock + rk) % S::kRaw;
+        const int kit = 2 * rk + ((team - block - 2 * rk) & (S::kTeams - 1));   // this team's next block
+        const bool mine = kit < min(2 * rk + 2, kits);
+        const int at = block + kit;
+        ok = wait_nap<0>(&raw[rs], (uint32_t)((rblock + rk) / S::kRaw) & 1u, limit, abort_flag) &&
+             (!mine || wait_nap<0>(&empty[team], ((uint32_t)(at / kStages) & 1u) ^ 1u, limit, abort_flag));
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           if (lane == 0) fail(kSiteGroupedStage);
           break;
         }
-        uint8_t* st = dst + (size_t)slot * kStage;
+        if (mine) {
+          const uint8_t* src = raws + (size_t)rs * kStage + to + ((((kit & 1) * 4 + cq) ^ r) << 4);
+          uint8_t* dst = stages + (size_t)team * kStage + to;
+          uint4 v[2 * kPer];
 #pragma unroll
-        for (int i = 0; i < 2 * kPer; ++i) {
-          if (i >= kPer && ((i - kPer) * S::kTeam + w) * kRows >= half) break;
-          const uint4 v = i < kPer ? a[i % kPer] : b[i % kPer];
-          uint8_t* d = st + (i < kPer ? 0 : kHalf) + (i % kPer) * kRows * S::kTeam * 128;
-          *reinterpret_cast<uint4*>(d + o0) = second ? widen(v.z, v.w) : widen(v.x, v.y);
-          *reinterpret_cast<uint4*>(d + o1) = second ? widen(v.x, v.y) : widen(v.z, v.w);
+          for (int i = 0; i < 2 * kPer; ++i)
+            if (i < kPer || ((i - kPer) * S::kTeam + w) * 8 < half)
+              v[i] = *reinterpret_cast<const uint4*>(src + i * S::kTeam * 1024);
+#pragma unroll
+          for (int i = 0; i < 2 * kPer; ++i) {
+            if (i >= kPer && ((i - kPer) * S::kTeam + w) * 8 >= half) break;
+            uint8_t* d = dst + i * S::kTeam * 1024;
+            *reinterpret_cast<uint4*>(d + o0) = widen(v[i].x, v[i].y);
+            *reinterpret_cast<uint4*>(d + o1) = widen(v[i].z, v[i].w);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && fill != skip) mbar_arrive(&raw[slot]);
+        if (lane == 0) mbar_arrive(&rempty[rs]);
+        if (mine && lane == 0) mbar_arrive_cluster(cluster_addr(&full[team], 0));   // (last: it takes longest)
       }
+      block += kits;
+      rblock += rkits;
     }
   }
   tc_fence_before();
@@ -708,23 +716,25 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base
 }
 
 constexpr CUtensorMapDataType k16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;   // (fp16 values too: bits are copied)
+constexpr CUtensorMapDataType k8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B, kSw64 = CU_TENSOR_MAP_SWIZZLE_64B;
 
-// Rows [rows, width] as K-major boxes of 64 columns x 128, 64 and 32 rows.
-bool map_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t width, uint64_t ld) {
-  const cuuint64_t dims[2] = {width, rows}, strides[1] = {ld * 2};
+// Rows [rows, width], 16-bit or codes, as K-major boxes of 128 bytes x 128, 64 and 32 rows.
+bool map_rows(CUtensorMap* m, const void* base, bool codes, uint64_t rows, uint64_t width, uint64_t ld) {
+  const cuuint64_t dims[2] = {width, rows}, strides[1] = {ld * (codes ? 1 : 2)};
   for (int i = 0; i < kBoxes; ++i) {
-    const cuuint32_t box[2] = {64, 128u >> i};
-    if (!encode(&m[i], k16, 2, base, dims, strides, box, kSw128)) return false;
+    const cuuint32_t box[2] = {codes ? 128u : 64u, 128u >> i};
+    if (!encode(&m[i], codes ? k8 : k16, 2, base, dims, strides, box, kSw128)) return false;
   }
   return true;
 }
 
-// Weights [G, N, K], K-major: boxes of 64 columns x 128 rows.
-bool map_weight(CUtensorMap* m, const void* base, uint64_t G, uint64_t N, uint64_t K) {
-  const cuuint64_t dims[3] = {K, N, G}, strides[2] = {K * 2, K * N * 2};
-  const cuuint32_t box[3] = {64, 128, 1};
-  return encode(m, k16, 3, base, dims, strides, box, kSw128);
+// Weights [G, N, K], K-major: boxes of 128 bytes x 128 rows.
+bool map_weight(CUtensorMap* m, const void* base, bool codes, uint64_t G, uint64_t N, uint64_t K) {
+  const uint64_t size = codes ? 1 : 2;
+  const cuuint64_t dims[3] = {K, N, G}, strides[2] = {K * size, K * N * size};
+  const cuuint32_t box[3] = {codes ? 128u : 64u, 128, 1};
+  return encode(m, codes ? k8 : k16, 3, base, dims, strides, box, kSw128);
 }
 
 // Weights [G, N, K] read MN-major (K contiguous): 64 x 64 boxes, two at a time when K allows (the columns
@@ -808,7 +818,7 @@ cudaError_t launch_grouped_mm(const Grouped& c, const int32_t* begin, const int3
   if (c.rows == 0) return cudaSuccess;
   if (stream_eligible(c)) return launch_stream_mm(c, begin, end, x, W, y, hdr, s);
   Params p = params_of(c, begin, end, hdr);
-  if (!map_weight(&p.a, W, c.G, c.N, c.K) || !map_rows(p.b, x, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
+  if (!map_weight(&p.a, W, false, c.G, c.N, c.K) || !map_rows(p.b, x, false, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
   p.y = y;
   p.ldy = c.ldo;
   p.depth = c.K;
@@ -824,7 +834,7 @@ cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int3
   if (c.rows == 0) return cudaSuccess;
   Params p = params_of(c, begin, end, hdr);
   p.wide_a = c.K % 64 == 0;
-  if (!map_weight_mn(&p.a, W, c.G, c.N, c.K, p.wide_a) || !map_rows(p.b, dy, c.rows, c.N, c.ldo))
+  if (!map_weight_mn(&p.a, W, c.G, c.N, c.K, p.wide_a) || !map_rows(p.b, dy, false, c.rows, c.N, c.ldo))
     return cudaErrorInvalidValue;
   p.y = dx;
   p.ldy = c.ldi;
@@ -864,11 +874,9 @@ cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int3
   if (c.rows == 0) return cudaSuccess;
   if (stream_eligible(c)) return launch_stream_i8(c, begin, end, q, qs, Wq, Ws, y, hdr, s);
   Params p = params_of(c, begin, end, hdr);
+  if (!map_weight(&p.a, Wq, true, c.G, c.N, c.K) || !map_rows(p.b, q, true, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
   p.y = y;
   p.ldy = c.ldo;
-  p.q = q;
-  p.wq = Wq;
-  p.ldq = c.ldi;
   p.qs = qs;
   p.ws = Ws;
   p.depth = c.K;
