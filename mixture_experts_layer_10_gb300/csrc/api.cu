@@ -322,9 +322,11 @@ moe_status_t make_grouped(const moe_grouped_t* in, Grouped* c) {
   return MOE_OK;
 }
 
-moe_status_t get_grouped_ws(void* ws, size_t ws_bytes, Hdr** hdr) {
+size_t grouped_ws_bytes(const Grouped& c) { return sizeof(Hdr) + (size_t)c.G * kGroupMapBytes; }
+
+moe_status_t get_grouped_ws(const Grouped& c, void* ws, size_t ws_bytes, Hdr** hdr) {
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < sizeof(Hdr)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < grouped_ws_bytes(c)) return MOE_ERR_WORKSPACE;
   *hdr = static_cast<Hdr*>(ws);
   return MOE_OK;
 }
@@ -993,7 +995,7 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_t* cfg, size_t* ws_byt
   Grouped c;
   MOE_TRY(make_grouped(cfg, &c));
   MOE_NEED(ws_bytes != nullptr);
-  *ws_bytes = sizeof(Hdr);
+  *ws_bytes = grouped_ws_bytes(c);
   return MOE_OK;
 }
 
@@ -1001,7 +1003,7 @@ moe_status_t moe_grouped_workspace_init(const moe_grouped_t* cfg, void* ws, size
   Grouped c;
   Hdr* hdr = nullptr;
   MOE_TRY(make_grouped(cfg, &c));
-  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(get_grouped_ws(c, ws, ws_bytes, &hdr));
   MOE_CUDA(cudaMemsetAsync(hdr, 0, sizeof(Hdr), stream));
   return MOE_OK;
 }
@@ -1025,7 +1027,7 @@ moe_status_t moe_grouped_mm(const moe_grouped_t* cfg, const int32_t* row_begin, 
   MOE_TRY(make_grouped(cfg, &c));
   MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
   MOE_NEED(W && aligned16(W) && (c.rows == 0 || (x && y)) && aligned16(x) && aligned16(y));
-  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(get_grouped_ws(c, ws, ws_bytes, &hdr));
   MOE_TRY(check_device());
   MOE_CUDA(launch_grouped_mm(c, row_begin, row_end, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(W),
                              static_cast<uint16_t*>(y), hdr, stream));
@@ -1040,7 +1042,7 @@ moe_status_t moe_grouped_mm_dx(const moe_grouped_t* cfg, const int32_t* row_begi
   MOE_TRY(make_grouped(cfg, &c));
   MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
   MOE_NEED(W && aligned16(W) && (c.rows == 0 || (dy && dx)) && aligned16(dy) && aligned16(dx));
-  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(get_grouped_ws(c, ws, ws_bytes, &hdr));
   MOE_TRY(check_device());
   MOE_CUDA(launch_grouped_dx(c, row_begin, row_end, static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(W),
                              static_cast<uint16_t*>(dx), hdr, stream));
@@ -1055,10 +1057,10 @@ moe_status_t moe_grouped_mm_dw(const moe_grouped_t* cfg, const int32_t* row_begi
   MOE_TRY(make_grouped(cfg, &c));
   MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
   MOE_NEED(dW && aligned16(dW) && (c.rows == 0 || (dy && x)) && aligned16(dy) && aligned16(x));
-  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(get_grouped_ws(c, ws, ws_bytes, &hdr));
   MOE_TRY(check_device());
   MOE_CUDA(launch_grouped_dw(c, row_begin, row_end, static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
-                             dW, hdr, stream));
+                             dW, hdr, hdr + 1, stream));
   return MOE_OK;
 }
 
@@ -1082,7 +1084,7 @@ moe_status_t moe_grouped_mm_i8(const moe_grouped_t* cfg, const int32_t* row_begi
   MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
   MOE_NEED(Wq && W_scale && aligned16(Wq) && aligned16(W_scale) && (c.rows == 0 || (codes && scales && y)) &&
            aligned16(codes) && aligned16(scales) && aligned16(y));
-  MOE_TRY(get_grouped_ws(ws, ws_bytes, &hdr));
+  MOE_TRY(get_grouped_ws(c, ws, ws_bytes, &hdr));
   MOE_TRY(check_device());
   MOE_CUDA(launch_grouped_i8(c, row_begin, row_end, codes, scales, Wq, W_scale, static_cast<uint16_t*>(y), hdr,
                              stream));

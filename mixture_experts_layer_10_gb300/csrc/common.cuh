@@ -339,12 +339,13 @@ struct Grouped {           // validated description
   bool fp16, dw_fp32, acc;
 };
 constexpr int kMaxGroups = 1024;
+constexpr size_t kGroupMapBytes = 256;   // workspace of a group, after the header: two tensor maps
 cudaError_t launch_grouped_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
                               const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s);
 cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* dy,
                               const uint16_t* W, uint16_t* dx, Hdr* hdr, cudaStream_t s);
 cudaError_t launch_grouped_dw(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* dy,
-                              const uint16_t* x, void* dW, Hdr* hdr, cudaStream_t s);
+                              const uint16_t* x, void* dW, Hdr* hdr, void* maps, cudaStream_t s);
 cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,
                               const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr,
                               cudaStream_t s);

@@ -10,9 +10,7 @@
 //   warp 0      TMA producer: operand tiles into a ring of shared-memory stages (64 deep in K)
 //   warp 1      MMA issuer (the even CTA's one thread)
 //   warps 2-5   epilogue: tcgen05.ld of the accumulator, scales, rounding, stores
-//   warps 6..   8-bit integers: twelve warps that fetch the codes and widen them to fp16 (below), in the
-//               producer's place;
-//               weight gradient: one warp that clears the rows past the end of a group
+//   warps 6-21  8-bit integers: widen the codes to fp16 (below)
 //
 // Rows times a weight.  The weight's 256 features are the M side of the tile and up to 256 rows of one
 // group its N side, so a group's ragged end costs a narrower product (N in steps of 32) rather than
@@ -22,10 +20,11 @@
 // so a warp stores 32 features of a row at a time.
 //
 // Weight gradient.  M = 256 columns of dy, N = 256 columns of x, K = the group's rows, both operands
-// MN-major.  Here rows past the end of the group would enter the sums, so in a group's last K block
-// both CTAs clear those rows of both operands in shared memory before the product.  With dW in fp32 the
-// rows go in runs of kRun (an accumulator loses up to one unit of its last place at each step of 16
-// rows, which a long contraction would let grow past fp32's own rounding); the runs add up in dW, in
+// MN-major.  Here rows past the end of the group would enter the sums, so every group has tensor maps of
+// its own whose rows end where the group does (written by a small kernel before: group_maps_kernel), and
+// the copies fill the rest of its last K block with zeros.  With dW in
+// fp32 the rows go in runs of kRun (an accumulator loses up to one unit of its last place at each step of
+// 16 rows, which a long contraction would let grow past fp32's own rounding); the runs add up in dW, in
 // row order, by reducing bulk stores of the same warp.
 //
 // 8-bit integers.  sm_103a has no integer product at tensor rates, but every code is exact in fp16 and a
@@ -60,10 +59,9 @@ constexpr uint32_t kEpiBox = 32 * 64;        // a staging box: 32 rows of 64 byt
 template <int kOp>
 struct Shape {
   static constexpr int kStages = kOp == kI8 ? 4 : 6;
-  static constexpr int kRing = kOp == kDw ? 5 : kStages;   // weight gradient: the last stage is set apart
   static constexpr int kRaw = kOp == kI8 ? 2 : 0;          // 8-bit integers: stages of codes, two K blocks each,
   static constexpr int kTeams = 4, kTeam = 4;              // and the teams of warps that widen them
-  static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : (kOp == kDw ? 1 : 0);
+  static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : 0;
   static constexpr int kThreads = 32 * (6 + kExtra);
   static constexpr uint32_t kEpi = kOp == kDw ? 4 * 2 * kEpiBox : 0;
   static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kEpi + 512 + sizeof(GroupTab);
@@ -74,6 +72,7 @@ struct Params {
   CUtensorMap a;              // M side: the weight, or dy (weight gradient)
   CUtensorMap b[kBoxes];      // N side: the rows in boxes of 128, 64, 32; or x in b[0] (weight gradient)
   CUtensorMap out;            // weight gradient: dW in boxes
+  const CUtensorMap* maps;    // weight gradient: every group's a and b[0]
   const int32_t *begin, *end;
   void* y;
   const float *qs, *ws;       // scales of the rows and of the output channels (8-bit integers)
@@ -92,7 +91,6 @@ struct Params {
 struct Job {
   int g, row, n, f0;   // rows times a weight: first row, rows, first feature
   int m0, kits, run;   // weight gradient: first dW row, K blocks of the run, its number
-  int tail;            // rows of the run's last K block that belong to the group (0: all of them)
 };
 
 // Rows times a weight: tile t -> group, row tile, feature tile.  Groups in order; within a group,
@@ -141,15 +139,11 @@ __device__ __forceinline__ Job dw_job(const Params& p, const GroupTab& s, int t,
   j.row = s.begin[j.g] + from;
   j.n = p.dw_fp32 ? min(kRun, n - from) : n;
   j.kits = (j.n + kBK - 1) / kBK;
-  j.tail = j.n % kBK;
   return j;
 }
 
 // The rows' box for a half of n rows: 0 (128 rows), 1 (64) or 2 (32).
 __device__ __forceinline__ int box_of(int half) { return half > 64 ? 0 : (half > 32 ? 1 : 2); }
-
-// Whether the run's last K block takes the stage set apart (below).
-__device__ __forceinline__ bool early_last(const Job& j) { return j.tail % 16 != 0 && j.kits >= 4; }
 
 // One pair's walk over its tiles, the same in every role of both CTAs: rows times a weight has one job a
 // tile, the weight gradient one a run of rows.
@@ -313,6 +307,11 @@ __device__ __forceinline__ void store_zero(const Params& p, const Job& j, int ra
   }
 }
 
+// Before the first copy by a tensor map that an earlier kernel wrote.
+__device__ __forceinline__ void fence_map(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Arrive once on the mbarrier at this shared-memory offset in both CTAs when every pair MMA this thread
 // issued so far has completed.
 __device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
@@ -323,22 +322,15 @@ __device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
       : "memory");
 }
 
-// The same for a whole warp: lane 0 polls.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = wait_nap<20>(bar, parity, limit_ns, abort);
-  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-}
-
 // Barriers (the same offsets in both CTAs; who uses which copy):
-//   full[s]     even CTA: the stage's operands of both CTAs are in place (TMA bytes; 8-bit integers, and
-//               a cleared K block: an arrival from each CTA)
+//   full[s]     even CTA: the stage's operands of both CTAs are in place (TMA bytes; 8-bit integers: the
+//               warps that widened them)
 //   empty[s]    stage free: committed to the even CTA, whose producer forwards it to the odd one when it
 //               refills the stage (8-bit integers: committed to both, the widening warps wait)
 //   tfull[a]    each CTA: accumulator a is complete
 //   tempty[a]   even CTA: both CTAs' epilogues have read it
-//   raw[s]      own CTA: bytes of a K block that needs clearing (weight gradient); codes widened to the
-//               stage (8-bit integers)
+//   raw[s]      8-bit integers, own CTA: the bytes of a raw stage
+//   rempty[s]   8-bit integers, own CTA: every widening warp has passed it
 // Every wait is bounded; whatever happens, both CTAs meet at the last cluster barrier before TMEM is
 // freed, with their own copies landed.
 template <int kOp>
@@ -346,7 +338,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     grouped_kernel(const __grid_constant__ Params p) {
   using S = Shape<kOp>;
   constexpr int kStages = S::kStages;
-  constexpr int kRing = S::kRing;
   constexpr uint32_t kStage = 2 * kHalf;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -369,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
-      mbar_init(&full[s], kOp == kI8 ? 2 * S::kTeam : (kOp == kDw ? 2 : 1));
+      mbar_init(&full[s], kOp == kI8 ? 2 * S::kTeam : 1);
       mbar_init(&empty[s], 1);
       mbar_init(&raw[s], 1);
       mbar_init(&rempty[s], S::kTeams * S::kTeam);
@@ -381,8 +372,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch(&p.a);
-    for (int i = 0; i < (kOp == kDw ? 1 : kBoxes); ++i) tma_prefetch(&p.b[i]);
+    if (kOp != kDw) {
+      tma_prefetch(&p.a);
+      for (int i = 0; i < kBoxes; ++i) tma_prefetch(&p.b[i]);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
@@ -407,12 +400,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   if (warp == 0) {
     if (lane == 0) {
       int slot = 0, uses = 0;
-      uint32_t phase = 0, phase_apart = 0;   // ring; the stage set apart
-      int uses_apart = 0;
+      uint32_t phase = 0;
+      int mapped = -1;   // weight gradient: the group whose maps are in use
       bool ok = true;
       // test hook: the first pair skips one fill, so that the wait for it runs out
       const int skip = pair == 0 ? *((volatile const int32_t*)&p.hdr->stall_fill_p1) - 1 : -1;
-      uint32_t raw_used = 0, raw_next = 0;   // weight gradient, a bit per stage: own barrier used, next phase
       if constexpr (kOp == kI8) {
         while (ok && !*abort_flag && walk.next(j)) {
           const int half = ((j.n + 31) / 32 * 32) / 2, bx = box_of(half);
@@ -440,103 +432,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
         while (ok && !*abort_flag && walk.next(j)) {
           const int half = ((j.n + 31) / 32 * 32) / 2, bx = kOp == kDw ? 0 : box_of(half);
           const uint32_t bytes = kHalf + (kOp == kDw ? kHalf : (128u >> bx) * 128u);
-          // K block kit to stage s, which is free
-          auto fill = [&](int kit, int s) {
-            uint8_t* st = stages + (size_t)s * kStage;
-            if constexpr (kOp == kDw) {
-              // a K block that needs clearing lands on this CTA's own barrier, for its clearing warp
-              const bool clear = j.tail % 16 != 0 && kit == j.kits - 1;
-              uint32_t bar = cluster_addr(&full[s], 0);
-              if (clear) {
-                mbar_arrive_expect_tx(&raw[s], bytes);
-                bar = cluster_addr(&raw[s], (uint32_t)rank);
-                raw_used |= 1u << s;
-                raw_next ^= 1u << s;
-              } else if (rank == 0) {
-                mbar_arrive_expect_tx(&full[s], 2 * bytes);
-                mbar_arrive(&full[s]);
-              }
-              const int row = j.row + kit * kBK, ca = j.m0 + kBM * rank, cb = j.f0 + kBM * rank;
-              if (p.wide_a) {
-                tma_load_3d_pair(st, &p.a, bar, 0, row, ca / 64);
-              } else {
-                tma_load_2d_pair(st, &p.a, bar, ca, row);
-                tma_load_2d_pair(st + kBox, &p.a, bar, ca + 64, row);
-              }
-              if (p.wide_b) {
-                tma_load_3d_pair(st + kHalf, &p.b[0], bar, 0, row, cb / 64);
-              } else {
-                tma_load_2d_pair(st + kHalf, &p.b[0], bar, cb, row);
-                tma_load_2d_pair(st + kHalf + kBox, &p.b[0], bar, cb + 64, row);
-              }
-            } else {
-              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-              const uint32_t bar = cluster_addr(&full[s], 0);
-              const int f = j.f0 + kBM * rank;
-              if (kOp == kMm) {
-                tma_load_3d_pair(st, &p.a, bar, kit * kBK, f, j.g);
-              } else if (p.wide_a) {
-                tma_load_4d_pair(st, &p.a, bar, 0, kit * kBK, f / 64, j.g);
-              } else {
-                tma_load_3d_pair(st, &p.a, bar, f, kit * kBK, j.g);
-                tma_load_3d_pair(st + kBox, &p.a, bar, f + 64, kit * kBK, j.g);
-              }
-              tma_load_2d_pair(st + kHalf, &p.b[bx], bar, kit * kBK, j.row + half * rank);
+          const CUtensorMap* ma = &p.a;
+          const CUtensorMap* mb = &p.b[bx];
+          if constexpr (kOp == kDw) {
+            ma = p.maps + 2 * j.g;
+            mb = ma + 1;
+            if (j.g != mapped && j.kits > 0) {
+              fence_map(ma);
+              fence_map(mb);
+              mapped = j.g;
             }
-          };
-          const bool apart = kOp == kDw && early_last(j);
-          auto fill_apart = [&] {
-            fill(j.kits - 1, kRing);
-            if (rank == 0 && uses_apart > 0) mbar_arrive_cluster_relaxed(cluster_addr(&empty[kRing], 1));
-            ++uses_apart;
-            phase_apart ^= 1;
-          };
-          bool pending = apart;
-          for (int kit = 0; kit < j.kits - (int)apart; ++kit) {
-            if (pending && mbar_try_wait(&empty[kRing], phase_apart ^ 1)) {
-              fill_apart();
-              pending = false;
-            }
+          }
+          for (int kit = 0; kit < j.kits; ++kit) {
             if (!wait_nap<20>(&empty[slot], phase ^ 1, limit, abort_flag)) {
               fail(kSiteGroupedProducer);
               ok = false;
               break;
             }
-            if (uses != skip) fill(kit, slot);
-            if (rank == 0 && uses >= kRing) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 1));
+            if (uses != skip) {
+              uint8_t* st = stages + (size_t)slot * kStage;
+              if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * bytes);
+              const uint32_t bar = cluster_addr(&full[slot], 0);
+              if constexpr (kOp == kDw) {
+                const int row = j.row + kit * kBK, ca = j.m0 + kBM * rank, cb = j.f0 + kBM * rank;
+                if (p.wide_a) {
+                  tma_load_3d_pair(st, ma, bar, 0, row, ca / 64);
+                } else {
+                  tma_load_2d_pair(st, ma, bar, ca, row);
+                  tma_load_2d_pair(st + kBox, ma, bar, ca + 64, row);
+                }
+                if (p.wide_b) {
+                  tma_load_3d_pair(st + kHalf, mb, bar, 0, row, cb / 64);
+                } else {
+                  tma_load_2d_pair(st + kHalf, mb, bar, cb, row);
+                  tma_load_2d_pair(st + kHalf + kBox, mb, bar, cb + 64, row);
+                }
+              } else {
+                const int f = j.f0 + kBM * rank;
+                if (kOp == kMm) {
+                  tma_load_3d_pair(st, ma, bar, kit * kBK, f, j.g);
+                } else if (p.wide_a) {
+                  tma_load_4d_pair(st, ma, bar, 0, kit * kBK, f / 64, j.g);
+                } else {
+                  tma_load_3d_pair(st, ma, bar, f, kit * kBK, j.g);
+                  tma_load_3d_pair(st + kBox, ma, bar, f + 64, kit * kBK, j.g);
+                }
+                tma_load_2d_pair(st + kHalf, mb, bar, kit * kBK, j.row + half * rank);
+              }
+            }
+            if (rank == 0 && uses >= kStages) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 1));
             ++uses;
-            if (++slot == kRing) {
+            if (++slot == kStages) {
               slot = 0;
               phase ^= 1;
             }
           }
-          if (ok && pending) {
-            ok = wait_nap<20>(&empty[kRing], phase_apart ^ 1, limit, abort_flag);
-            if (ok) fill_apart();
-            else fail(kSiteGroupedProducer);
-          }
         }
         // every load of the pair lands before either CTA's shared memory is released: the even CTA's
-        // full barriers complete after both CTAs' bytes, and the odd CTA waits at the cluster barrier
-        if (rank == 0) {
-          drain_fills(full, kRing, slot, phase, uses, limit);
-          if (uses_apart > 0) mbar_wait_drain(&full[kRing], phase_apart ^ 1, limit);
-        }
-        for (int s = 0; s < kStages; ++s)
-          if ((raw_used >> s) & 1) mbar_wait_drain(&raw[s], ((raw_next >> s) & 1) ^ 1u, limit);
+        // full barriers count both CTAs' bytes, and the odd CTA waits at the cluster barrier
+        if (rank == 0) drain_fills(full, kStages, slot, phase, uses, limit);
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       int slot = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0, phase_apart = 0;
+      uint32_t phase = 0, acc_phase = 0;
       bool ok = true, more = walk.next(j);
       while (ok && more && !*abort_flag) {
         const int kits = j.kits;
-        const bool apart = kOp == kDw && early_last(j);
-        // steps of 16 in the last K block (weight gradient: the rest of it holds no rows of the group)
-        int last = kBK / 16;
-        if (kOp == kDw && j.tail != 0) last = (j.tail + 15) / 16;
         const int n = kOp == kDw ? kTile : (j.n + 31) / 32 * 32;
         const uint32_t idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(n >> 3) << 17);
         more = walk.next(j);   // the next job, worked out while this one's products run
@@ -548,27 +511,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
         }
         tc_fence_after();
         for (int kit = 0; kit < kits; ++kit) {
-          const bool set_apart = apart && kit == kits - 1;
-          const int s = set_apart ? kRing : slot;
-          if (!wait_nap<20, kOp == kI8 || kOp == kDw>(&full[s], set_apart ? phase_apart : phase, limit, abort_flag)) {
+          if (!wait_nap<20, kOp == kI8>(&full[slot], phase, limit, abort_flag)) {
             fail(kSiteGroupedMma);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(stages + (size_t)s * kStage);
+          const uint32_t sa = smem_u32(stages + (size_t)slot * kStage);
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk) {
-            if (kOp == kDw && kit == kits - 1 && kk >= last) break;
             const uint64_t da = kOp == kMm || kOp == kI8 ? sdesc_kmajor(sa + kk * 32) : sdesc_mnmajor(sa + kk * 2048, kBox);
             const uint64_t db = kOp == kDw ? sdesc_mnmajor(sa + kHalf + kk * 2048, kBox) : sdesc_kmajor(sa + kHalf + kk * 32);
             umma_bf16_pair(dt, da, db, idesc, (kit | kk) != 0);
           }
-          if (kOp == kI8) umma_commit_both(&empty[s]);
-          else umma_commit_pair(smem_u32(&empty[s]));
-          if (set_apart) {
-            phase_apart ^= 1;
-          } else if (++slot == kRing) {
+          if (kOp == kI8) umma_commit_both(&empty[slot]);
+          else umma_commit_pair(smem_u32(&empty[slot]));
+          if (++slot == kStages) {
             slot = 0;
             phase ^= 1;
           }
@@ -611,29 +569,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       }
     }
     if (kOp == kDw && lane == 0) bulk_wait_all();   // this warp's output stores have landed
-  } else if constexpr (kOp == kDw) {
-    // the rows past the end of the group in its last step of 16 rows, in both operands' boxes of this CTA
-    int slot = 0;
-    uint32_t raw_phase = 0;   // a bit per stage: only cleared blocks use these barriers
-    bool ok = true;
-    while (ok && walk.next(j)) {
-      const int from = j.tail, to = (j.tail + 15) / 16 * 16;
-      if (from != to) {
-        const int s = early_last(j) ? kRing : (slot + j.kits - 1) % kRing;
-        ok = wait_warp(&raw[s], (raw_phase >> s) & 1, limit, abort_flag);
-        if (!ok) {
-          if (lane == 0) fail(kSiteGroupedStage);
-          break;
-        }
-        raw_phase ^= 1u << s;
-        uint8_t* at = stages + (size_t)s * kStage + (lane >> 3) * kBox + (lane & 7) * 16;   // eight lanes a box
-        for (int r = from; r < to; ++r) *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[s], 0));
-      }
-      slot = (slot + j.kits - (int)early_last(j)) % kRing;
-    }
   } else if constexpr (kOp == kI8) {
     // Widen: the teams take turns at the K blocks (a raw stage holds two), each with a stage of its own; a
     // warp takes every fourth octet of rows (of the weight's 128, then of up to 128 token rows), a lane a
@@ -695,6 +630,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }
+}
+
+// The maps of every group's rows of dy and x for the weight gradient: those of all rows (dimension 1
+// counts rows in both forms), ending at the group's end.  A block a group, a warp a map.
+__global__ void __launch_bounds__(64) group_maps_kernel(const __grid_constant__ CUtensorMap a,
+                                                        const __grid_constant__ CUtensorMap b, const int32_t* end,
+                                                        int64_t rows, CUtensorMap* maps) {
+  __shared__ __align__(128) CUtensorMap map[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.x;
+  reinterpret_cast<uint32_t*>(&map[warp])[lane] = reinterpret_cast<const uint32_t*>(warp == 0 ? &a : &b)[lane];
+  __syncwarp();
+  if (lane == 0) {
+    const int64_t to = end[g];   // (whatever it holds, the map stays within the tensor)
+    const uint32_t dim = (uint32_t)(to < 1 ? 1 : (to > rows ? rows : to));
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_u32(&map[warp])),
+                 "r"(dim)
+                 : "memory");
+  }
+  __syncwarp();
+  asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+                   reinterpret_cast<uint64_t>(maps + 2 * g + warp)),
+               "r"(smem_u32(&map[warp]))
+               : "memory");
 }
 
 __global__ void segments_kernel(const Tables* tabs, int G, int32_t* begin, int32_t* end) {
@@ -847,16 +805,19 @@ cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int3
 }
 
 cudaError_t launch_grouped_dw(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* dy,
-                              const uint16_t* x, void* dW, Hdr* hdr, cudaStream_t s) {
+                              const uint16_t* x, void* dW, Hdr* hdr, void* maps, cudaStream_t s) {
   Params p = params_of(c, begin, end, hdr);
   p.wide_a = c.N % 64 == 0;
   p.wide_b = c.K % 64 == 0;
   if (!map_dw(&p.out, dW, c.G, c.N, c.K, c.dw_fp32)) return cudaErrorInvalidValue;
-  // without rows every tile is a zero tile and the operands' maps go unused
-  if (c.rows > 0 && (!map_rows_mn(&p.a, dy, c.rows, c.N, c.ldo, p.wide_a) ||
-                     !map_rows_mn(&p.b[0], x, c.rows, c.K, c.ldi, p.wide_b)))
-    return cudaErrorInvalidValue;
-  if (c.rows == 0) p.a = p.b[0] = p.out;
+  p.maps = static_cast<const CUtensorMap*>(maps);
+  if (c.rows > 0) {   // (without rows every tile is a zero tile)
+    if (!map_rows_mn(&p.a, dy, c.rows, c.N, c.ldo, p.wide_a) || !map_rows_mn(&p.b[0], x, c.rows, c.K, c.ldi, p.wide_b))
+      return cudaErrorInvalidValue;
+    group_maps_kernel<<<c.G, 64, 0, s>>>(p.a, p.b[0], end, c.rows, static_cast<CUtensorMap*>(maps));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   p.y = dW;
   p.M = c.N;
   p.width = c.K;
