@@ -19,13 +19,14 @@
 // their own, which nothing stores.  The accumulator holds a feature per TMEM lane and a row per column,
 // so a warp stores 32 features of a row at a time.
 //
-// Weight gradient.  M = 256 columns of dy, N = 256 columns of x, K = the group's rows, both operands
-// MN-major.  Here rows past the end of the group would enter the sums, so every group has tensor maps of
-// its own whose rows end where the group does (written by a small kernel before: group_maps_kernel), and
-// the copies fill the rest of its last K block with zeros.  With dW in
+// Weight gradient.  M = 256 columns of x, N = 256 columns of dy, K = the group's rows, both operands
+// MN-major; so here too the accumulator holds a column of dW per TMEM lane and a row per column, and a warp
+// stores runs of a row (128 bytes of fp32).  Rows past the end of the group would enter the sums, so
+// every group has tensor maps of its own whose rows end where the group does (written by a small kernel
+// before: group_maps_kernel), and the copies fill the rest of its last K block with zeros.  With dW in
 // fp32 the rows go in runs of kRun (an accumulator loses up to one unit of its last place at each step of
-// 16 rows, which a long contraction would let grow past fp32's own rounding); the runs add up in dW, in
-// row order, by reducing bulk stores of the same warp.
+// 16 rows, which a long contraction would let grow past fp32's own rounding); every run after the first
+// adds to dW what the same threads stored before it.
 //
 // 8-bit integers.  sm_103a has no integer product at tensor rates, but every code is exact in fp16 and a
 // product of two in fp32, so fp16 tensor products of widened codes are the integer products, and their
@@ -54,7 +55,6 @@ constexpr int kBoxes = 3;                    // row-operand boxes: 128, 64 and 3
 constexpr int kChunkM = 16;                  // row tiles per L2 reuse chunk of a group
 constexpr int kRun = 2048;                   // rows of an fp32 weight-gradient run
 constexpr int kTmemCols = 512;
-constexpr uint32_t kEpiBox = 32 * 64;        // a staging box: 32 rows of 64 bytes
 
 template <int kOp>
 struct Shape {
@@ -62,24 +62,23 @@ struct Shape {
   static constexpr int kRaw = kOp == kI8 ? 2 : 0;          // 8-bit integers: stages of codes, two K blocks each,
   static constexpr int kTeams = 4, kTeam = 4;              // and the teams of warps that widen them
   static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : 0;
-  static constexpr int kThreads = 32 * (6 + kExtra);
-  static constexpr uint32_t kEpi = kOp == kDw ? 4 * 2 * kEpiBox : 0;
-  static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kEpi + 512 + sizeof(GroupTab);
+  static constexpr int kEpiWarps = kOp == kDw ? 8 : 4;
+  static constexpr int kThreads = 32 * (2 + kEpiWarps + kExtra);
+  static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + 512 + sizeof(GroupTab);
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
 struct Params {
-  CUtensorMap a;              // M side: the weight, or dy (weight gradient)
-  CUtensorMap b[kBoxes];      // N side: the rows in boxes of 128, 64, 32; or x in b[0] (weight gradient)
-  CUtensorMap out;            // weight gradient: dW in boxes
-  const CUtensorMap* maps;    // weight gradient: every group's a and b[0]
+  CUtensorMap a;              // M side: the weight
+  CUtensorMap b[kBoxes];      // N side: the rows in boxes of 128, 64, 32
+  const CUtensorMap* maps;    // weight gradient: every group's x (M side) and dy (N side)
   const int32_t *begin, *end;
   void* y;
   const float *qs, *ws;       // scales of the rows and of the output channels (8-bit integers)
   int64_t rows, ldy;
   int depth;                  // contraction length (rows times a weight)
   int width;                  // features of the output row; weight gradient: columns of dW (n_in)
-  int M;                      // weight gradient: rows of dW (n_out)
+  int M;                      // weight gradient: rows of a dW (n_out)
   int G, nf, mf;              // whole tiles across width; weight gradient: all tiles across width and M
   bool narrow;                // rows times a weight: there is a last, narrower tile across width
   bool fp16, wide_a, wide_b;  // wide: one copy fetches two 64-column boxes (columns a multiple of 64)
@@ -90,7 +89,8 @@ struct Params {
 
 struct Job {
   int g, row, n, f0;   // rows times a weight: first row, rows, first feature
-  int m0, kits, run;   // weight gradient: first dW row, K blocks of the run, its number
+  int kits;            // K blocks
+  int k0, k, run;      // weight gradient (row, n, f0: rows and columns of dW): rows of the run, its number
 };
 
 // Rows times a weight: tile t -> group, row tile, feature tile.  Groups in order; within a group,
@@ -132,13 +132,14 @@ __device__ __forceinline__ Job dw_job(const Params& p, const GroupTab& s, int t,
   Job j{};
   j.g = t / per;
   const int r = t - j.g * per;
-  j.m0 = r / p.nf * kTile;
+  j.row = r / p.nf * kTile;
+  j.n = min(kTile, p.M - j.row);
   j.f0 = r % p.nf * kTile;
   j.run = run;
   const int n = s.end[j.g] - s.begin[j.g], from = run * kRun;
-  j.row = s.begin[j.g] + from;
-  j.n = p.dw_fp32 ? min(kRun, n - from) : n;
-  j.kits = (j.n + kBK - 1) / kBK;
+  j.k0 = s.begin[j.g] + from;
+  j.k = p.dw_fp32 ? min(kRun, n - from) : n;
+  j.kits = (j.k + kBK - 1) / kBK;
   return j;
 }
 
@@ -176,28 +177,37 @@ struct Walk {
   }
 };
 
-// A store under a predicate rather than a branch, so that a run of them needs no reconvergence.
-__device__ __forceinline__ void store_if(uint16_t* at, uint32_t w, bool yes) {
+// A store or load under a predicate rather than a branch, so that a run of them needs no reconvergence.
+__device__ __forceinline__ void store_if(void* at, uint32_t w, bool yes) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(at), "r"(w),
                "r"((int)yes)
                : "memory");
 }
 
+__device__ __forceinline__ float load_if(const float* at, bool yes) {
+  float v = 0.f;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.f32 %0, [%1];\n\t}"
+               : "+f"(v)
+               : "l"(at), "r"((int)yes)
+               : "memory");
+  return v;
+}
+
 // ---- epilogues -----------------------------------------------------------------------------------
 
-// Rows times a weight: this warp's 32 features (lanes) of the tile's rows (columns).  Lanes exchange
-// with their neighbour so that each holds two features of one row: an instruction stores 64 bytes of
-// two rows.
+// 16-bit outputs: this warp's 32 features (lanes) of the tile's rows (columns), the first row at `out`, ld
+// elements apart.  Lanes exchange with their neighbour so that each holds two features of one row: an
+// instruction stores 64 bytes of two rows.
 template <int kOp>
-__device__ __forceinline__ void store_rows(const Params& p, const Job& j, int rank, int q, int lane, uint32_t ta) {
-  const int f = j.f0 + kBM * rank + 32 * q + lane;
+__device__ __forceinline__ void store16(const Params& p, const Job& j, uint16_t* out, int64_t ld, int f, int lane,
+                                        uint32_t ta, int share) {
+  constexpr int kStep = 8 * Shape<kOp>::kEpiWarps;   // rows from one turn of the warp to the next
   const bool odd = lane & 1;
-  if (j.f0 + kBM * rank + 32 * q >= p.width) return;   // the whole warp lies past the last feature
-  const bool live = f < p.width;                       // a multiple of 8: the same for both lanes of a pair
+  const bool live = f < p.width;   // a multiple of 8: the same for both lanes of a pair
   const float ws = kOp == kI8 && live ? p.ws[(int64_t)j.g * p.width + f] : 1.f;
-  uint16_t* out = static_cast<uint16_t*>(p.y) + (int64_t)(j.row + odd) * p.ldy + (f & ~1);
+  out += (32 * share + odd) * ld + (f & ~1);
 #pragma unroll 1
-  for (int c = 0; c < j.n; c += 32) {
+  for (int c = 32 * share; c < j.n; c += kStep, out += kStep * ld) {
     uint32_t v[32];
     tmem_ld32(ta + c, v);
     float qs = 0.f;
@@ -220,90 +230,75 @@ __device__ __forceinline__ void store_rows(const Params& p, const Job& j, int ra
       }
     }
     const int left = live ? j.n - c - odd : 0;   // this lane's rows from c on
-    uint16_t* at = out + (int64_t)c * p.ldy;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      store_if(at, w[i], 2 * i < left);
-      at += 2 * p.ldy;
-    }
+    for (int i = 0; i < 16; ++i) store_if(out + 2 * i * ld, w[i], 2 * i < left);
   }
 }
 
-__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int32_t c0, int32_t c1, int32_t c2) {
-  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
-}
-
-// Weight gradient: this warp's 32 rows of dW (lanes), 256 columns, through two staging boxes of 32 rows
-// x 64 bytes (the layout of the 64-byte swizzle: 16-byte chunk c of row r at c ^ ((r >> 1) & 3)) and
-// bulk stores, which clip what lies past dW.  A run after the first adds to what this warp stored
-// before, so it first waits for those stores to be performed.
-__device__ __forceinline__ void store_dw(const Params& p, const Job& j, int rank, int q, int lane, uint32_t ta,
-                                         uint8_t* boxes) {
-  const int y = j.m0 + kBM * rank + 32 * q;
-  if (y >= p.M) return;
+// fp32 outputs (weight gradient): an instruction stores 128 bytes of a row.  To add to what is there, the
+// next 32 rows are on their way (from L2: prefetch_dw) while 32 are added.
+template <int kOp>
+__device__ __forceinline__ void store32(const Params& p, const Job& j, float* out, int64_t ld, int f, uint32_t ta,
+                                        int share) {
+  constexpr int kStep = 8 * Shape<kOp>::kEpiWarps;
   const bool add = p.acc || j.run > 0;
-  if (lane == 0) {
-    if (j.run > 0) bulk_wait_all();
-    else bulk_wait_read<0>();
-  }
-  __syncwarp();
-  int n = 0;
+  const int n = f < p.width ? j.n : 0;
+  out += 32 * share * ld + f;
+  float old[32], next[32];
+  auto fetch = [&](int c, const float* from) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) next[i] = load_if(from + i * ld, add && c + i < n);
+  };
+  fetch(32 * share, out);
 #pragma unroll 1
-  for (int c = 0; c < kTile; c += 32) {
-    if (j.f0 + c >= p.width) break;
+  for (int c = 32 * share; c < j.n; c += kStep, out += kStep * ld) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) old[i] = next[i];
+    fetch(c + kStep, out + kStep * ld);
     uint32_t v[32];
     tmem_ld32(ta + c, v);
     tmem_ld_wait();
-    const int parts = p.dw_fp32 ? 2 : 1;   // 32 columns: two fp32 boxes or one 16-bit box
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == parts || j.f0 + c + 16 * h >= p.width) break;
-      if (n >= 2) {   // the box of two stores ago has been read
-        if (lane == 0) bulk_wait_read<1>();
-        __syncwarp();
-      }
-      uint8_t* box = boxes + (n & 1) * kEpiBox;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint4 w;
-        if (p.dw_fp32) {
-          w = make_uint4(v[16 * h + 4 * k], v[16 * h + 4 * k + 1], v[16 * h + 4 * k + 2], v[16 * h + 4 * k + 3]);
-        } else {
-          uint32_t u[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            u[i] = pack16(__uint_as_float(v[8 * k + 2 * i]), __uint_as_float(v[8 * k + 2 * i + 1]), p.fp16);
-          w = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-        *reinterpret_cast<uint4*>(box + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = w;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (add) tma_add_3d(&p.out, box, j.f0 + c + 16 * h, y, j.g);
-        else tma_store_3d(&p.out, box, j.f0 + c + 16 * h, y, j.g);
-        bulk_commit();
-      }
-      ++n;
-    }
+    for (int i = 0; i < 32; ++i)
+      store_if(out + i * ld, __float_as_uint(__uint_as_float(v[i]) + old[i]), c + i < n);
   }
 }
 
-// A group without rows has a zero gradient (nothing to add to a running one): this warp's 32 rows of
-// the tile, a row at a time.
-__device__ __forceinline__ void store_zero(const Params& p, const Job& j, int rank, int q, int lane) {
-  if (p.acc) return;
-  const int size = p.dw_fp32 ? 4 : 2, per = 16 / size;
-  const int c1 = min(p.width, j.f0 + kTile);
-  for (int i = 0; i < 32; ++i) {
-    const int y = j.m0 + kBM * rank + 32 * q + i;
-    if (y >= p.M) break;
-    char* row = static_cast<char*>(p.y) + (((int64_t)j.g * p.M + y) * p.width) * size;
-    for (int c = j.f0 + lane * per; c < c1; c += 32 * per)
-      *reinterpret_cast<uint4*>(row + (int64_t)c * size) = make_uint4(0, 0, 0, 0);
+// This warp's share of a finished tile.
+template <int kOp>
+__device__ __forceinline__ void store_tile(const Params& p, const Job& j, int rank, int q, int lane, uint32_t ta, int share) {
+  const int f = j.f0 + kBM * rank + 32 * q + lane;
+  if (f - lane >= p.width) return;   // the whole warp lies past the last feature
+  if (kOp == kDw) {
+    const int64_t first = ((int64_t)j.g * p.M + j.row) * p.width;
+    if (p.dw_fp32) store32<kOp>(p, j, static_cast<float*>(p.y) + first, p.width, f, ta, share);
+    else store16<kOp>(p, j, static_cast<uint16_t*>(p.y) + first, p.width, f, lane, ta, share);
+  } else {
+    store16<kOp>(p, j, static_cast<uint16_t*>(p.y) + (int64_t)j.row * p.ldy, p.ldy, f, lane, ta, share);
+  }
+}
+
+// A running gradient's tile that a later epilogue will add to, to L2 ahead of it (a row a thread).
+__device__ __forceinline__ void prefetch_dw(const Params& p, const Job& j, int rank, int q, int lane, int share) {
+  const int f = j.f0 + kBM * rank, bytes = min(p.width - f, kBM) * 4;
+  if (!p.acc || j.kits == 0 || j.run > 0 || bytes <= 0) return;
+  const int row = j.row + 128 * share + 32 * q + lane;
+  if (row < p.M)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const float*>(p.y) +
+                                                                   ((int64_t)j.g * p.M + row) * p.width + f),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// A group without rows has a zero gradient (nothing to add to a running one): this warp's 32 columns of
+// the tile.
+__device__ __forceinline__ void store_zero(const Params& p, const Job& j, int rank, int q, int lane, int share) {
+  const int f = j.f0 + kBM * rank + 32 * q + lane;
+  if (p.acc || f >= p.width) return;
+  const int64_t first = ((int64_t)j.g * p.M + j.row) * p.width + f;
+  for (int i = share; i < j.n; i += 2) {
+    if (p.dw_fp32) static_cast<float*>(p.y)[first + (int64_t)i * p.width] = 0.f;
+    else static_cast<uint16_t*>(p.y)[first + (int64_t)i * p.width] = 0;
   }
 }
 
@@ -343,8 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = smem;
   uint8_t* raws = stages + kStages * kStage;
-  uint8_t* boxes = raws + S::kRaw * kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + S::kEpi);
+  uint64_t* full = reinterpret_cast<uint64_t*>(raws + S::kRaw * kStage);
   uint64_t* empty = full + 6;
   uint64_t* raw = empty + 6;
   uint64_t* rempty = raw + 6;
@@ -353,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  GroupTab& tab = *reinterpret_cast<GroupTab*>(boxes + S::kEpi + 512);
+  GroupTab& tab = *reinterpret_cast<GroupTab*>(raws + S::kRaw * kStage + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -367,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 8);
+      mbar_init(&tempty[a], 2 * S::kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -454,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
               if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * bytes);
               const uint32_t bar = cluster_addr(&full[slot], 0);
               if constexpr (kOp == kDw) {
-                const int row = j.row + kit * kBK, ca = j.m0 + kBM * rank, cb = j.f0 + kBM * rank;
+                const int row = j.k0 + kit * kBK, ca = j.f0 + kBM * rank, cb = j.row + kBM * rank;
                 if (p.wide_a) {
                   tma_load_3d_pair(st, ma, bar, 0, row, ca / 64);
                 } else {
@@ -543,13 +537,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       umma_commit_both(drain);
     }
     if (lane == 0) mbar_wait_drain(drain, 0, limit);
-  } else if (warp < 6) {
-    const int q = warp & 3;   // TMEM lane quarter this warp may access
+  } else if (warp < 2 + S::kEpiWarps) {
+    const int q = warp & 3;                      // TMEM lane quarter this warp may access
+    const int share = (warp - 2) / 4;            // of two warps of a quarter: every other 32 rows
     int acc = 0;
     uint32_t acc_phase = 0;
-    while (walk.next(j)) {
+    Job next;
+    bool more = walk.next(next);
+    if (kOp == kDw && more) prefetch_dw(p, next, rank, q, lane, share);
+    while (more) {
+      j = next;
+      more = walk.next(next);
+      if (kOp == kDw && more) prefetch_dw(p, next, rank, q, lane, share);
       if (j.kits == 0) {
-        store_zero(p, j, rank, q, lane);
+        store_zero(p, j, rank, q, lane, share);
         continue;
       }
       if (!mbar_wait_idle(&tfull[acc], acc_phase, limit, abort_flag)) {
@@ -558,17 +559,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       }
       tc_fence_after();
       const uint32_t ta = tmem_base + (uint32_t)(acc * kTile) + ((uint32_t)(q * 32) << 16);
-      if constexpr (kOp == kDw) store_dw(p, j, rank, q, lane, ta, boxes + (warp - 2) * 2 * kEpiBox);
-      else store_rows<kOp>(p, j, rank, q, lane, ta);
+      store_tile<kOp>(p, j, rank, q, lane, ta, share);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+      // (relaxed: the reads of the accumulator have completed, and a release would wait for the tile's stores)
+      if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[acc], 0));
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
       }
     }
-    if (kOp == kDw && lane == 0) bulk_wait_all();   // this warp's output stores have landed
   } else if constexpr (kOp == kI8) {
     // Widen: the teams take turns at the K blocks (a raw stage holds two), each with a stage of its own; a
     // warp takes every fourth octet of rows (of the weight's 128, then of up to 128 token rows), a lane a
@@ -577,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     // at cluster scope) takes about as long as a block's products: with two it was 1.3 times the time.
     static_assert(kStages == S::kTeams, "a stage a team");
     constexpr int kPer = kBM / 8 / S::kTeam;
-    const int team = (warp - 6) / S::kTeam, w = (warp - 6) % S::kTeam, r = lane & 7, cq = lane >> 3;
+    const int team = (warp - 2 - S::kEpiWarps) / S::kTeam, w = (warp - 2 - S::kEpiWarps) % S::kTeam, r = lane & 7, cq = lane >> 3;
     const uint32_t to = (w * 8 + r) * 128;
     const uint32_t o0 = ((2 * cq) ^ r) << 4, o1 = ((2 * cq + 1) ^ r) << 4;
     int block = 0, rblock = 0;   // K blocks and raw stages before this job
@@ -632,7 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   }
 }
 
-// The maps of every group's rows of dy and x for the weight gradient: those of all rows (dimension 1
+// The maps of every group's rows of x and dy for the weight gradient: those of all rows (dimension 1
 // counts rows in both forms), ending at the group's end.  A block a group, a warp a map.
 __global__ void __launch_bounds__(64) group_maps_kernel(const __grid_constant__ CUtensorMap a,
                                                         const __grid_constant__ CUtensorMap b, const int32_t* end,
@@ -675,7 +675,7 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base
 
 constexpr CUtensorMapDataType k16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;   // (fp16 values too: bits are copied)
 constexpr CUtensorMapDataType k8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B, kSw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B;
 
 // Rows [rows, width], 16-bit or codes, as K-major boxes of 128 bytes x 128, 64 and 32 rows.
 bool map_rows(CUtensorMap* m, const void* base, bool codes, uint64_t rows, uint64_t width, uint64_t ld) {
@@ -714,14 +714,6 @@ bool map_rows_mn(CUtensorMap* m, const void* base, uint64_t rows, uint64_t width
   const cuuint64_t dims[2] = {width, rows}, strides[1] = {ld * 2};
   const cuuint32_t box[2] = {64, 64};
   return encode(m, k16, 2, base, dims, strides, box, kSw128);
-}
-
-// dW [G, N, K] in boxes of 32 rows x 64 bytes.
-bool map_dw(CUtensorMap* m, const void* base, uint64_t G, uint64_t N, uint64_t K, bool fp32) {
-  const uint64_t size = fp32 ? 4 : 2;
-  const cuuint64_t dims[3] = {K, N, G}, strides[2] = {K * size, K * N * size};
-  const cuuint32_t box[3] = {(cuuint32_t)(64 / size), 32, 1};
-  return encode(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : k16, 3, base, dims, strides, box, kSw64);
 }
 
 uint32_t idesc_of(bool fp16, bool a_mn, bool b_mn) {
@@ -807,14 +799,14 @@ cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int3
 cudaError_t launch_grouped_dw(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* dy,
                               const uint16_t* x, void* dW, Hdr* hdr, void* maps, cudaStream_t s) {
   Params p = params_of(c, begin, end, hdr);
-  p.wide_a = c.N % 64 == 0;
-  p.wide_b = c.K % 64 == 0;
-  if (!map_dw(&p.out, dW, c.G, c.N, c.K, c.dw_fp32)) return cudaErrorInvalidValue;
+  p.wide_a = c.K % 64 == 0;
+  p.wide_b = c.N % 64 == 0;
   p.maps = static_cast<const CUtensorMap*>(maps);
   if (c.rows > 0) {   // (without rows every tile is a zero tile)
-    if (!map_rows_mn(&p.a, dy, c.rows, c.N, c.ldo, p.wide_a) || !map_rows_mn(&p.b[0], x, c.rows, c.K, c.ldi, p.wide_b))
+    CUtensorMap mx, mdy;
+    if (!map_rows_mn(&mx, x, c.rows, c.K, c.ldi, p.wide_a) || !map_rows_mn(&mdy, dy, c.rows, c.N, c.ldo, p.wide_b))
       return cudaErrorInvalidValue;
-    group_maps_kernel<<<c.G, 64, 0, s>>>(p.a, p.b[0], end, c.rows, static_cast<CUtensorMap*>(maps));
+    group_maps_kernel<<<c.G, 64, 0, s>>>(mx, mdy, end, c.rows, static_cast<CUtensorMap*>(maps));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
