@@ -177,20 +177,17 @@ struct Walk {
   }
 };
 
-// A store or load under a predicate rather than a branch, so that a run of them needs no reconvergence.
+// A store or an addition under a predicate rather than a branch, so that a run of them needs no reconvergence.
 __device__ __forceinline__ void store_if(void* at, uint32_t w, bool yes) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(at), "r"(w),
                "r"((int)yes)
                : "memory");
 }
 
-__device__ __forceinline__ float load_if(const float* at, bool yes) {
-  float v = 0.f;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.f32 %0, [%1];\n\t}"
-               : "+f"(v)
-               : "l"(at), "r"((int)yes)
+__device__ __forceinline__ void add_if(float* at, float v, bool yes) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p red.global.add.f32 [%0], %1;\n\t}" ::"l"(at), "f"(v),
+               "r"((int)yes)
                : "memory");
-  return v;
 }
 
 // ---- epilogues -----------------------------------------------------------------------------------
@@ -235,32 +232,27 @@ __device__ __forceinline__ void store16(const Params& p, const Job& j, uint16_t*
   }
 }
 
-// fp32 outputs (weight gradient): an instruction stores 128 bytes of a row.  To add to what is there, the
-// next 32 rows are on their way (from L2: prefetch_dw) while 32 are added.
+// fp32 outputs (weight gradient): an instruction stores 128 bytes of a row, or adds them to what is there
+// (one addition an element and run, in order: the same sum every time; subnormal values count as zero).
 template <int kOp>
 __device__ __forceinline__ void store32(const Params& p, const Job& j, float* out, int64_t ld, int f, uint32_t ta,
                                         int share) {
   constexpr int kStep = 8 * Shape<kOp>::kEpiWarps;
   const bool add = p.acc || j.run > 0;
-  const int n = f < p.width ? j.n : 0;
+  const int n = f < p.width ? j.n : 0, step = (int)ld;
   out += 32 * share * ld + f;
-  float old[32], next[32];
-  auto fetch = [&](int c, const float* from) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) next[i] = load_if(from + i * ld, add && c + i < n);
-  };
-  fetch(32 * share, out);
 #pragma unroll 1
   for (int c = 32 * share; c < j.n; c += kStep, out += kStep * ld) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) old[i] = next[i];
-    fetch(c + kStep, out + kStep * ld);
     uint32_t v[32];
     tmem_ld32(ta + c, v);
     tmem_ld_wait();
+    if (add) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      store_if(out + i * ld, __float_as_uint(__uint_as_float(v[i]) + old[i]), c + i < n);
+      for (int i = 0; i < 32; ++i) add_if(out + i * step, __uint_as_float(v[i]), c + i < n);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) store_if(out + i * step, v[i], c + i < n);
+    }
   }
 }
 
@@ -278,7 +270,8 @@ __device__ __forceinline__ void store_tile(const Params& p, const Job& j, int ra
   }
 }
 
-// A running gradient's tile that a later epilogue will add to, to L2 ahead of it (a row a thread).
+// A running gradient's tile that the next epilogue will add to, to L2 ahead of it (a row a thread): without
+// it the additions wait in L2 for HBM.
 __device__ __forceinline__ void prefetch_dw(const Params& p, const Job& j, int rank, int q, int lane, int share) {
   const int f = j.f0 + kBM * rank, bytes = min(p.width - f, kBM) * 4;
   if (!p.acc || j.kits == 0 || j.run > 0 || bytes <= 0) return;
@@ -574,7 +567,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     // warp takes every fourth octet of rows (of the weight's 128, then of up to 128 token rows), a lane a
     // row and 16 of its codes: in the 128-byte swizzle the eight lanes of a phase touch distinct banks
     // on both sides.  Four teams, because the arrival that the even CTA's MMA thread waits for (a release
-    // at cluster scope) takes about as long as a block's products: with two it was 1.3 times the time.
+    // at cluster scope) takes about as long as a block's products: with two teams the kernel took 1.3 times
+    // as long.  (One arrival a team, after a barrier of its own, was 6% slower.)
     static_assert(kStages == S::kTeams, "a stage a team");
     constexpr int kPer = kBM / 8 / S::kTeam;
     const int team = (warp - 2 - S::kEpiWarps) / S::kTeam, w = (warp - 2 - S::kEpiWarps) % S::kTeam, r = lane & 7, cq = lane >> 3;
