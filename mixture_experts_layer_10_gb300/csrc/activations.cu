@@ -18,6 +18,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "grouped.cuh"
 #include "e4m3.cuh"
 
 namespace moe {
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_i8_kernel(const uint16
   const int nvec = cols / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int buf = 0;
+  after_previous_kernel();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, buf ^= 1) {
     uint4 v[NV];
     load_row<NV>(src, cols, nullptr, 0, r, nvec, nvec, kThreads, v);
@@ -349,15 +351,20 @@ cudaError_t launch_quantize_rows_i8(const uint16_t* src, bool fp16, int64_t rows
   if (rows <= 0) return cudaSuccess;
   prof_mark(kKQuantI8, s, true);
   // up to four vectors of eight values a thread; past 32768 values, eight
-  const int nvec = cols / 8, blocks = (int)std::min<int64_t>(rows, 1 << 30);
-  if (nvec <= 4 * 32) quantize_rows_i8_kernel<32, 4><<<blocks, 32, 0, s>>>(src, fp16, rows, cols, codes, scales);
-  else if (nvec <= 4 * 64) quantize_rows_i8_kernel<64, 4><<<blocks, 64, 0, s>>>(src, fp16, rows, cols, codes, scales);
-  else if (nvec <= 4 * 128) quantize_rows_i8_kernel<128, 4><<<blocks, 128, 0, s>>>(src, fp16, rows, cols, codes, scales);
-  else if (nvec <= 4 * 256) quantize_rows_i8_kernel<256, 4><<<blocks, 256, 0, s>>>(src, fp16, rows, cols, codes, scales);
-  else if (nvec <= 4 * 1024) quantize_rows_i8_kernel<1024, 4><<<blocks, 1024, 0, s>>>(src, fp16, rows, cols, codes, scales);
-  else quantize_rows_i8_kernel<1024, 8><<<blocks, 1024, 0, s>>>(src, fp16, rows, cols, codes, scales);
+  const int nvec = cols / 8;
+  const int64_t blocks = std::min<int64_t>(rows, 1 << 30);
+  auto launch = [&](auto kernel, int threads) {
+    return launch_after(kernel, blocks, threads, 0, 1, s, src, fp16, rows, cols, codes, scales);
+  };
+  cudaError_t e;
+  if (nvec <= 4 * 32) e = launch(quantize_rows_i8_kernel<32, 4>, 32);
+  else if (nvec <= 4 * 64) e = launch(quantize_rows_i8_kernel<64, 4>, 64);
+  else if (nvec <= 4 * 128) e = launch(quantize_rows_i8_kernel<128, 4>, 128);
+  else if (nvec <= 4 * 256) e = launch(quantize_rows_i8_kernel<256, 4>, 256);
+  else if (nvec <= 4 * 1024) e = launch(quantize_rows_i8_kernel<1024, 4>, 1024);
+  else e = launch(quantize_rows_i8_kernel<1024, 8>, 1024);
   prof_mark(kKQuantI8, s, false);
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_quantize_rows_e4m3(const uint16_t* src, int64_t rows, int cols, uint8_t* codes, float* scales,

@@ -368,6 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
+  after_previous_kernel();
   const int rtiles = load_groups(tab, p.begin, p.end, p.G, p.rows, kTile, p.hdr);
   tc_fence_before();
   __syncthreads();
@@ -635,6 +636,7 @@ __global__ void __launch_bounds__(64) group_maps_kernel(const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.x;
   reinterpret_cast<uint32_t*>(&map[warp])[lane] = reinterpret_cast<const uint32_t*>(warp == 0 ? &a : &b)[lane];
   __syncwarp();
+  after_previous_kernel();
   if (lane == 0) {
     const int64_t to = end[g];   // (whatever it holds, the map stays within the tensor)
     const uint32_t dim = (uint32_t)(to < 1 ? 1 : (to > rows ? rows : to));
@@ -747,9 +749,9 @@ cudaError_t launch(const Params& p, int64_t most_tiles, int id, cudaStream_t s) 
   }
   const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(most, most_tiles));
   prof_mark(id, s, true);
-  grouped_kernel<kOp><<<2 * pairs, S::kThreads, S::kSmem, s>>>(p);
+  e = launch_after(grouped_kernel<kOp>, 2 * pairs, S::kThreads, S::kSmem, 1, s, p);   // (clusters of two: by its attribute)
   prof_mark(id, s, false);
-  return cudaGetLastError();
+  return e;
 }
 
 // The most row tiles the rows can make.
@@ -800,8 +802,8 @@ cudaError_t launch_grouped_dw(const Grouped& c, const int32_t* begin, const int3
     CUtensorMap mx, mdy;
     if (!map_rows_mn(&mx, x, c.rows, c.K, c.ldi, p.wide_a) || !map_rows_mn(&mdy, dy, c.rows, c.N, c.ldo, p.wide_b))
       return cudaErrorInvalidValue;
-    group_maps_kernel<<<c.G, 64, 0, s>>>(mx, mdy, end, c.rows, static_cast<CUtensorMap*>(maps));
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(group_maps_kernel, c.G, 64, 0, 1, s, mx, mdy, end, c.rows,
+                                       static_cast<CUtensorMap*>(maps));
     if (e != cudaSuccess) return e;
   }
   p.y = dW;

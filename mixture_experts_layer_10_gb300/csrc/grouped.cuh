@@ -104,6 +104,35 @@ struct SmemOnce {
   }
 };
 
+// The kernels of the grouped products are launched so that a kernel's blocks may start, as those of the
+// kernel before it in the stream end, before that one has ended altogether (programmatic dependent launch).
+// Each first waits for the kernels before it to have ended and their writes to be visible, so nothing
+// but its launch and its barriers' setup overlaps them, and then lets the next one do the same.
+__device__ __forceinline__ void after_previous_kernel() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), int64_t blocks, int threads, size_t smem, int cluster,
+                         cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Bounded wait with naps of kNap ns between polls.  kCluster acquires at cluster scope: for barriers on
 // which the peer CTA's threads arrive after writing shared memory.
 template <bool kCluster>

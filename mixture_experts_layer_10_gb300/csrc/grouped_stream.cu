@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
     tma_prefetch(&p.W);
     tma_prefetch(&p.x);
   }
+  after_previous_kernel();
   const int tiles = load_groups(tab, p.begin, p.end, p.G, p.rows, kRows, p.hdr);   // (a barrier of the block, too)
   if (p.split > 1) cluster_sync();   // all blocks' barriers exist before any remote arrival
   const int ntiles = max(tiles, 0) * p.nf;
@@ -314,22 +315,10 @@ cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, cons
   static SmemOnce once;
   cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(32 * (kWarps + 1));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
   prof_mark(id, s, true);
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  e = launch_after(kernel, grid, 32 * (kWarps + 1), smem, p.split, s, p);
   prof_mark(id, s, false);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return e;
 }
 
 template <int kType>
