@@ -107,10 +107,9 @@ struct SmemOnce {
 // The kernels of the grouped products are launched so that a kernel's blocks may start, as those of the
 // kernel before it in the stream end, before that one has ended altogether (programmatic dependent launch).
 // Each first waits for the kernels before it to have ended and their writes to be visible, so nothing
-// but its launch and its barriers' setup overlaps them, and then lets the next one do the same.
-__device__ __forceinline__ void after_previous_kernel() {
-  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
-}
+// but its launch and its barriers' setup overlaps them.  (Blocks that start earlier still, as soon as all
+// of the kernel before them are running, take room and slow it: 63.6 -> 66.8 us at 64 tokens, 64 experts.)
+__device__ __forceinline__ void after_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <class... Params, class... Args>
 cudaError_t launch_after(void (*kernel)(Params...), int64_t blocks, int threads, size_t smem, int cluster,
