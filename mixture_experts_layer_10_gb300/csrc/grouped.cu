@@ -55,6 +55,7 @@ constexpr int kBoxes = 3;                    // row-operand boxes: 128, 64 and 3
 constexpr int kChunkM = 16;                  // row tiles per L2 reuse chunk of a group
 constexpr int kRun = 2048;                   // rows of an fp32 weight-gradient run
 constexpr int kTmemCols = 512;
+constexpr int kAhead = 4;                    // raw stages of weights fetched to L2 ahead (8-bit integers)
 
 template <int kOp>
 struct Shape {
@@ -300,6 +301,20 @@ __device__ __forceinline__ void fence_map(const CUtensorMap* map) {
   asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// A box of a tensor to L2.
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+// Releases, at cluster scope, what this thread knows of writes to its CTA's shared memory, to whoever sees a
+// relaxed arrival that follows.  (A releasing arrival waits for every other memory operation too: 9% of the
+// time of the 8-bit product.)
+__device__ __forceinline__ void fence_release_smem() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+
 // Arrive once on the mbarrier at this shared-memory offset in both CTAs when every pair MMA this thread
 // issued so far has completed.
 __device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
@@ -406,6 +421,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
               uint8_t* st = raws + (size_t)slot * kStage;
               mbar_arrive_expect_tx(&raw[slot], kHalf + (128u >> bx) * 128u);
               tma_load_3d(st, &p.a, &raw[slot], kit * 2 * kBK, j.f0 + kBM * rank, j.g);
+              // two raw stages do not cover the way from HBM: the weight's next ones come to L2 before
+              if ((kit + kAhead) * 2 * kBK < p.depth)
+                prefetch_3d(&p.a, (kit + kAhead) * 2 * kBK, j.f0 + kBM * rank, j.g);
               tma_load_2d(st + kHalf, &p.b[bx], &raw[slot], kit * 2 * kBK, j.row + half * rank);
             }
             ++uses;
@@ -567,9 +585,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     // Widen: the teams take turns at the K blocks (a raw stage holds two), each with a stage of its own; a
     // warp takes every fourth octet of rows (of the weight's 128, then of up to 128 token rows), a lane a
     // row and 16 of its codes: in the 128-byte swizzle the eight lanes of a phase touch distinct banks
-    // on both sides.  Four teams, because the arrival that the even CTA's MMA thread waits for (a release
-    // at cluster scope) takes about as long as a block's products: with two teams the kernel took 1.3 times
-    // as long.  (One arrival a team, after a barrier of its own, was 6% slower.)
+    // on both sides.  (Four teams of four warps hide the way of a block
+    // through its barriers better than two of eight: 1632 against 1920 us at 16384 rows, 4096 x 14336.)
     static_assert(kStages == S::kTeams, "a stage a team");
     constexpr int kPer = kBM / 8 / S::kTeam;
     const int team = (warp - 2 - S::kEpiWarps) / S::kTeam, w = (warp - 2 - S::kEpiWarps) % S::kTeam, r = lane & 7, cq = lane >> 3;
@@ -612,7 +629,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
           __syncwarp();
         }
         if (lane == 0) mbar_arrive(&rempty[rs]);
-        if (mine && lane == 0) mbar_arrive_cluster(cluster_addr(&full[team], 0));   // (last: it takes longest)
+        if (mine && lane == 0) {
+          fence_release_smem();
+          mbar_arrive_cluster_relaxed(cluster_addr(&full[team], 0));
+        }
       }
       block += kits;
       rblock += rkits;
