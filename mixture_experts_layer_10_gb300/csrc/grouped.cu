@@ -28,11 +28,18 @@
 // 16 rows, which a long contraction would let grow past fp32's own rounding); every run after the first
 // adds to dW what the same threads stored before it.
 //
-// 8-bit integers.  sm_103a has no integer product at tensor rates, but every code is exact in fp16 and a
-// product of two in fp32, so fp16 tensor products of widened codes are the integer products, and their
-// fp32 sums are exact up to 2^24.  Codes travel as bytes as far as the registers of the warps that widen
-// them into the stages.  (A ring of raw stages that TMA fills, read and widened from there, took the
-// room of half the stages and a third more shared-memory traffic: PERF_I8.)
+// 8-bit integers.  sm_103a has no integer product at tensor rates (mma.sync on 8-bit integers: 256 products
+// a clock and SM, a quarter of its fp16 rate and a sixteenth of tcgen05's), but every code is exact in
+// fp16 and a product of two in fp32, so fp16 tensor products of widened codes are the integer products,
+// and their fp32 sums are exact up to 2^24.  TMA brings the codes as bytes to a ring of raw stages, and
+// sixteen warps widen them into the ring that the tensor cores read.
+//
+// Measured (graph replays on inputs larger than L2): y of 16384 rows, 8 groups, 4096 x 14336, bf16: 1.04 to
+// 1.15 ms by the GPU's clock, 1.67 to 1.85 PFLOP/s, bound by the tensor cores under the power cap; with
+// 8-bit integers 1.38 ms, bound by the way of a block through the two rings.  dx and dW of 98304 rows, 64
+// groups, 2048 x 1408: 0.35 and 0.36 ms, 1.6 PFLOP/s; the rest is the tiles' ends (22 K blocks and
+// fewer a tile).  fp32 dW += of 8192 rows, 128 groups, 2048 x 768: 0.27 ms, 5.5 TB/s, bound by reading and
+// writing dW.
 #include <algorithm>
 
 #include "common.cuh"
@@ -306,13 +313,6 @@ __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int32_t c0, 
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
                "r"(c0), "r"(c1), "r"(c2)
                : "memory");
-}
-
-// Releases, at cluster scope, what this thread knows of writes to its CTA's shared memory, to whoever sees a
-// relaxed arrival that follows.  (A releasing arrival waits for every other memory operation too: 9% of the
-// time of the 8-bit product.)
-__device__ __forceinline__ void fence_release_smem() {
-  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
 
 // Arrive once on the mbarrier at this shared-memory offset in both CTAs when every pair MMA this thread

@@ -132,6 +132,13 @@ cudaError_t launch_after(void (*kernel)(Params...), int64_t blocks, int threads,
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Releases, at cluster scope, what this thread knows of writes to its CTA's shared memory, to whoever sees a
+// relaxed arrival that follows.  (A releasing arrival waits for every other memory operation too: 9% of the
+// time of the 8-bit product on CTA pairs.)
+__device__ __forceinline__ void fence_release_smem() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+
 // Bounded wait with naps of kNap ns between polls.  kCluster acquires at cluster scope: for barriers on
 // which the peer CTA's threads arrive after writing shared memory.
 template <bool kCluster>

@@ -254,7 +254,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
 #pragma unroll
       for (int v = 0; v < 4; ++v) red[(8 * k + 2 * c + (v & 1)) * kPitch + warp * 16 + r + 8 * (v >> 1)] = acc[k][v];
     __syncwarp();
-    if (lane < p.split) mbar_arrive_cluster(cluster_addr(&sums, lane));
+    if (lane < p.split) {
+      fence_release_smem();
+      mbar_arrive_cluster_relaxed(cluster_addr(&sums, lane));
+    }
     wait_sums(&sums, turn);
     if (ok) {
       // two features of a row a thread
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
       }
     }
     __syncwarp();
-    if (lane < p.split) mbar_arrive_cluster(cluster_addr(&read, lane));
+    if (t + stride < ntiles && lane < p.split) mbar_arrive_cluster(cluster_addr(&read, lane));
   }
   __syncwarp();
   if (p.split > 1) cluster_sync();   // no block ends while another may read its sums or arrive at its barriers
