@@ -350,7 +350,7 @@ cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int3
                               const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr,
                               cudaStream_t s);
 // The same for few rows a group (grouped_stream.cu): y = x W[g]^T, or with 8-bit integers.
-bool stream_eligible(const Grouped& c);
+bool stream_eligible(const Grouped& c, bool codes);
 cudaError_t launch_stream_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
                              const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s);
 cudaError_t launch_stream_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,

@@ -782,7 +782,7 @@ int64_t most_row_tiles(const Grouped& c) { return c.rows / kTile + std::min<int6
 cudaError_t launch_grouped_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
                               const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s) {
   if (c.rows == 0) return cudaSuccess;
-  if (stream_eligible(c)) return launch_stream_mm(c, begin, end, x, W, y, hdr, s);
+  if (stream_eligible(c, false)) return launch_stream_mm(c, begin, end, x, W, y, hdr, s);
   Params p = params_of(c, begin, end, hdr);
   if (!map_weight(&p.a, W, false, c.G, c.N, c.K) || !map_rows(p.b, x, false, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
   p.y = y;
@@ -841,7 +841,7 @@ cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int3
                               const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr,
                               cudaStream_t s) {
   if (c.rows == 0) return cudaSuccess;
-  if (stream_eligible(c)) return launch_stream_i8(c, begin, end, q, qs, Wq, Ws, y, hdr, s);
+  if (stream_eligible(c, true)) return launch_stream_i8(c, begin, end, q, qs, Wq, Ws, y, hdr, s);
   Params p = params_of(c, begin, end, hdr);
   if (!map_weight(&p.a, Wq, true, c.G, c.N, c.K) || !map_rows(p.b, q, true, c.rows, c.K, c.ldi)) return cudaErrorInvalidValue;
   p.y = y;

@@ -28,6 +28,7 @@ constexpr int kWarps = 8;                  // that multiply
 constexpr int kFeat = 16 * kWarps;         // features of a tile
 constexpr int kCols = 128;                 // bytes of a row in a stage
 constexpr int kMaxSplit = 8;               // blocks of a cluster
+constexpr int kPairRows = 256;             // rows of a tile of the pairs' kernel
 constexpr int kPitch = kFeat + 4;          // floats between the rows of the partial sums
 
 struct StreamParams {
@@ -308,9 +309,11 @@ cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, cons
     return cudaErrorInvalidValue;
   p.nst = (int)((row + kCols - 1) / kCols);
   p.nf = (c.N + kFeat - 1) / kFeat;
-  // the tiles if the rows spread evenly over the groups; at most (live + c.rows / (8 NT)) nf
+  // blocks of a cluster: as many as all fit at once (one token, 8 of 128 experts, 2048 x 768: 7.9 us, 14.7 with
+  // one block a tile).  More tiles than that only lose by the cluster's sums: 64 x 2048 x 1408, one row a group,
+  // 62 us with one block a tile, 65 with two.
   const int64_t live = std::min<int64_t>(c.G, c.rows), slots = kBlocks * (int64_t)num_sms();
-  const int64_t tiles = (live + (c.rows - live) / (8 * NT)) * p.nf;
+  const int64_t tiles = (live + (c.rows - live) / (8 * NT)) * p.nf;   // (of an even spread, with some room)
   p.split = 1;
   while (p.split < kMaxSplit && 2 * p.split * tiles <= slots && 2 * p.split <= p.nst) p.split *= 2;
   const int grid = p.split * (int)std::min<int64_t>((live + c.rows / (8 * NT)) * p.nf, slots / p.split);
@@ -327,6 +330,8 @@ cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, cons
 template <int kType>
 cudaError_t launch_type(const Grouped& c, StreamParams& p, const void* x, const void* W, int id, cudaStream_t s) {
   constexpr int size = kType == kCodes ? 1 : 2;
+  // up to 8 rows in all: tiles of 8, whose smaller stages let three blocks of an SM stream (one token as above
+  // 7.9 us, 8.5 with tiles of 32; 8-bit integers, 8 experts of 4096 x 14336, 26.0 and 28.1 us)
   return c.rows <= 8 ? launch_stream<kType, 1, 3, 3>(c, p, x, W, size, id, s)
                      : launch_stream<kType, 4, 4, 2>(c, p, x, W, size, id, s);
 }
@@ -347,7 +352,25 @@ StreamParams stream_params(const Grouped& c, const int32_t* begin, const int32_t
 
 }  // namespace
 
-bool stream_eligible(const Grouped& c) { return c.rows <= 32 * (int64_t)c.G || c.rows <= 64; }
+// Few rows a group: this kernel or the CTA pairs' of the same product.  By device time (graph replays, weights from
+// HBM; this kernel : pairs) at one average of rows a group, evenly spread, or in brackets in proportion to
+// exponential draws, where a group of more than 32 rows has its weights read again from L2:
+//   64 groups of 2048 x 1408   8 rows 62.8 : 73 us (64 : 62)   16 rows 66 : 73 (72 : 63)   32 rows 74 : 75 (90 : 65)
+//     8-bit integers           8 rows 39 : 82 (50 : 71)        16 rows 47 : 82 (72 : 73)   32 rows 67 : 82 (90 : 76)
+//   8 groups of 4096 x 14336   8 rows 137 : 145 (138 : 146)    16 rows 139 : 146 (148 : 146)
+//     8-bit integers           16 rows 98 : 150 (119 : 150)    32 rows 144 : 150 (219 : 154)
+// so 8 rows a group on average, 16 with 8-bit integers.  Where the tiles are few, this kernel fills the GPU by its
+// split of the contraction and the pairs do not:
+//   64 tiles   4096 x 4096, 64 rows 17 : 23 (integers 17 : 30)     768 x 2048, 128 rows 8.2 : 8.8 (8.6 : 12.5)
+//   88 tiles   2048 x 1408, 256 rows 17 : 15 (17.5 : 22.6)         44 tiles   the same, 128 rows 11 : 14 (11 : 20)
+//   128 tiles  4096 x 4096, 128 rows 28 : 24 (29 : 33)             224 tiles  4096 x 14336, 64 rows 49 : 27 (50 : 32)
+// so up to half a tile an SM, one with 8-bit integers, for at most the rows of one tile of the pairs.
+bool stream_eligible(const Grouped& c, bool codes) {
+  if (c.rows <= (codes ? 16 : 8) * (int64_t)c.G) return true;
+  if (c.rows > kPairRows) return false;
+  const int64_t live = std::min<int64_t>(c.G, c.rows), per = (c.rows + live - 1) / live;   // spread evenly
+  return live * ((per + 31) / 32) * ((c.N + kFeat - 1) / kFeat) <= num_sms() / (codes ? 1 : 2);
+}
 
 cudaError_t launch_stream_mm(const Grouped& c, const int32_t* begin, const int32_t* end, const uint16_t* x,
                              const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s) {

@@ -341,11 +341,11 @@ def test_repeats_streams_and_graphs(moe, sizes):
     assert moe.moe_check_error(ws) == 0
 
 
-@pytest.mark.parametrize("op", ["mm", "dx", "dw", "i8"])
-def test_a_wait_that_runs_out_is_reported(moe, op):
-    """A fill of the operand ring that never comes ends in MOE_ERR_TIMEOUT, and the next call runs.  (Few
-    rows a group take a kernel that waits for nothing.)"""
-    sizes, K, N = [600, 70], 256, 256
+@pytest.mark.parametrize("op,sizes,K,N", [("mm", [600, 70], 256, 256), ("dx", [600, 70], 256, 256),
+                                          ("dw", [600, 70], 256, 256), ("i8", [600, 70], 256, 256),
+                                          ("mm", [9, 3], 2048, 2048), ("i8", [1, 1], 2048, 2048)])
+def test_a_wait_that_runs_out_is_reported(moe, op, sizes, K, N):
+    """A fill of the operand ring that never comes ends in MOE_ERR_TIMEOUT, and the next call runs."""
     begin, end, rows = layout(sizes)
     cfg = moe.grouped_config(rows, K, N, 2)
     ws = moe.grouped_workspace(cfg)
