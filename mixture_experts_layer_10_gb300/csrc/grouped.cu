@@ -603,33 +603,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
         const int kit = 2 * rk + ((team - block - 2 * rk) & (S::kTeams - 1));   // this team's next block
         const bool mine = kit < min(2 * rk + 2, kits);
         const int at = block + kit;
-        ok = wait_nap<0>(&raw[rs], (uint32_t)((rblock + rk) / S::kRaw) & 1u, limit, abort_flag) &&
-             (!mine || wait_nap<0>(&empty[team], ((uint32_t)(at / kStages) & 1u) ^ 1u, limit, abort_flag));
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, wait_nap<0>(&raw[rs], (uint32_t)((rblock + rk) / S::kRaw) & 1u, limit, abort_flag));
         if (!ok) {
           if (lane == 0) fail(kSiteGroupedStage);
           break;
         }
+        // the codes to registers, and the raw stage free before this warp waits for the stage they go to
+        uint4 v[2 * kPer];
         if (mine) {
           const uint8_t* src = raws + (size_t)rs * kStage + to + ((((kit & 1) * 4 + cq) ^ r) << 4);
-          uint8_t* dst = stages + (size_t)team * kStage + to;
-          uint4 v[2 * kPer];
 #pragma unroll
           for (int i = 0; i < 2 * kPer; ++i)
             if (i < kPer || ((i - kPer) * S::kTeam + w) * 8 < half)
               v[i] = *reinterpret_cast<const uint4*>(src + i * S::kTeam * 1024);
-#pragma unroll
-          for (int i = 0; i < 2 * kPer; ++i) {
-            if (i >= kPer && ((i - kPer) * S::kTeam + w) * 8 >= half) break;
-            uint8_t* d = dst + i * S::kTeam * 1024;
-            *reinterpret_cast<uint4*>(d + o0) = widen(v[i].x, v[i].y);
-            *reinterpret_cast<uint4*>(d + o1) = widen(v[i].z, v[i].w);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
         }
+        __syncwarp();
         if (lane == 0) mbar_arrive(&rempty[rs]);
-        if (mine && lane == 0) {
+        if (!mine) continue;
+        ok = __all_sync(0xffffffffu, wait_nap<0>(&empty[team], ((uint32_t)(at / kStages) & 1u) ^ 1u, limit, abort_flag));
+        if (!ok) {
+          if (lane == 0) fail(kSiteGroupedStage);
+          break;
+        }
+        uint8_t* dst = stages + (size_t)team * kStage + to;
+#pragma unroll
+        for (int i = 0; i < 2 * kPer; ++i) {
+          if (i >= kPer && ((i - kPer) * S::kTeam + w) * 8 >= half) break;
+          uint8_t* d = dst + i * S::kTeam * 1024;
+          *reinterpret_cast<uint4*>(d + o0) = widen(v[i].x, v[i].y);
+          *reinterpret_cast<uint4*>(d + o1) = widen(v[i].z, v[i].w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
           fence_release_smem();
           mbar_arrive_cluster_relaxed(cluster_addr(&full[team], 0));
         }
