@@ -36,7 +36,7 @@
 //
 // Measured (graph replays on inputs larger than L2): y of 16384 rows, 8 groups, 4096 x 14336, bf16: 1.04 to
 // 1.15 ms by the GPU's clock, 1.67 to 1.85 PFLOP/s, bound by the tensor cores under the power cap; with
-// 8-bit integers 1.38 ms, bound by the way of a block through the two rings.  dx and dW of 98304 rows, 64
+// 8-bit integers 1.38 ms, bound by shared memory (the codes' way in, through the widening and out to the products).  dx and dW of 98304 rows, 64
 // groups, 2048 x 1408: 0.35 and 0.36 ms, 1.6 PFLOP/s; the rest is the tiles' ends (22 K blocks and
 // fewer a tile).  fp32 dW += of 8192 rows, 128 groups, 2048 x 768: 0.27 ms, 5.5 TB/s, bound by reading and
 // writing dW.
@@ -89,7 +89,8 @@ struct Params {
   int M;                      // weight gradient: rows of a dW (n_out)
   int G, nf, mf;              // whole tiles across width; weight gradient: all tiles across width and M
   bool narrow;                // rows times a weight: there is a last, narrower tile across width
-  bool fp16, wide_a, wide_b;  // wide: one copy fetches two 64-column boxes (columns a multiple of 64)
+  bool fp16;
+  bool wide_a, wide_b;        // weight gradient: one copy fetches two 64-column boxes (columns a multiple of 64)
   bool dw_fp32, acc;
   uint32_t idesc;             // N and M as of a full tile
   Hdr* hdr;
@@ -477,8 +478,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
                 const int f = j.f0 + kBM * rank;
                 if (kOp == kMm) {
                   tma_load_3d_pair(st, ma, bar, kit * kBK, f, j.g);
-                } else if (p.wide_a) {
-                  tma_load_4d_pair(st, ma, bar, 0, kit * kBK, f / 64, j.g);
                 } else {
                   tma_load_3d_pair(st, ma, bar, f, kit * kBK, j.g);
                   tma_load_3d_pair(st + kBox, ma, bar, f + 64, kit * kBK, j.g);
@@ -585,8 +584,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     // Widen: the teams take turns at the K blocks (a raw stage holds two), each with a stage of its own; a
     // warp takes every fourth octet of rows (of the weight's 128, then of up to 128 token rows), a lane a
     // row and 16 of its codes: in the 128-byte swizzle the eight lanes of a phase touch distinct banks
-    // on both sides.  (Four teams of four warps hide the way of a block
-    // through its barriers better than two of eight: 1632 against 1920 us at 16384 rows, 4096 x 14336.)
+    // on both sides.  (Four teams of four warps hide the way of a block through its barriers better than two of
+    // eight: 1632 against 1920 us at 16384 rows, 4096 x 14336, when that was tried.)
     static_assert(kStages == S::kTeams, "a stage a team");
     constexpr int kPer = kBM / 8 / S::kTeam;
     const int team = (warp - 2 - S::kEpiWarps) / S::kTeam, w = (warp - 2 - S::kEpiWarps) % S::kTeam, r = lane & 7, cq = lane >> 3;
@@ -717,16 +716,17 @@ bool map_weight(CUtensorMap* m, const void* base, bool codes, uint64_t G, uint64
   return encode(m, codes ? k8 : k16, 3, base, dims, strides, box, kSw128);
 }
 
-// Weights [G, N, K] read MN-major (K contiguous): 64 x 64 boxes, two at a time when K allows (the columns
-// seen as blocks of 64 would reach past the last row otherwise).
-bool map_weight_mn(CUtensorMap* m, const void* base, uint64_t G, uint64_t N, uint64_t K, bool wide) {
-  if (wide) return map_mn2_g(m, base, K, N, G);
+// Weights [G, N, K] read MN-major (K contiguous): boxes of 64 x 64.
+bool map_weight_mn(CUtensorMap* m, const void* base, uint64_t G, uint64_t N, uint64_t K) {
   const cuuint64_t dims[3] = {K, N, G}, strides[2] = {K * 2, K * N * 2};
   const cuuint32_t box[3] = {64, 64, 1};
   return encode(m, k16, 3, base, dims, strides, box, kSw128);
 }
 
-// Rows [rows, width] read MN-major (width contiguous): likewise.
+// Rows [rows, width] read MN-major (width contiguous): likewise, or two boxes at a time where the width allows (the
+// columns seen as blocks of 64 would reach past the last row otherwise).  dW reads both operands so, and is
+// the faster by it: 98304 rows, 64 groups of 2048 x 1408, 375 us with a copy for two boxes and 411 with two
+// copies.  (dx measured the same either way and has one form.)
 bool map_rows_mn(CUtensorMap* m, const void* base, uint64_t rows, uint64_t width, uint64_t ld, bool wide) {
   if (wide) {
     const cuuint64_t dims[3] = {64, rows, width / 64}, strides[2] = {ld * 2, 128};
@@ -805,8 +805,7 @@ cudaError_t launch_grouped_dx(const Grouped& c, const int32_t* begin, const int3
                               const uint16_t* W, uint16_t* dx, Hdr* hdr, cudaStream_t s) {
   if (c.rows == 0) return cudaSuccess;
   Params p = params_of(c, begin, end, hdr);
-  p.wide_a = c.K % 64 == 0;
-  if (!map_weight_mn(&p.a, W, c.G, c.N, c.K, p.wide_a) || !map_rows(p.b, dy, false, c.rows, c.N, c.ldo))
+  if (!map_weight_mn(&p.a, W, c.G, c.N, c.K) || !map_rows(p.b, dy, false, c.rows, c.N, c.ldo))
     return cudaErrorInvalidValue;
   p.y = dx;
   p.ldy = c.ldi;
