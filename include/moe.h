@@ -389,8 +389,9 @@ moe_status_t moe_layer_bwd(const moe_config_t* cfg, const moe_bf16* x, const flo
  *
  * Numerics.  Products are exact and summed in fp32, and each output is rounded once.  NaN and
  * infinities stay within the rows (moe_grouped_mm, _dx, _i8) or the group (_dw) that hold them.
- * fp32 dW is summed 2048 rows of a group at a time, the parts added in row order; additions to it
- * (accumulate, and those parts) take subnormal values as zero.  Results are the same on every run. */
+ * dW is summed 2048 rows of a group at a time and the parts are added in fp32 in row order, whatever its
+ * type; additions to an fp32 dW (accumulate, and those parts) take subnormal values as zero.  Results
+ * are the same on every run. */
 typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
 
 typedef struct {

@@ -23,10 +23,12 @@
 // MN-major; so here too the accumulator holds a column of dW per TMEM lane and a row per column, and a warp
 // stores runs of a row (128 bytes of fp32).  Rows past the end of the group would enter the sums, so
 // every group has tensor maps of its own whose rows end where the group does (written by a small kernel
-// before: group_maps_kernel), and the copies fill the rest of its last K block with zeros.  With dW in
-// fp32 the rows go in runs of kRun (an accumulator loses up to one unit of its last place at each step of
-// 16 rows, which a long contraction would let grow past fp32's own rounding); every run after the first
-// adds to dW what the same threads stored before it.
+// before: group_maps_kernel), and the copies fill the rest of its last K block with zeros.  The rows
+// go in runs of kRun: an accumulator loses up to one unit of its last place at each step of 16 rows, always
+// towards zero, and over a whole group the losses would pass the output's own rounding (rows of one sign
+// without runs: 4.0e-4 low at 65536 rows, 6.6e-3 at 2^20, where half a step of fp16 is 4.9e-4).  With dW in
+// fp32 every run after the first adds to dW what the same threads stored before it; with dW in 16 bits the
+// epilogue's threads keep their sums in registers from run to run, and round them once.
 //
 // 8-bit integers.  sm_103a has no integer product at tensor rates (mma.sync on 8-bit integers: 256 products
 // a clock and SM, a quarter of its fp16 rate and a sixteenth of tcgen05's), but every code is exact in
@@ -60,7 +62,7 @@ constexpr uint32_t kHalf = kBM * kBK * 2;    // 16 KB: one operand of a stage
 constexpr uint32_t kBox = 64 * kBK * 2;      // 8 KB: a 64 x 64 box (MN-major)
 constexpr int kBoxes = 3;                    // row-operand boxes: 128, 64 and 32 rows
 constexpr int kChunkM = 16;                  // row tiles per L2 reuse chunk of a group
-constexpr int kRun = 2048;                   // rows of an fp32 weight-gradient run
+constexpr int kRun = 2048;                   // rows of a run of the weight gradient
 constexpr int kTmemCols = 512;
 constexpr int kAhead = 4;                    // raw stages of weights fetched to L2 ahead (8-bit integers)
 
@@ -99,7 +101,8 @@ struct Params {
 struct Job {
   int g, row, n, f0;   // rows times a weight: first row, rows, first feature
   int kits;            // K blocks
-  int k0, k, run;      // weight gradient (row, n, f0: rows and columns of dW): rows of the run, its number
+  int k0, k;           // weight gradient (row, n, f0: rows and columns of dW): rows of the run,
+  int run, runs;       // its number, of how many
 };
 
 // Rows times a weight: tile t -> group, row tile, feature tile.  Groups in order; within a group,
@@ -131,10 +134,8 @@ __device__ __forceinline__ Job row_job(const Params& p, const GroupTab& s, int t
   return j;
 }
 
-// Weight gradient: tile t -> group, tile of dW; a tile is one job a run of rows (job_runs).
-__device__ __forceinline__ int job_runs(const Params& p, int n) {
-  return p.dw_fp32 && n > kRun ? (n + kRun - 1) / kRun : 1;
-}
+// Weight gradient: tile t -> group, tile of dW; a tile is one job a run of rows.
+__device__ __forceinline__ int job_runs(int n) { return n > kRun ? (n + kRun - 1) / kRun : 1; }
 
 __device__ __forceinline__ Job dw_job(const Params& p, const GroupTab& s, int t, int run) {
   const int per = p.mf * p.nf;
@@ -146,8 +147,9 @@ __device__ __forceinline__ Job dw_job(const Params& p, const GroupTab& s, int t,
   j.f0 = r % p.nf * kTile;
   j.run = run;
   const int n = s.end[j.g] - s.begin[j.g], from = run * kRun;
+  j.runs = job_runs(n);
   j.k0 = s.begin[j.g] + from;
-  j.k = p.dw_fp32 ? min(kRun, n - from) : n;
+  j.k = min(kRun, n - from);
   j.kits = (j.k + kBK - 1) / kBK;
   return j;
 }
@@ -161,7 +163,7 @@ template <int kOp>
 struct Walk {
   const Params& p;
   const GroupTab& s;
-  int t, step, ntiles, run = 0, runs = 0;
+  int t, step, ntiles, run = 0;
   __device__ Walk(const Params& p_, const GroupTab& s_, int first, int step_, int ntiles_)
       : p(p_), s(s_), t(first), step(step_), ntiles(ntiles_) {}
   __device__ bool next(Job& j) {
@@ -173,12 +175,8 @@ struct Walk {
       return true;
     }
     if (t >= ntiles) return false;
-    if (run == 0) {
-      const int g = t / (p.mf * p.nf);
-      runs = job_runs(p, s.end[g] - s.begin[g]);
-    }
     j = dw_job(p, s, t, run);
-    if (++run == runs) {
+    if (++run == j.runs) {
       run = 0;
       t += step;
     }
@@ -201,43 +199,87 @@ __device__ __forceinline__ void add_if(float* at, float v, bool yes) {
 
 // ---- epilogues -----------------------------------------------------------------------------------
 
-// 16-bit outputs: this warp's 32 features (lanes) of the tile's rows (columns), the first row at `out`, ld
-// elements apart.  Lanes exchange with their neighbour so that each holds two features of one row: an
-// instruction stores 64 bytes of two rows.
+// 16-bit outputs: 32 rows (from c on) of this warp's 32 features, `out` at this lane's first of them.  Lanes
+// exchange with their neighbour so that each holds two features of one row: an instruction stores 64 bytes
+// of two rows.
+template <int kOp>
+__device__ __forceinline__ void emit16(const Params& p, const Job& j, uint16_t* out, int64_t ld, bool live, int lane,
+                                       int c, float ws, float qs, const float (&v)[32]) {
+  const bool odd = lane & 1;
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
+    if (kOp == kI8) {
+      a *= ws;
+      b *= ws;
+    }
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+    if (kOp == kI8) {   // this lane now has two features of row c + 2 i + odd
+      const float s = __shfl_sync(0xffffffffu, qs, 2 * i + odd);
+      w[i] = odd ? pack16(got * s, b * s, p.fp16) : pack16(a * s, got * s, p.fp16);
+    } else {
+      w[i] = odd ? pack16(got, b, p.fp16) : pack16(a, got, p.fp16);
+    }
+  }
+  const int left = live ? j.n - c - odd : 0;   // this lane's rows from c on
+#pragma unroll
+  for (int i = 0; i < 16; ++i) store_if(out + 2 * i * ld, w[i], 2 * i < left);
+}
+
+// This warp's 32 features (lanes) of the tile's rows (columns), the first row at `out`, ld elements apart.
 template <int kOp>
 __device__ __forceinline__ void store16(const Params& p, const Job& j, uint16_t* out, int64_t ld, int f, int lane,
                                         uint32_t ta, int share) {
   constexpr int kStep = 8 * Shape<kOp>::kEpiWarps;   // rows from one turn of the warp to the next
-  const bool odd = lane & 1;
   const bool live = f < p.width;   // a multiple of 8: the same for both lanes of a pair
   const float ws = kOp == kI8 && live ? p.ws[(int64_t)j.g * p.width + f] : 1.f;
-  out += (32 * share + odd) * ld + (f & ~1);
+  out += (32 * share + (lane & 1)) * ld + (f & ~1);
 #pragma unroll 1
   for (int c = 32 * share; c < j.n; c += kStep, out += kStep * ld) {
-    uint32_t v[32];
-    tmem_ld32(ta + c, v);
+    uint32_t u[32];
+    tmem_ld32(ta + c, u);
     float qs = 0.f;
     if (kOp == kI8) qs = c + lane < j.n ? p.qs[j.row + c + lane] : 0.f;
     tmem_ld_wait();
-    uint32_t w[16];
+    float v[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
-      if (kOp == kI8) {
-        a *= ws;
-        b *= ws;
-      }
-      const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-      if (kOp == kI8) {   // this lane now has two features of row c + 2 i + odd
-        const float s = __shfl_sync(0xffffffffu, qs, 2 * i + odd);
-        w[i] = odd ? pack16(got * s, b * s, p.fp16) : pack16(a * s, got * s, p.fp16);
-      } else {
-        w[i] = odd ? pack16(got, b, p.fp16) : pack16(a, got, p.fp16);
-      }
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+    emit16<kOp>(p, j, out, ld, live, lane, c, ws, qs, v);
+  }
+}
+
+// A 16-bit dW whose rows come in runs: the warp's share of the sums stays in its registers from run to run
+// and is rounded once, at the end.
+constexpr int kCarry = kTile / 64;   // 32 rows each: two warps share a lane quarter
+__device__ __forceinline__ void sum16(const Params& p, const Job& j, int rank, int q, uint32_t ta, int share,
+                                      float (&sum)[kCarry][32]) {
+  if (j.f0 + kBM * rank + 32 * q >= p.width) return;   // the whole warp lies past the last feature
+#pragma unroll
+  for (int h = 0; h < kCarry; ++h) {
+    const int c = 32 * share + 64 * h;
+#pragma unroll
+    for (int t = 0; t < 32; t += 16) {
+      if (c + t >= j.n) continue;
+      uint32_t u[16];
+      tmem_ld16(ta + c + t, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[h][t + i] += __uint_as_float(u[i]);
     }
-    const int left = live ? j.n - c - odd : 0;   // this lane's rows from c on
+  }
+}
+
+__device__ __forceinline__ void store_sum16(const Params& p, const Job& j, int rank, int q, int lane, int share,
+                                            float (&sum)[kCarry][32]) {
+  const int f0 = j.f0 + kBM * rank + 32 * q, f = f0 + lane;
+  if (f0 >= p.width) return;
+  uint16_t* out = static_cast<uint16_t*>(p.y) + ((int64_t)j.g * p.M + j.row + 32 * share + (lane & 1)) * p.width + (f & ~1);
+  const int64_t step = 64 * (int64_t)p.width;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) store_if(out + 2 * i * ld, w[i], 2 * i < left);
+  for (int h = 0; h < kCarry; ++h, out += step) {
+    const int c = 32 * share + 64 * h;
+    if (c < j.n) emit16<kDw>(p, j, out, p.width, f < p.width, lane, c, 1.f, 0.f, sum[h]);
   }
 }
 
@@ -553,6 +595,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     const int share = (warp - 2) / 4;            // of two warps of a quarter: every other 32 rows
     int acc = 0;
     uint32_t acc_phase = 0;
+    auto wait_acc = [&]() {
+      if (!mbar_wait_idle(&tfull[acc], acc_phase, limit, abort_flag)) {
+        fail(kSiteGroupedEpilogue);
+        return false;
+      }
+      tc_fence_after();
+      return true;
+    };
+    auto acc_addr = [&]() { return tmem_base + (uint32_t)(acc * kTile) + ((uint32_t)(q * 32) << 16); };
+    auto release_acc = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      // (relaxed: the reads of the accumulator have completed, and a release would wait for the tile's stores)
+      if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[acc], 0));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    };
     Job next;
     bool more = walk.next(next);
     if (kOp == kDw && more) prefetch_dw(p, next, rank, q, lane, share);
@@ -564,21 +625,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
         store_zero(p, j, rank, q, lane, share);
         continue;
       }
-      if (!mbar_wait_idle(&tfull[acc], acc_phase, limit, abort_flag)) {
-        fail(kSiteGroupedEpilogue);
-        break;
+      if (kOp == kDw && !p.dw_fp32 && j.runs > 1) {
+        float sum[kCarry][32] = {};
+        bool ok = true;
+        while (true) {
+          ok = wait_acc();
+          if (!ok) break;
+          sum16(p, j, rank, q, acc_addr(), share, sum);
+          release_acc();
+          if (j.run == j.runs - 1) break;
+          j = next;   // (the next run)
+          more = walk.next(next);
+        }
+        if (!ok) break;
+        store_sum16(p, j, rank, q, lane, share, sum);
+        continue;
       }
-      tc_fence_after();
-      const uint32_t ta = tmem_base + (uint32_t)(acc * kTile) + ((uint32_t)(q * 32) << 16);
-      store_tile<kOp>(p, j, rank, q, lane, ta, share);
-      tc_fence_before();
-      __syncwarp();
-      // (relaxed: the reads of the accumulator have completed, and a release would wait for the tile's stores)
-      if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[acc], 0));
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1;
-      }
+      if (!wait_acc()) break;
+      store_tile<kOp>(p, j, rank, q, lane, acc_addr(), share);
+      release_acc();
     }
   } else if constexpr (kOp == kI8) {
     // Widen: the teams take turns at the K blocks (a raw stage holds two), each with a stage of its own; a

@@ -1,0 +1,47 @@
+"""Grouped products (GPU) where sums are long: rows or columns by the ten thousand.
+
+A tensor-core accumulator drops up to one unit of its last place, 2^-23 of the running sum, at each step of
+16 products, always towards zero, so with values of one sign the losses add up.  A weight gradient is summed
+2048 rows at a time (128 steps) and the parts are added in fp32, rounded to nearest (2^-24 each).
+"""
+import pytest
+import torch
+
+from test_grouped import TYPES, dev_i32
+
+pytestmark = pytest.mark.gpu
+
+
+def positive(shape, dtype, seed, scale):
+    """Values of one sign in [scale / 2, scale]."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    return (torch.rand(shape, generator=g, device="cuda") * 0.5 + 0.5).mul_(scale).to(dtype)
+
+
+@pytest.mark.parametrize("rows", [[2049], [65536, 3, 16384], [262144]])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_long_group_16bit_weight_gradient(moe, dtype, rows):
+    """dW in the operands' type over many rows of one sign: each output within half a step of its type and
+    the sums' own error of 64 bits, and no bias of all outputs together."""
+    t = TYPES[dtype]
+    K, N, n, G = 72, 136, sum(rows), len(rows)
+    begin = [sum(rows[:g]) for g in range(G)]
+    end = [b + r for b, r in zip(begin, rows)]
+    # columns of different size, so that the outputs lie anywhere between two 16-bit values
+    x = positive((n, K), t, 1, 4 * max(rows) ** -0.5) * torch.linspace(0.5, 1, K, device="cuda").to(t)
+    dy = positive((n, N), t, 2, 4 * max(rows) ** -0.5)
+    cfg = moe.grouped_config(n, K, N, G, dtype=t)
+    ws = moe.grouped_workspace(cfg)
+    dW = torch.empty(G, N, K, dtype=t, device="cuda")
+    moe.moe_grouped_mm_dw(cfg, dev_i32(begin), dev_i32(end), dy, x, dW, ws)
+    assert moe.moe_check_error(ws) == 0
+    eps = torch.finfo(t).eps
+    for g in range(G):
+        ref = dy[begin[g]:end[g]].double().T @ x[begin[g]:end[g]].double()
+        off = (dW[g].double() - ref) / ref
+        runs = (rows[g] + 2047) // 2048
+        sums = (128 + 1) * 2.0 ** -23 + runs * 2.0 ** -24
+        assert off.abs().max().item() <= sums + eps / 2 * (1 + sums)
+        if rows[g] > 2048:
+            # the roundings of N K outputs average out: eps / 2 / sqrt(3) each at most, five deviations
+            assert off.mean().abs().item() <= sums + 5 * eps / 2 / (3 * N * K) ** 0.5
