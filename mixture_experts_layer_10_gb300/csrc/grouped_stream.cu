@@ -9,8 +9,9 @@
 //
 // Where the tiles are fewer than the blocks that fit (one token's 8 experts x 768 features are 48), a
 // cluster of 2, 4 or 8 blocks splits the contraction of a tile, and each block adds up its share of the
-// tile's partial sums, in the order of the blocks, from the others' shared memory.  Rows of a group past
-// those of a tile make another tile, whose weights come from L2.
+// tile's partial sums, in the order of the blocks, from the others' shared memory.  A cluster has one tile
+// then: the split is chosen so that there is a cluster for every tile that the rows can make.  Rows of a
+// group past those of a tile make another tile, whose weights come from L2.
 #include <algorithm>
 
 #include "common.cuh"
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
   float* red = reinterpret_cast<float*>(ring + kDepth * kStage);   // partial sums [kRows][kPitch]
   __shared__ GroupTab tab;
   __shared__ uint64_t full[kDepth], empty[kDepth];
-  __shared__ uint64_t sums, read;   // every block's partial sums are in place; have been read
+  __shared__ uint64_t sums;   // every block's partial sums are in place
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
@@ -96,7 +97,6 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
       mbar_init(&empty[s], kWarps);
     }
     mbar_init(&sums, kWarps * p.split);
-    mbar_init(&read, kWarps * p.split);
     abort_word = 0;
     fence_mbar_init();
     tma_prefetch(&p.W);
@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
       drain_fills(full, kDepth, slot, phase, uses, limit);   // every copy lands before the block exits
     }
   }
-  uint32_t turn = 0;   // parity of the tile, for the cluster's sums
-  for (int t = first; warp < kWarps && t < ntiles; t += stride, turn ^= 1) {
+  for (int t = first; warp < kWarps && t < ntiles; t += stride) {
     const Tile j = tile_of(t);
     float acc[NT][4];
     {
@@ -180,7 +179,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
 #pragma unroll 1
       for (int s = s0; s < s1 && ok; ++s) {
         ok = __all_sync(0xffffffffu, wait_nap<0>(&full[slot], phase, limit, abort_flag));
-        if (!ok) {   // still arrives at the cluster's barriers below, so that no block waits for it in vain
+        if (!ok) {   // still arrives at the cluster's barrier below, so that no block waits for it in vain
           if (lane == 0) {
             record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedMma);
             *abort_flag = 1;
@@ -241,15 +240,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
       }
       continue;
     }
-    auto wait_sums = [&](uint64_t* bar, uint32_t parity) {
-      if (!ok) return;
-      ok = __all_sync(0xffffffffu, wait_nap<0, true>(bar, parity, limit, abort_flag));
-      if (!ok && lane == 0) {
-        record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedEpilogue);
-        *abort_flag = 1;
-      }
-    };
-    if (t != first) wait_sums(&read, turn ^ 1);
+    // the cluster's one tile (its barrier is used once)
 #pragma unroll
     for (int k = 0; k < NT; ++k)
 #pragma unroll
@@ -259,7 +250,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
       fence_release_smem();
       mbar_arrive_cluster_relaxed(cluster_addr(&sums, lane));
     }
-    wait_sums(&sums, turn);
+    if (ok) {
+      ok = __all_sync(0xffffffffu, wait_nap<0, true>(&sums, 0, limit, abort_flag));
+      if (!ok && lane == 0) {
+        record_error(p.hdr, MOE_ERR_TIMEOUT, kSiteGroupedEpilogue);
+        *abort_flag = 1;
+      }
+    }
     if (ok) {
       // two features of a row a thread
 #pragma unroll 1
@@ -282,8 +279,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
         *reinterpret_cast<uint32_t*>(p.y + (j.row0 + row) * p.ldy + f) = pack16(v.x, v.y, p.fp16);
       }
     }
-    __syncwarp();
-    if (t + stride < ntiles && lane < p.split) mbar_arrive_cluster(cluster_addr(&read, lane));
+    break;
   }
   __syncwarp();
   if (p.split > 1) cluster_sync();   // no block ends while another may read its sums or arrive at its barriers
@@ -313,10 +309,10 @@ cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, cons
   // one block a tile).  More tiles than that only lose by the cluster's sums: 64 x 2048 x 1408, one row a group,
   // 62 us with one block a tile, 65 with two.
   const int64_t live = std::min<int64_t>(c.G, c.rows), slots = kBlocks * (int64_t)num_sms();
-  const int64_t tiles = (live + (c.rows - live) / (8 * NT)) * p.nf;   // (of an even spread, with some room)
+  const int64_t tiles = (live + (c.rows - live) / (8 * NT)) * p.nf;   // the most that any spread of the rows makes
   p.split = 1;
   while (p.split < kMaxSplit && 2 * p.split * tiles <= slots && 2 * p.split <= p.nst) p.split *= 2;
-  const int grid = p.split * (int)std::min<int64_t>((live + c.rows / (8 * NT)) * p.nf, slots / p.split);
+  const int grid = (int)std::min<int64_t>(p.split * tiles, slots);   // (split > 1: a cluster a tile, see above)
   auto kernel = stream_kernel<kType, NT, kDepth, kBlocks>;
   static SmemOnce once;
   cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), smem);

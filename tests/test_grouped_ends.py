@@ -7,7 +7,7 @@ A tensor-core accumulator drops up to one unit of its last place, 2^-23 of the r
 import pytest
 import torch
 
-from test_grouped import TYPES, dev_i32
+from test_grouped import TYPES, dev_i32, layout, run_all, run_i8
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,22 @@ def test_long_group_16bit_weight_gradient(moe, dtype, rows):
         if rows[g] > 2048:
             # the roundings of N K outputs average out: eps / 2 / sqrt(3) each at most, five deviations
             assert off.mean().abs().item() <= sums + 5 * eps / 2 / (3 * N * K) ** 0.5
+
+
+# few rows a group: a cluster of blocks splits the contraction, with a tile for every cluster at most.
+# Spreads of the rows that make the most tiles of 8 or 32 rows, and the fewest.
+SPREADS = {
+    "8 rows": [[8, 0, 0, 0], [5, 1, 1, 1], [2, 2, 2, 2], [0, 0, 0, 8], [0, 0, 0, 0]],
+    "32 rows": [[32, 0, 0, 0], [29, 1, 1, 1], [0, 31, 0, 1], [8, 8, 8, 8]],
+    "200 rows": [[200, 0, 0, 0, 0, 0, 0, 0], [193, 1, 1, 1, 1, 1, 1, 1], [97, 33, 65, 1, 1, 1, 1, 1],
+                 [25, 25, 25, 25, 25, 25, 25, 25], [0, 199, 0, 0, 0, 0, 0, 1]],
+}
+
+
+@pytest.mark.parametrize("name", list(SPREADS))
+def test_few_rows_spreads(moe, name):
+    for groups in SPREADS[name]:
+        begin, end, _ = layout(groups)
+        rows = int(name.split()[0])   # of the buffer: what the call is planned for
+        run_all(moe, begin, end, rows, 2048, 136, torch.bfloat16)
+        run_i8(moe, begin, end, rows, 4096, 136, torch.float16, codes=(-32, 33))
