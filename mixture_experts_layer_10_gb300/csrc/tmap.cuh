@@ -3,26 +3,36 @@
 // operand pairs as 64-column blocks, and 8-bit (e4m3 code) tensors.  Host only.
 #pragma once
 
-#include <mutex>
-
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 namespace moe {
 
+// A driver function of the CUDA version given, or null.
+inline void* driver_fn(const char* name, unsigned version) {
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  return cudaGetDriverEntryPointByVersion(name, &ptr, version, cudaEnableDefault, &q) == cudaSuccess &&
+                 q == cudaDriverEntryPointSuccess
+             ? ptr
+             : nullptr;
+}
+
+// The driver takes the calling thread's context.  The runtime makes its own current in a thread with that
+// thread's first launch or copy, which comes after the maps: here it is made so at once.
+inline bool have_context() {
+  static const auto current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(driver_fn("cuCtxGetCurrent", 4000));
+  CUcontext ctx = nullptr;
+  if (current != nullptr && current(&ctx) == CUDA_SUCCESS && ctx != nullptr) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
+// Null where the function or a context is not to be had.
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
+  static const auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_fn("cuTensorMapEncodeTiled", 12000));
+  return fn != nullptr && have_context() ? fn : nullptr;
 }
 
 // Swizzle of a box whose inner extent is box_w bf16 elements (64 -> 128 bytes, 32 -> 64 bytes).
