@@ -1,6 +1,7 @@
 // The C ABI (include/moe.h): argument validation, workspace layout and the composition of the
 // layer's forward and backward from the kernels of route.cu, dispatch.cu, gemm.cu and combine.cu.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <mutex>
@@ -199,7 +200,7 @@ SavedLayout saved_layout(const Cfg& c) {
 }
 
 int num_sms() {
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64] = {};   // (several threads may find it at once: the same number)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     (void)cudaGetLastError();

@@ -39,6 +39,7 @@
 //              K blocks of 128 codes, row / channel scales applied in the epilogue      N=256
 //   FwdDown8   O    = sh sd (H8 Wd8^T), e4m3 operands, eight epilogue warps             N=256
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -2027,9 +2028,11 @@ template <class P>
 cudaError_t launch_pair(const typename P::Params& p, cudaStream_t s) {
   constexpr size_t smem = smem_bytes<P>();
   static_assert(smem <= 232448, "shared memory per block");
-  static int grid = 0;   // per problem type and process (all devices here are alike)
+  // per problem type and process (all devices here are alike; several threads may find it at once: the same number)
+  static std::atomic<int> found{0};
   cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  int grid = found.load(std::memory_order_relaxed);
   if (grid == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
@@ -2041,6 +2044,7 @@ cudaError_t launch_pair(const typename P::Params& p, cudaStream_t s) {
       nclusters = num_sms() / 2;
     }
     grid = 2 * std::min(nclusters, num_sms() / 2);
+    found.store(grid, std::memory_order_relaxed);
   }
   prof_mark(P::kId, s, true);
   gemm_pair_kernel<P><<<grid, threads_of<P>(), smem, s>>>(p);

@@ -822,11 +822,12 @@ Params params_of(const Grouped& c, const int32_t* begin, const int32_t* end, Hdr
 template <int kOp>
 cudaError_t launch(const Params& p, int64_t most_tiles, int id, cudaStream_t s) {
   using S = Shape<kOp>;
-  static int most = 0;   // pairs that run at once, per process (all devices here are alike)
   static SmemOnce once;
+  static IntOnce most;   // pairs that run at once
   cudaError_t e = once.set(reinterpret_cast<const void*>(grouped_kernel<kOp>), S::kSmem);
   if (e != cudaSuccess) return e;
-  if (most == 0) {
+  int fit = 0;
+  e = most.get(&fit, [] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
     cfg.blockDim = dim3(S::kThreads, 1, 1);
@@ -836,9 +837,10 @@ cudaError_t launch(const Params& p, int64_t most_tiles, int id, cudaStream_t s) 
       (void)cudaGetLastError();
       n = num_sms() / 2;
     }
-    most = std::min(n, num_sms() / 2);
-  }
-  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(most, most_tiles));
+    return std::min(n, num_sms() / 2);
+  });
+  if (e != cudaSuccess) return e;
+  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(fit, most_tiles));
   prof_mark(id, s, true);
   e = launch_after(grouped_kernel<kOp>, 2 * pairs, S::kThreads, S::kSmem, 1, s, p);   // (clusters of two: by its attribute)
   prof_mark(id, s, false);

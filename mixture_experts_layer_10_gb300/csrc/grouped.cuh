@@ -104,6 +104,25 @@ struct SmemOnce {
   }
 };
 
+// A positive number of a device, found by the first call there (of several threads at once, by each of them:
+// the answer is the same).
+struct IntOnce {
+  std::atomic<int> found[64] = {};
+  template <class F>
+  cudaError_t get(int* value, F find) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool keep = dev < 64;
+    *value = keep ? found[dev].load(std::memory_order_acquire) : 0;
+    if (*value == 0) {
+      *value = find();
+      if (keep) found[dev].store(*value, std::memory_order_release);
+    }
+    return cudaSuccess;
+  }
+};
+
 // The kernels of the grouped products are launched so that a kernel's blocks may start, as those of the
 // kernel before it in the stream end, before that one has ended altogether (programmatic dependent launch).
 // Each first waits for the kernels before it to have ended and their writes to be visible, so nothing

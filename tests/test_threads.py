@@ -1,5 +1,8 @@
 """Calls from host threads that have not used CUDA before (GPU): the library's first call in such a thread
 builds tensor maps before anything else has made a context current there."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -76,3 +79,49 @@ def test_expert_ffn(moe):
     moe.moe_expert_ffn_fwd(cfg, xp, Wg, Wu, Wd, out, buf.ws, stream)
     assert moe.moe_check_error(buf.ws) == 0
     assert bool((got != 0).any()) and torch.equal(got, out)
+
+
+FIRST_CALLS = """
+import threading, torch
+import mixture_experts_layer_10_gb300 as moe
+rows, K, N, G, n = 600, 256, 320, 2, 8
+moe.load()
+g = torch.Generator("cuda").manual_seed(1)
+x, dy, W = (torch.empty(s, device="cuda").normal_(generator=g).bfloat16() for s in ((rows, K), (rows, N), (G, N, K)))
+b, e = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 250], [250, 600]))
+cfg = moe.grouped_config(rows, K, N, G)
+outs = [[torch.zeros_like(t) for t in (dy, x, W)] for _ in range(n)]
+ws = [moe.grouped_workspace(cfg) for _ in range(n)]
+streams = [torch.cuda.Stream() for _ in range(n)]
+torch.cuda.synchronize()
+start, failed = threading.Barrier(n), []
+
+def calls(i):
+    try:
+        y, dx, dW = outs[i]
+        start.wait()
+        moe.moe_grouped_mm(cfg, b, e, x, W, y, ws[i], streams[i])
+        moe.moe_grouped_mm_dx(cfg, b, e, dy, W, dx, ws[i], streams[i])
+        moe.moe_grouped_mm_dw(cfg, b, e, dy, x, dW, ws[i], streams[i])
+        assert moe.moe_check_error(ws[i], streams[i]) == 0
+    except Exception as err:
+        failed.append(repr(err))
+
+threads = [threading.Thread(target=calls, args=(i,)) for i in range(n)]
+for t in threads: t.start()
+for t in threads: t.join()
+torch.cuda.synchronize()
+assert not failed, failed
+ref = [[x[p:q].float() @ W[i].float().T for i, (p, q) in enumerate(((0, 250), (250, 600)))]]
+assert torch.allclose(outs[0][0].float(), torch.cat(ref[0]), atol=0.5, rtol=0.02)
+for o in outs[1:]:
+    assert all(torch.equal(u, v) for u, v in zip(o, outs[0]))
+print("same")
+"""
+
+
+def test_first_calls_of_several_threads():
+    """A new process's first calls, made by eight threads at once on streams and workspaces of their own."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
