@@ -387,6 +387,9 @@ moe_status_t moe_layer_bwd(const moe_config_t* cfg, const moe_bf16* x, const flo
  * outputs are not written.  Values out of range or out of order record MOE_ERR_BAD_INDEX
  * (moe_check_error) and the call writes nothing.
  *
+ * Pointers.  Rows, weights and codes are 16-byte aligned; row_begin, row_end and the scales of 8-bit
+ * integers 4-byte aligned, so that they may be parts of larger arrays.
+ *
  * Numerics.  Products are exact and summed in fp32, and each output is rounded once.  NaN and
  * infinities stay within the rows (moe_grouped_mm, _dx, _i8) or the group (_dw) that hold them.
  * dW is summed 2048 rows of a group at a time and the parts are added in fp32 in row order, whatever its
@@ -437,7 +440,7 @@ moe_status_t moe_grouped_mm_dw(const moe_grouped_t* cfg, const int32_t* row_begi
  * scales [rows] fp32, scale = amax / 127 over the row (1 where that is zero) and code = v / scale
  * rounded to nearest even, at most 127 in magnitude, all in fp32.  A NaN or an infinity in a row
  * makes its scale NaN, and so its products.  For activations (one scale per token) and for the rows of
- * weights (one per output channel).  cols a multiple of 16, at most 65536; 16-byte-aligned pointers. */
+ * weights (one per output channel).  cols a multiple of 16, at most 65536. */
 moe_status_t moe_quantize_rows_i8(const void* src, int32_t dtype, int64_t rows, int32_t cols, int8_t* codes,
                                   float* scales, moe_stream_t stream);
 

@@ -1068,7 +1068,7 @@ moe_status_t moe_grouped_mm_dw(const moe_grouped_t* cfg, const int32_t* row_begi
 moe_status_t moe_quantize_rows_i8(const void* src, int32_t dtype, int64_t rows, int32_t cols, int8_t* codes,
                                   float* scales, moe_stream_t stream) {
   MOE_NEED((dtype == MOE_BF16 || dtype == MOE_FP16) && rows >= 0 && cols >= 16 && cols <= 65536 && cols % 16 == 0);
-  MOE_NEED(rows == 0 || (src && codes && scales && aligned16(src) && aligned16(codes) && aligned16(scales)));
+  MOE_NEED(rows == 0 || (src && codes && scales && aligned16(src) && aligned16(codes) && aligned4(scales)));
   MOE_TRY(check_device());
   MOE_CUDA(launch_quantize_rows_i8(static_cast<const uint16_t*>(src), dtype == MOE_FP16, rows, cols, codes, scales,
                                    stream));
@@ -1083,8 +1083,8 @@ moe_status_t moe_grouped_mm_i8(const moe_grouped_t* cfg, const int32_t* row_begi
   MOE_TRY(make_grouped(cfg, &c));
   MOE_NEED(c.K % 16 == 0 && c.ldi % 16 == 0);
   MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
-  MOE_NEED(Wq && W_scale && aligned16(Wq) && aligned16(W_scale) && (c.rows == 0 || (codes && scales && y)) &&
-           aligned16(codes) && aligned16(scales) && aligned16(y));
+  MOE_NEED(Wq && W_scale && aligned16(Wq) && aligned4(W_scale) && (c.rows == 0 || (codes && scales && y)) &&
+           aligned16(codes) && aligned4(scales) && aligned16(y));
   MOE_TRY(get_grouped_ws(c, ws, ws_bytes, &hdr));
   MOE_TRY(check_device());
   MOE_CUDA(launch_grouped_i8(c, row_begin, row_end, codes, scales, Wq, W_scale, static_cast<uint16_t*>(y), hdr,

@@ -272,9 +272,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(cons
         for (int s = 1; s < kMaxSplit; ++s)
           if (s < p.split) v = make_float2(v.x + part[s].x, v.y + part[s].y);
         if (kType == kCodes) {
-          const float2 ws = __ldg(reinterpret_cast<const float2*>(p.ws + (int64_t)j.g * p.N + f));
+          const float* ws = p.ws + (int64_t)j.g * p.N + f;   // (aligned as floats are)
           const float xs = p.xs[j.row0 + row];
-          v = make_float2(v.x * ws.x * xs, v.y * ws.y * xs);
+          v = make_float2(v.x * __ldg(ws) * xs, v.y * __ldg(ws + 1) * xs);
         }
         *reinterpret_cast<uint32_t*>(p.y + (j.row0 + row) * p.ldy + f) = pack16(v.x, v.y, p.fp16);
       }

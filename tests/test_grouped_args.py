@@ -98,3 +98,16 @@ def test_binding_checks_tensors():
         moe.moe_grouped_mm(c, P[0], P[1], x, P[2], P[3], ws, stream=0)
     with pytest.raises(ValueError):
         moe.grouped_config(4, 64, 64, 1, dtype=torch.float64)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="pointers that no device may be given")
+def test_scales_may_start_at_any_float(lib):
+    """Scales that are part of a larger array: refused only where they are no floats' addresses."""
+    c = cfg()
+    for i in (3, 5):
+        for off, answer in ((4, UNSUPPORTED), (8, UNSUPPORTED), (1, INVALID), (6, INVALID)):
+            a = list(P)
+            a[i] += off
+            assert lib.moe_grouped_mm_i8(ctypes.byref(c), *a, 1 << 20, None) == answer
+    for off, answer in ((4, UNSUPPORTED), (2, INVALID)):
+        assert lib.moe_quantize_rows_i8(P[0], 0, 4, 64, P[1], P[2] + off, None) == answer

@@ -7,7 +7,7 @@ A tensor-core accumulator drops up to one unit of its last place, 2^-23 of the r
 import pytest
 import torch
 
-from test_grouped import TYPES, dev_i32, layout, run_all, run_i8
+from test_grouped import TYPES, dev_i32, layout, rand, run_all, run_i8
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,27 @@ def test_few_rows_spreads(moe, name):
         rows = int(name.split()[0])   # of the buffer: what the call is planned for
         run_all(moe, begin, end, rows, 2048, 136, torch.bfloat16)
         run_i8(moe, begin, end, rows, 4096, 136, torch.float16, codes=(-32, 33))
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+def test_scales_in_a_larger_array(moe, rows):
+    """Scales that start at any float of an array: the same results to the bit, nothing written beside them."""
+    K, N, G = 256, 136, 3
+    x, W = rand((rows, K), torch.bfloat16, 1), rand((G, N, K), torch.bfloat16, 2)
+    cfg = moe.grouped_config(rows, K, N, G)
+    ws = moe.grouped_workspace(cfg)
+    b, e = dev_i32([0, 2, 4]), dev_i32([2, 4, rows])
+    q, Wq = torch.empty(rows, K, dtype=torch.int8, device="cuda"), torch.empty(G, N, K, dtype=torch.int8, device="cuda")
+    out = []
+    for at in (0, 1, 2, 3):
+        qs, Ws = torch.full((rows + 8,), 7.0, device="cuda"), torch.full((G * N + 8,), 7.0, device="cuda")
+        y = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+        s, t = qs[at:at + rows], Ws[at:at + G * N].view(G, N)
+        moe.moe_quantize_rows_i8(x, q, s)
+        moe.moe_quantize_rows_i8(W, Wq, t)
+        moe.moe_grouped_mm_i8(cfg, b, e, q, s, Wq, t, y, ws)
+        assert moe.moe_check_error(ws) == 0
+        assert bool((qs[:at] == 7).all()) and bool((qs[at + rows:] == 7).all())
+        out.append((y, s.clone(), t.clone()))
+    for other in out[1:]:
+        assert all(torch.equal(u, v) for u, v in zip(other, out[0]))
