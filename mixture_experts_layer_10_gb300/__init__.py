@@ -178,22 +178,35 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_holds = None   # kind -> the torch dtypes that hold it
+_holds = None            # kind -> the torch dtypes that hold it
+_current_device = None   # () -> index of the device that calls run on
+_current_stream = None   # index of a device -> handle of its current stream
 
 
-def _grouped_ptr(t, shape, kind, what, stride=0):
-    """Pointer of an operand of the grouped products: a CUDA tensor of this shape and type, contiguous
-    but for the rows of a matrix, which may be `stride` elements apart.  None and integers pass."""
-    global _holds
+def _bind_torch():
+    global _holds, _current_device, _current_stream
+    import torch
+    _holds = {BF16: (torch.bfloat16, torch.int16, torch.uint16), FP16: (torch.float16, torch.int16, torch.uint16),
+              FP32: (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,)}
+    if _current_device is None:
+        _current_device = torch._C._cuda_getDevice
+    _current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _grouped_ptr(t, shape, kind, what, on, stride=0):
+    """Pointer of an operand of the grouped products: a CUDA tensor of this shape and type on the device `on`
+    of the workspace (which is checked for itself), contiguous but for the rows of a matrix, which may be
+    `stride` elements apart.  None and integers pass."""
     if t is None or isinstance(t, int):
         return t
     if _holds is None:
-        import torch
-        _holds = {BF16: (torch.bfloat16, torch.int16, torch.uint16), FP16: (torch.float16, torch.int16, torch.uint16),
-                  FP32: (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,)}
-    if t.shape != shape or t.dtype not in _holds[kind] or not t.is_cuda:
+        _bind_torch()
+    at = t.get_device()   # -1: the host
+    if t.shape != shape or t.dtype not in _holds[kind] or at < 0:
         raise ValueError(f"{what}: CUDA tensor {shape} of {_holds[kind][0]} expected, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
+    if at != on >= 0:
+        raise ValueError(f"{what}: tensors on one device expected, got one on {t.device}, others on cuda:{on}")
     if stride and stride != shape[1]:
         if t.numel() and (t.stride(1) != 1 or (shape[0] > 1 and t.stride(0) != stride)):
             raise ValueError(f"{what}: rows {stride} elements apart expected, got strides {t.stride()}")
@@ -202,11 +215,28 @@ def _grouped_ptr(t, shape, kind, what, stride=0):
     return t.data_ptr()
 
 
+def _on_current(t, what):
+    """Device of t, which is the one that the call runs on (an address of another may be none there)."""
+    if _holds is None:
+        _bind_torch()
+    at = t.get_device()
+    if at < 0 or at != _current_device():
+        raise ValueError(f"{what}: a tensor on the current device expected, got one on {t.device}")
+    return at
+
+
+def _grouped_ws(ws):
+    """Pointer and size of a workspace: contiguous, on the current CUDA device."""
+    _on_current(ws, "ws")
+    return _ptr(ws), ws.nbytes
+
+
 def _stream(stream):
     if stream is None:
-        import torch
+        if _current_stream is None:
+            _bind_torch()
         # (the raw handle: a Stream object costs more than the rest of a call's marshalling)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -362,9 +392,9 @@ def moe_layer_bwd(cfg, x, W_r, b_r, W_gate, W_up, W_down, saved, dy, dx, dW_r, d
 
 def moe_segments(cfg, row_begin, row_end, ws, stream=None):
     """begin and end [E + S] int32 of the padded segments of the last moe_dispatch on ws."""
-    n = (cfg.E + cfg.n_shared,)
-    _call("moe_segments", ctypes.byref(cfg), _grouped_ptr(row_begin, n, "i32", "row_begin"),
-          _grouped_ptr(row_end, n, "i32", "row_end"), _ptr(ws), ws.numel(), _stream(stream))
+    n, on = (cfg.E + cfg.n_shared,), ws.get_device()
+    _call("moe_segments", ctypes.byref(cfg), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
+          _grouped_ptr(row_end, n, "i32", "row_end", on), *_grouped_ws(ws), _stream(stream))
 
 
 def moe_grouped_workspace_size(cfg: moe_grouped_t) -> int:
@@ -374,56 +404,59 @@ def moe_grouped_workspace_size(cfg: moe_grouped_t) -> int:
 
 
 def moe_grouped_workspace_init(cfg, ws, stream=None):
-    _call("moe_grouped_workspace_init", ctypes.byref(cfg), _ptr(ws), ws.numel(), _stream(stream))
+    _call("moe_grouped_workspace_init", ctypes.byref(cfg), *_grouped_ws(ws), _stream(stream))
 
 
 def moe_grouped_mm(cfg, row_begin, row_end, x, W, y, ws, stream=None):
     """y = x W[g]^T for the rows of every group g."""
-    c, n = cfg, (cfg.groups,)
-    _call("moe_grouped_mm", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin"),
-          _grouped_ptr(row_end, n, "i32", "row_end"), _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", c.in_stride),
-          _grouped_ptr(W, (c.groups, c.n_out, c.n_in), c.dtype, "W"),
-          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", c.out_stride), _ptr(ws), ws.numel(), _stream(stream))
+    c, n, on = cfg, (cfg.groups,), ws.get_device()
+    _call("moe_grouped_mm", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
+          _grouped_ptr(row_end, n, "i32", "row_end", on),
+          _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", on, c.in_stride),
+          _grouped_ptr(W, (c.groups, c.n_out, c.n_in), c.dtype, "W", on),
+          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws), _stream(stream))
 
 
 def moe_grouped_mm_dx(cfg, row_begin, row_end, dy, W, dx, ws, stream=None):
     """dx = dy W[g] for the rows of every group g."""
-    c, n = cfg, (cfg.groups,)
-    _call("moe_grouped_mm_dx", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin"),
-          _grouped_ptr(row_end, n, "i32", "row_end"), _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", c.out_stride),
-          _grouped_ptr(W, (c.groups, c.n_out, c.n_in), c.dtype, "W"),
-          _grouped_ptr(dx, (c.rows, c.n_in), c.dtype, "dx", c.in_stride), _ptr(ws), ws.numel(), _stream(stream))
+    c, n, on = cfg, (cfg.groups,), ws.get_device()
+    _call("moe_grouped_mm_dx", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
+          _grouped_ptr(row_end, n, "i32", "row_end", on),
+          _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", on, c.out_stride),
+          _grouped_ptr(W, (c.groups, c.n_out, c.n_in), c.dtype, "W", on),
+          _grouped_ptr(dx, (c.rows, c.n_in), c.dtype, "dx", on, c.in_stride), *_grouped_ws(ws), _stream(stream))
 
 
 def moe_grouped_mm_dw(cfg, row_begin, row_end, dy, x, dW, ws, stream=None):
     """dW[g] = dy^T x over the rows of group g; with cfg.accumulate added to dW."""
-    c, n = cfg, (cfg.groups,)
-    _call("moe_grouped_mm_dw", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin"),
-          _grouped_ptr(row_end, n, "i32", "row_end"), _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", c.out_stride),
-          _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", c.in_stride),
-          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), c.dw_dtype, "dW"), _ptr(ws), ws.numel(), _stream(stream))
+    c, n, on = cfg, (cfg.groups,), ws.get_device()
+    _call("moe_grouped_mm_dw", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
+          _grouped_ptr(row_end, n, "i32", "row_end", on),
+          _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", on, c.out_stride),
+          _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", on, c.in_stride),
+          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), c.dw_dtype, "dW", on), *_grouped_ws(ws), _stream(stream))
 
 
 def moe_quantize_rows_i8(src, codes, scales, stream=None):
     """src [.., rows, cols] bf16 or fp16 -> codes of the same shape int8, scales [.., rows] fp32."""
     cols = src.shape[-1]
     rows = src.numel() // cols if cols else 0
-    code = dtype_code(src.dtype)
-    _call("moe_quantize_rows_i8", _grouped_ptr(src, tuple(src.shape), code, "src"), code, int(rows), int(cols),
-          _grouped_ptr(codes, tuple(src.shape), "i8", "codes"),
-          _grouped_ptr(scales, tuple(src.shape[:-1]), FP32, "scales"), _stream(stream))
+    code, on = dtype_code(src.dtype), _on_current(src, "src")
+    _call("moe_quantize_rows_i8", _grouped_ptr(src, tuple(src.shape), code, "src", on), code, int(rows), int(cols),
+          _grouped_ptr(codes, tuple(src.shape), "i8", "codes", on),
+          _grouped_ptr(scales, tuple(src.shape[:-1]), FP32, "scales", on), _stream(stream))
 
 
 def moe_grouped_mm_i8(cfg, row_begin, row_end, codes, scales, Wq, W_scale, y, ws, stream=None):
     """y = (codes Wq[g]^T) scaled by the rows' and the output channels' scales."""
-    c, n = cfg, (cfg.groups,)
-    _call("moe_grouped_mm_i8", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin"),
-          _grouped_ptr(row_end, n, "i32", "row_end"),
-          _grouped_ptr(codes, (c.rows, c.n_in), "i8", "codes", c.in_stride),
-          _grouped_ptr(scales, (c.rows,), FP32, "scales"),
-          _grouped_ptr(Wq, (c.groups, c.n_out, c.n_in), "i8", "Wq"),
-          _grouped_ptr(W_scale, (c.groups, c.n_out), FP32, "W_scale"),
-          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", c.out_stride), _ptr(ws), ws.numel(), _stream(stream))
+    c, n, on = cfg, (cfg.groups,), ws.get_device()
+    _call("moe_grouped_mm_i8", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
+          _grouped_ptr(row_end, n, "i32", "row_end", on),
+          _grouped_ptr(codes, (c.rows, c.n_in), "i8", "codes", on, c.in_stride),
+          _grouped_ptr(scales, (c.rows,), FP32, "scales", on),
+          _grouped_ptr(Wq, (c.groups, c.n_out, c.n_in), "i8", "Wq", on),
+          _grouped_ptr(W_scale, (c.groups, c.n_out), FP32, "W_scale", on),
+          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws), _stream(stream))
 
 
 def moe_check_error(ws, stream=None) -> int:

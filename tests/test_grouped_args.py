@@ -111,3 +111,57 @@ def test_scales_may_start_at_any_float(lib):
             assert lib.moe_grouped_mm_i8(ctypes.byref(c), *a, 1 << 20, None) == answer
     for off, answer in ((4, UNSUPPORTED), (2, INVALID)):
         assert lib.moe_quantize_rows_i8(P[0], 0, 4, 64, P[1], P[2] + off, None) == answer
+
+
+class OnDevice:
+    """What the binding asks of a tensor, of one that lies on a CUDA device (no machine needs to have it)."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, index):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", index)
+        self.nbytes = 1 << 20
+
+    def get_device(self):
+        return self.device.index
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        return 0x10000
+
+
+def test_operands_lie_on_the_current_device(monkeypatch):
+    """Operands and the workspace: on a CUDA device, and on the one that the call runs on."""
+    monkeypatch.setattr(moe, "_current_device", lambda: 1, raising=False)
+    called = []
+    monkeypatch.setattr(moe, "_call", lambda name, *args: called.append(name))
+    c, bf = cfg(), torch.bfloat16
+    args = {"begin": ((4,), torch.int32), "end": ((4,), torch.int32), "x": ((100, 64), bf), "W": ((4, 128, 64), bf),
+            "y": ((100, 128), bf), "ws": ((1 << 20,), torch.uint8)}
+
+    def call(**index):
+        moe.moe_grouped_mm(c, *(OnDevice(*a, index.get(k, 1)) for k, a in args.items()), stream=0)
+
+    call()
+    assert called == ["moe_grouped_mm"]
+    with pytest.raises(ValueError, match="ws: "):
+        call(**dict.fromkeys(args, 0))   # all on one device, and not the current one
+    with pytest.raises(ValueError, match="src: "):
+        moe.moe_quantize_rows_i8(OnDevice((100, 64), bf, 0), OnDevice((100, 64), torch.int8, 0),
+                                 OnDevice((100,), torch.float32, 0), stream=0)
+    for k in args:
+        with pytest.raises(ValueError, match="device"):
+            call(**{k: 0})
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)   # the host's
+    on = [OnDevice(*a, 1) for k, a in args.items() if k != "ws"]
+    with pytest.raises(ValueError, match="ws: "):
+        moe.moe_grouped_mm(c, *on, ws, stream=0)
+    with pytest.raises(ValueError, match="ws: "):
+        moe.moe_grouped_workspace_init(c, ws, stream=0)
+    with pytest.raises(ValueError, match="ws: "):
+        moe.moe_segments(moe.config(T=64, d=128, f=256, E=4, k=2), *on[:2], ws, stream=0)
+    assert called == ["moe_grouped_mm"]
