@@ -187,7 +187,7 @@ def _bind_torch():
     global _holds, _current_device, _current_stream
     import torch
     _holds = {BF16: (torch.bfloat16, torch.int16, torch.uint16), FP16: (torch.float16, torch.int16, torch.uint16),
-              FP32: (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,)}
+              "f32": (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,)}
     if _current_device is None:
         _current_device = torch._C._cuda_getDevice
     _current_stream = torch._C._cuda_getCurrentRawStream
@@ -202,8 +202,9 @@ def _grouped_ptr(t, shape, kind, what, on, stride=0):
     if _holds is None:
         _bind_torch()
     at = t.get_device()   # -1: the host
-    if t.shape != shape or t.dtype not in _holds[kind] or at < 0:
-        raise ValueError(f"{what}: CUDA tensor {shape} of {_holds[kind][0]} expected, got {tuple(t.shape)} {t.dtype} "
+    holds = _holds.get(kind, (t.dtype,))   # (a type that is none is the library's to refuse)
+    if t.shape != shape or t.dtype not in holds or at < 0:
+        raise ValueError(f"{what}: CUDA tensor {shape} of {holds[0]} expected, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
     if at != on >= 0:
         raise ValueError(f"{what}: tensors on one device expected, got one on {t.device}, others on cuda:{on}")
@@ -434,7 +435,8 @@ def moe_grouped_mm_dw(cfg, row_begin, row_end, dy, x, dW, ws, stream=None):
           _grouped_ptr(row_end, n, "i32", "row_end", on),
           _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", on, c.out_stride),
           _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", on, c.in_stride),
-          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), c.dw_dtype, "dW", on), *_grouped_ws(ws), _stream(stream))
+          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), "f32" if c.dw_dtype == FP32 else c.dw_dtype, "dW", on),
+          *_grouped_ws(ws), _stream(stream))
 
 
 def moe_quantize_rows_i8(src, codes, scales, stream=None):
@@ -444,7 +446,7 @@ def moe_quantize_rows_i8(src, codes, scales, stream=None):
     code, on = dtype_code(src.dtype), _on_current(src, "src")
     _call("moe_quantize_rows_i8", _grouped_ptr(src, tuple(src.shape), code, "src", on), code, int(rows), int(cols),
           _grouped_ptr(codes, tuple(src.shape), "i8", "codes", on),
-          _grouped_ptr(scales, tuple(src.shape[:-1]), FP32, "scales", on), _stream(stream))
+          _grouped_ptr(scales, tuple(src.shape[:-1]), "f32", "scales", on), _stream(stream))
 
 
 def moe_grouped_mm_i8(cfg, row_begin, row_end, codes, scales, Wq, W_scale, y, ws, stream=None):
@@ -453,9 +455,9 @@ def moe_grouped_mm_i8(cfg, row_begin, row_end, codes, scales, Wq, W_scale, y, ws
     _call("moe_grouped_mm_i8", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
           _grouped_ptr(row_end, n, "i32", "row_end", on),
           _grouped_ptr(codes, (c.rows, c.n_in), "i8", "codes", on, c.in_stride),
-          _grouped_ptr(scales, (c.rows,), FP32, "scales", on),
+          _grouped_ptr(scales, (c.rows,), "f32", "scales", on),
           _grouped_ptr(Wq, (c.groups, c.n_out, c.n_in), "i8", "Wq", on),
-          _grouped_ptr(W_scale, (c.groups, c.n_out), FP32, "W_scale", on),
+          _grouped_ptr(W_scale, (c.groups, c.n_out), "f32", "W_scale", on),
           _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws), _stream(stream))
 
 

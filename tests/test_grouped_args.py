@@ -165,3 +165,15 @@ def test_operands_lie_on_the_current_device(monkeypatch):
     with pytest.raises(ValueError, match="ws: "):
         moe.moe_segments(moe.config(T=64, d=128, f=256, E=4, k=2), *on[:2], ws, stream=0)
     assert called == ["moe_grouped_mm"]
+
+
+@pytest.mark.parametrize("over", [dict(dtype=7), dict(dw_dtype=9), dict(dtype=2)])
+def test_unknown_types_are_the_librarys_to_refuse(monkeypatch, over):
+    """A description with a type that is none gets the library's answer from the binding, as from C."""
+    monkeypatch.setattr(moe, "_current_device", lambda: 1)
+    c, bf = cfg(**over), torch.bfloat16
+    b, ws = OnDevice((4,), torch.int32, 1), OnDevice((1 << 20,), torch.uint8, 1)
+    x, dy, dW = OnDevice((100, 64), bf, 1), OnDevice((100, 128), bf, 1), OnDevice((4, 128, 64), bf, 1)
+    with pytest.raises(moe.MoEError) as e:
+        moe.moe_grouped_mm_dw(c, b, b, dy, x, dW, ws, stream=0)
+    assert e.value.code == INVALID
