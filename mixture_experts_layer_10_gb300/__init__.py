@@ -435,7 +435,7 @@ def moe_grouped_mm_dw(cfg, row_begin, row_end, dy, x, dW, ws, stream=None):
           _grouped_ptr(row_end, n, "i32", "row_end", on),
           _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", on, c.out_stride),
           _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", on, c.in_stride),
-          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), "f32" if c.dw_dtype == FP32 else c.dw_dtype, "dW", on),
+          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), "f32" if c.dw_dtype == FP32 != c.dtype else c.dw_dtype, "dW", on),
           *_grouped_ws(ws), _stream(stream))
 
 
