@@ -390,11 +390,15 @@ moe_status_t moe_layer_bwd(const moe_config_t* cfg, const moe_bf16* x, const flo
  * Pointers.  Rows, weights and codes are 16-byte aligned; row_begin, row_end and the scales of 8-bit
  * integers 4-byte aligned, so that they may be parts of larger arrays.
  *
- * Numerics.  Products are exact and summed in fp32, and each output is rounded once.  NaN and
- * infinities stay within the rows (moe_grouped_mm, _dx, _i8) or the group (_dw) that hold them.
- * dW is summed 2048 rows of a group at a time and the parts are added in fp32 in row order, whatever its
- * type; additions to an fp32 dW (accumulate, and those parts) take subnormal values as zero.  Results
- * are the same on every run. */
+ * Numerics.  Products are exact and summed in fp32 by the tensor cores, and each output is rounded once.
+ * At every 16 products the tensor cores drop up to a unit of the sum's last place, towards zero.  So y and
+ * dx are off by at most n_in / 16 (n_out / 16) x 2^-23 of the sum of the products' magnitudes before they
+ * are rounded: 2^-14 at 8192 columns, 2^-11, half a step of fp16, at 65536 (values of one sign: 4.2e-4 low
+ * there, 1.0e-4 at 16384; values of both signs far less).  dW, over any number of rows, is summed 2048
+ * rows of a group at a time (2^-16) and the parts are added in fp32 in row order, whatever its type;
+ * additions to an fp32 dW (accumulate, and those parts) take subnormal values as zero.  NaN and infinities
+ * stay within the rows (moe_grouped_mm, _dx, _i8) or the group (_dw) that hold them.  Results are the same
+ * on every run. */
 typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
 
 typedef struct {
@@ -438,15 +442,18 @@ moe_status_t moe_grouped_mm_dw(const moe_grouped_t* cfg, const int32_t* row_begi
 
 /* Rows of 8-bit integers: src [rows, cols] (dtype MOE_BF16 or MOE_FP16) -> codes [rows, cols] and
  * scales [rows] fp32, scale = amax / 127 over the row (1 where that is zero) and code = v / scale
- * rounded to nearest even, at most 127 in magnitude, all in fp32.  A NaN or an infinity in a row
- * makes its scale NaN, and so its products.  For activations (one scale per token) and for the rows of
- * weights (one per output channel).  cols a multiple of 16, at most 65536. */
+ * rounded to nearest even, at most 127 in magnitude, all in fp32 with IEEE division.  (A value of half the
+ * row's largest lies between the codes 63 and 64; the scale's rounding decides, so another way to divide
+ * by 127 may give the other one.)  A NaN or an infinity in a row makes its scale NaN, and so its products.
+ * For activations (one scale per token) and for the rows of weights (one per output channel).  cols a
+ * multiple of 16, at most 65536. */
 moe_status_t moe_quantize_rows_i8(const void* src, int32_t dtype, int64_t rows, int32_t cols, int8_t* codes,
                                   float* scales, moe_stream_t stream);
 
 /* codes [rows, n_in] int8, scales [rows] fp32, Wq [groups, n_out, n_in] int8, W_scale [groups, n_out]
  * fp32 -> y [rows, n_out] (dtype).  n_in a multiple of 16.  One group is a dense product.  The sums of
- * integer products are exact up to 2^24 in magnitude and rounded as fp32 sums beyond it. */
+ * integer products are exact up to 2^24 in magnitude; beyond it they lose what the sums of
+ * moe_grouped_mm lose. */
 moe_status_t moe_grouped_mm_i8(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
                                const int8_t* codes, const float* scales, const int8_t* Wq, const float* W_scale,
                                void* y, void* ws, size_t ws_bytes, moe_stream_t stream);

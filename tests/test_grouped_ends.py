@@ -88,3 +88,33 @@ def test_scales_in_a_larger_array(moe, rows):
         out.append((y, s.clone(), t.clone()))
     for other in out[1:]:
         assert all(torch.equal(u, v) for u, v in zip(other, out[0]))
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_widest_contraction(moe, dtype, rows):
+    """65536 columns of one sign, on few rows and on many: y, dx and 8-bit products lose at most 2^-23 of the
+    sum at each 16 products, and one rounding of the type."""
+    t, L, N = TYPES[dtype], 65536, 136
+    steps = (L // 16 + 1) * 2.0 ** -23
+    eps = torch.finfo(t).eps
+    x = positive((rows, L), t, 1, 4 * L ** -0.5)
+    W = positive((N, L), t, 2, 4 * L ** -0.5) * torch.linspace(0.5, 1, N, device="cuda").to(t)[:, None]
+    b, e = dev_i32([0]), dev_i32([rows])
+    ref = x.double() @ W.double().T
+    wide, back = moe.grouped_config(rows, L, N, 1, dtype=t), moe.grouped_config(rows, N, L, 1, dtype=t)
+    ws = moe.grouped_workspace(wide)
+    y, dx = (torch.empty(rows, N, dtype=t, device="cuda") for _ in range(2))
+    moe.moe_grouped_mm(wide, b, e, x, W[None], y, ws)
+    moe.moe_grouped_mm_dx(back, b, e, x, W.T.contiguous()[None], dx, ws)
+    assert moe.moe_check_error(ws) == 0
+    for out in (y, dx):
+        assert ((out.double() - ref) / ref).abs().max().item() <= steps + eps / 2 * (1 + steps)
+    q, P = ((positive(s, torch.float32, i, 127)).round().to(torch.int8) for i, s in ((3, (rows, L)), (4, (1, N, L))))
+    qs = torch.linspace(0.5, 1, rows, device="cuda") * 2.0 ** -14
+    Ps = torch.linspace(0.5, 1, N, device="cuda")[None] * 2.0 ** -14
+    moe.moe_grouped_mm_i8(wide, b, e, q, qs, P, Ps, y, ws)
+    assert moe.moe_check_error(ws) == 0
+    ref = q.double() @ P[0].double().T * qs.double()[:, None] * Ps.double()
+    before = steps + 3 * 2.0 ** -24
+    assert ((y.double() - ref) / ref).abs().max().item() <= before + eps / 2 * (1 + before)
