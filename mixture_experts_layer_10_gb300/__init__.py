@@ -202,11 +202,11 @@ def _grouped_ptr(t, shape, kind, what, on, stride=0):
     if _holds is None:
         _bind_torch()
     at = t.get_device()   # -1: the host
-    holds = _holds.get(kind, (t.dtype,))   # (a type that is none is the library's to refuse)
-    if t.shape != shape or t.dtype not in holds or at < 0:
-        raise ValueError(f"{what}: CUDA tensor {shape} of {holds[0]} expected, got {tuple(t.shape)} {t.dtype} "
-                         f"on {t.device}")
-    if at != on >= 0:
+    holds = _holds.get(kind)   # None: a type that is none, the library's to refuse
+    if t.shape != shape or at < 0 or (holds and t.dtype not in holds):
+        raise ValueError(f"{what}: CUDA tensor {shape} of {holds[0] if holds else 'any type'} expected, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if at != on and on >= 0:
         raise ValueError(f"{what}: tensors on one device expected, got one on {t.device}, others on cuda:{on}")
     if stride and stride != shape[1]:
         if t.numel() and (t.stride(1) != 1 or (shape[0] > 1 and t.stride(0) != stride)):
@@ -216,20 +216,18 @@ def _grouped_ptr(t, shape, kind, what, on, stride=0):
     return t.data_ptr()
 
 
-def _on_current(t, what):
-    """Device of t, which is the one that the call runs on (an address of another may be none there)."""
+def _on_current(on, t, what):
+    """t's device `on` is the one that the call runs on (an address of another may be none there)."""
     if _holds is None:
         _bind_torch()
-    at = t.get_device()
-    if at < 0 or at != _current_device():
+    if on < 0 or on != _current_device():
         raise ValueError(f"{what}: a tensor on the current device expected, got one on {t.device}")
-    return at
 
 
-def _grouped_ws(ws):
-    """Pointer and size of a workspace: contiguous, on the current CUDA device."""
-    _on_current(ws, "ws")
-    return _ptr(ws), ws.nbytes
+def _grouped_ws(ws, on, stream):
+    """Pointer and size of a workspace on device `on`, and the stream of the call."""
+    _on_current(on, ws, "ws")
+    return _ptr(ws), ws.nbytes, _current_stream(on) if stream is None else _stream(stream)
 
 
 def _stream(stream):
@@ -395,7 +393,7 @@ def moe_segments(cfg, row_begin, row_end, ws, stream=None):
     """begin and end [E + S] int32 of the padded segments of the last moe_dispatch on ws."""
     n, on = (cfg.E + cfg.n_shared,), ws.get_device()
     _call("moe_segments", ctypes.byref(cfg), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
-          _grouped_ptr(row_end, n, "i32", "row_end", on), *_grouped_ws(ws), _stream(stream))
+          _grouped_ptr(row_end, n, "i32", "row_end", on), *_grouped_ws(ws, on, stream))
 
 
 def moe_grouped_workspace_size(cfg: moe_grouped_t) -> int:
@@ -405,7 +403,7 @@ def moe_grouped_workspace_size(cfg: moe_grouped_t) -> int:
 
 
 def moe_grouped_workspace_init(cfg, ws, stream=None):
-    _call("moe_grouped_workspace_init", ctypes.byref(cfg), *_grouped_ws(ws), _stream(stream))
+    _call("moe_grouped_workspace_init", ctypes.byref(cfg), *_grouped_ws(ws, ws.get_device(), stream))
 
 
 def moe_grouped_mm(cfg, row_begin, row_end, x, W, y, ws, stream=None):
@@ -415,7 +413,7 @@ def moe_grouped_mm(cfg, row_begin, row_end, x, W, y, ws, stream=None):
           _grouped_ptr(row_end, n, "i32", "row_end", on),
           _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", on, c.in_stride),
           _grouped_ptr(W, (c.groups, c.n_out, c.n_in), c.dtype, "W", on),
-          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws), _stream(stream))
+          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws, on, stream))
 
 
 def moe_grouped_mm_dx(cfg, row_begin, row_end, dy, W, dx, ws, stream=None):
@@ -425,25 +423,26 @@ def moe_grouped_mm_dx(cfg, row_begin, row_end, dy, W, dx, ws, stream=None):
           _grouped_ptr(row_end, n, "i32", "row_end", on),
           _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", on, c.out_stride),
           _grouped_ptr(W, (c.groups, c.n_out, c.n_in), c.dtype, "W", on),
-          _grouped_ptr(dx, (c.rows, c.n_in), c.dtype, "dx", on, c.in_stride), *_grouped_ws(ws), _stream(stream))
+          _grouped_ptr(dx, (c.rows, c.n_in), c.dtype, "dx", on, c.in_stride), *_grouped_ws(ws, on, stream))
 
 
 def moe_grouped_mm_dw(cfg, row_begin, row_end, dy, x, dW, ws, stream=None):
     """dW[g] = dy^T x over the rows of group g; with cfg.accumulate added to dW."""
     c, n, on = cfg, (cfg.groups,), ws.get_device()
+    kind = "f32" if c.dw_dtype == FP32 and c.dtype != FP32 else c.dw_dtype
     _call("moe_grouped_mm_dw", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
           _grouped_ptr(row_end, n, "i32", "row_end", on),
           _grouped_ptr(dy, (c.rows, c.n_out), c.dtype, "dy", on, c.out_stride),
           _grouped_ptr(x, (c.rows, c.n_in), c.dtype, "x", on, c.in_stride),
-          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), "f32" if c.dw_dtype == FP32 != c.dtype else c.dw_dtype, "dW", on),
-          *_grouped_ws(ws), _stream(stream))
+          _grouped_ptr(dW, (c.groups, c.n_out, c.n_in), kind, "dW", on), *_grouped_ws(ws, on, stream))
 
 
 def moe_quantize_rows_i8(src, codes, scales, stream=None):
     """src [.., rows, cols] bf16 or fp16 -> codes of the same shape int8, scales [.., rows] fp32."""
     cols = src.shape[-1]
     rows = src.numel() // cols if cols else 0
-    code, on = dtype_code(src.dtype), _on_current(src, "src")
+    code, on = dtype_code(src.dtype), src.get_device()
+    _on_current(on, src, "src")
     _call("moe_quantize_rows_i8", _grouped_ptr(src, tuple(src.shape), code, "src", on), code, int(rows), int(cols),
           _grouped_ptr(codes, tuple(src.shape), "i8", "codes", on),
           _grouped_ptr(scales, tuple(src.shape[:-1]), "f32", "scales", on), _stream(stream))
@@ -458,7 +457,7 @@ def moe_grouped_mm_i8(cfg, row_begin, row_end, codes, scales, Wq, W_scale, y, ws
           _grouped_ptr(scales, (c.rows,), "f32", "scales", on),
           _grouped_ptr(Wq, (c.groups, c.n_out, c.n_in), "i8", "Wq", on),
           _grouped_ptr(W_scale, (c.groups, c.n_out), "f32", "W_scale", on),
-          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws), _stream(stream))
+          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws, on, stream))
 
 
 def moe_check_error(ws, stream=None) -> int:
