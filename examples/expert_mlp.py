@@ -4,7 +4,8 @@ layer's routing, from the grouped products:
 * ``train_step``: forward and backward on packed rows (the dispatch's exact offsets), the weight
   gradients added to fp32 accumulators;
 * ``serve``: the same MLP with 8-bit weights and activations on the dispatch's padded rows
-  (``moe_segments``), for any number of tokens down to one.
+  (``moe_segments``), for any number of tokens down to one (the products' kernel is chosen by the rows of
+  the buffer, so that a few tokens on padded rows take the kernel of many).
 
     python examples/expert_mlp.py [--tokens T]
 

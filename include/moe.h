@@ -385,7 +385,9 @@ moe_status_t moe_layer_bwd(const moe_config_t* cfg, const moe_bf16* x, const flo
  * at any row, and rows between groups belong to none.  The offsets [groups + 1] of packed groups serve
  * as both arrays (row_end = offsets + 1).  Rows of no group are not read into any product and their
  * outputs are not written.  Values out of range or out of order record MOE_ERR_BAD_INDEX
- * (moe_check_error) and the call writes nothing.
+ * (moe_check_error) and the call writes nothing.  (A product of no rows writes nothing and looks at no
+ * group; moe_grouped_mm_dw looks at them.)  The buffer's rows choose the kernel: few rows a group are
+ * fastest in a buffer of their own number.
  *
  * Pointers.  Rows, weights and codes are 16-byte aligned; row_begin, row_end and the scales of 8-bit
  * integers 4-byte aligned, so that they may be parts of larger arrays.

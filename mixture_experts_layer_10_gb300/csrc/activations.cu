@@ -260,8 +260,10 @@ __global__ void col_scales_kernel(const uint32_t* __restrict__ amax_bits, float*
 // a row of 2048 takes one warp and no barrier.  The maximum is found on pairs in the values' own type,
 // which is exact.  The quotient from the row's reciprocal (div_by_scale's steps) is the correctly rounded
 // one wherever the code is not zero.  A row with a NaN or an infinity gets a NaN scale and zero codes, which
-// make its products NaN.  Measured on bf16: 16384 x 4096 in 30.2 us (6.7 TB/s), 24576 x 2048 in 23.4 us (6.5),
-// one row in 2.2 us; with four vectors a thread 31.3, 24.4 and 1.9 us.  Bound by HBM.
+// make its products NaN.  Measured on bf16: 16384 x 4096 in 30.4 us (6.6 TB/s), 24576 x 2048 in 23.0 us (6.6),
+// one row of 2048 in 1.8 us; with four vectors a thread 31.3, 24.4 and 1.9 us.  Bound by HBM from 2048 columns
+// on; narrower rows by the start of a block a row, about 0.5 ns each: 49152 x 1024 in 27 us (5.6 TB/s), 98304 x
+// 512 in 51 us (3.0), 393216 x 128 in 199 us (0.8).
 
 __device__ __forceinline__ void unpack8(const uint4& u, bool fp16, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};

@@ -36,12 +36,15 @@
 // and their fp32 sums are exact up to 2^24.  TMA brings the codes as bytes to a ring of raw stages, and
 // sixteen warps widen them into the ring that the tensor cores read.
 //
-// Measured (graph replays on inputs larger than L2): y of 16384 rows, 8 groups, 4096 x 14336, bf16: 1.04 to
-// 1.15 ms by the GPU's clock, 1.67 to 1.85 PFLOP/s, bound by the tensor cores under the power cap; with
-// 8-bit integers 1.38 ms, bound by shared memory (the codes' way in, through the widening and out to the products).  dx and dW of 98304 rows, 64
-// groups, 2048 x 1408: 0.35 and 0.36 ms, 1.6 PFLOP/s; the rest is the tiles' ends (22 K blocks and
-// fewer a tile).  fp32 dW += of 8192 rows, 128 groups, 2048 x 768: 0.27 ms, 5.5 TB/s, bound by reading and
-// writing dW.
+// Measured (graph replays on inputs larger than L2; 36 launches / after three seconds of them, when the power
+// cap has lowered the clock): y of 16384 rows, 8 groups, 4096 x 14336, bf16: 1.14 / 1.19 ms, 1.69 / 1.62
+// PFLOP/s, bound by the tensor cores under the power cap; with 8-bit integers 1.38 / 1.39 ms, bound by
+// shared memory (the codes' way in, through the widening and out to the products).  dx and dW of 98304 rows,
+// 64 groups, 2048 x 1408: 0.35 and 0.37 / 0.41 and 0.43 ms, 1.61 and 1.51 / 1.39 and 1.32 PFLOP/s; the rest is
+// the tiles' ends (22 K blocks and fewer a tile).  fp32 dW += of 8192 rows, 128 groups, 2048 x 768: 0.27 ms,
+// 5.5 TB/s, bound by reading and writing dW.  The contraction of a tile is one pair's: few tiles of a long one
+// leave the other pairs idle (dW of one group, 65536 rows, 128 x 128: one tile, 294 us; y of 300 rows,
+// 14336 to 512: four, 67 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -250,7 +253,8 @@ __device__ __forceinline__ void store16(const Params& p, const Job& j, uint16_t*
 }
 
 // A 16-bit dW whose rows come in runs: the warp's share of the sums stays in its registers from run to run
-// and is rounded once, at the end.
+// and is rounded once, at the end.  (8 groups of 12288 rows, 2048 x 1408: 373 us, 359 with one accumulator
+// over each group; groups of up to 2048 rows the same.)
 constexpr int kCarry = kTile / 64;   // 32 rows each: two warps share a lane quarter
 __device__ __forceinline__ void sum16(const Params& p, const Job& j, int rank, int q, uint32_t ta, int share,
                                       float (&sum)[kCarry][32]) {
@@ -274,7 +278,8 @@ __device__ __forceinline__ void store_sum16(const Params& p, const Job& j, int r
                                             float (&sum)[kCarry][32]) {
   const int f0 = j.f0 + kBM * rank + 32 * q, f = f0 + lane;
   if (f0 >= p.width) return;
-  uint16_t* out = static_cast<uint16_t*>(p.y) + ((int64_t)j.g * p.M + j.row + 32 * share + (lane & 1)) * p.width + (f & ~1);
+  const int64_t row = (int64_t)j.g * p.M + j.row + 32 * share + (lane & 1);
+  uint16_t* out = static_cast<uint16_t*>(p.y) + row * p.width + (f & ~1);
   const int64_t step = 64 * (int64_t)p.width;
 #pragma unroll
   for (int h = 0; h < kCarry; ++h, out += step) {

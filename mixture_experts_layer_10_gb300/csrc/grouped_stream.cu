@@ -305,8 +305,8 @@ cudaError_t launch_stream(const Grouped& c, StreamParams& p, const void* x, cons
     return cudaErrorInvalidValue;
   p.nst = (int)((row + kCols - 1) / kCols);
   p.nf = (c.N + kFeat - 1) / kFeat;
-  // blocks of a cluster: as many as all fit at once (one token, 8 of 128 experts, 2048 x 768: 7.9 us, 14.7 with
-  // one block a tile).  More tiles than that only lose by the cluster's sums: 64 x 2048 x 1408, one row a group,
+  // blocks of a cluster: as many as all fit at once (one token, 8 of 128 experts, 2048 x 768: 7.7 us, 14.3 with
+  // one block a tile; 37 rows, 8-bit integers, 4096 x 4096: 16.9 and 35.4).  More tiles than that only lose by the cluster's sums: 64 x 2048 x 1408, one row a group,
   // 62 us with one block a tile, 65 with two.
   const int64_t live = std::min<int64_t>(c.G, c.rows), slots = kBlocks * (int64_t)num_sms();
   const int64_t tiles = (live + (c.rows - live) / (8 * NT)) * p.nf;   // the most that any spread of the rows makes
@@ -327,7 +327,7 @@ template <int kType>
 cudaError_t launch_type(const Grouped& c, StreamParams& p, const void* x, const void* W, int id, cudaStream_t s) {
   constexpr int size = kType == kCodes ? 1 : 2;
   // up to 8 rows in all: tiles of 8, whose smaller stages let three blocks of an SM stream (one token as above
-  // 7.9 us, 8.5 with tiles of 32; 8-bit integers, 8 experts of 4096 x 14336, 26.0 and 28.1 us)
+  // 7.7 us, 8.4 with tiles of 32; 8-bit integers, 2 of 8 experts of 4096 x 14336, 25.0 and 28.3 us)
   return c.rows <= 8 ? launch_stream<kType, 1, 3, 3>(c, p, x, W, size, id, s)
                      : launch_stream<kType, 4, 4, 2>(c, p, x, W, size, id, s);
 }
@@ -361,6 +361,13 @@ StreamParams stream_params(const Grouped& c, const int32_t* begin, const int32_t
 //   88 tiles   2048 x 1408, 256 rows 17 : 15 (17.5 : 22.6)         44 tiles   the same, 128 rows 11 : 14 (11 : 20)
 //   128 tiles  4096 x 4096, 128 rows 28 : 24 (29 : 33)             224 tiles  4096 x 14336, 64 rows 49 : 27 (50 : 32)
 // so up to half a tile an SM, one with 8-bit integers, for at most the rows of one tile of the pairs.
+// The rule sees the rows of the buffer and the number of groups, not the lengths (they are on the device).  So
+// - all rows in one group, as many as the rule takes, are slower here, though faster than the even spread:
+//     64 groups of 2048 x 1408   512 rows 26 : 15 us   8-bit integers, 1024 rows 43 : 24
+//     8 groups of 4096 x 14336   64 rows 49 : 26 us    8-bit integers, 128 rows 95 : 33
+// - rows in a larger buffer, as the layer's dispatch lays them out (up to 255 rows of padding a group), run on the
+//   pairs however few they are: 8 rows of 8 of 128 groups, 2048 x 768, 14.7 us (8.0 packed), 8-bit 19.5 (7.9);
+//   384 rows of 64 groups, 2048 x 1408, 73 us (63), 8-bit 81 (39).
 bool stream_eligible(const Grouped& c, bool codes) {
   if (c.rows <= (codes ? 16 : 8) * (int64_t)c.G) return true;
   if (c.rows > kPairRows) return false;
