@@ -465,7 +465,8 @@ moe_status_t moe_grouped_mm_i8(const moe_grouped_t* cfg, const int32_t* row_begi
 moe_status_t moe_check_error(void* ws, moe_stream_t stream);
 
 /* Test hook: make dispatch scan block `stall_block` never publish its counts (-1: off), make the
- * first CTA pair of every expert GEMM skip its fill number `stall_fill` of the operand ring -- no
+ * first CTA pair of every expert GEMM and grouped product (of few rows: the first block) skip its
+ * fill number `stall_fill` of the operand ring -- no
  * loads, no expected bytes, so the MMA's wait for that stage never completes (-1: off) -- and bound
  * every device wait of later calls by `timeout_ns` (0: the default, 2 s).  Used to check that a
  * wait that runs out returns MOE_ERR_TIMEOUT through moe_check_error instead of hanging: the kernel
@@ -486,10 +487,11 @@ moe_status_t moe_profile_read(int32_t kernel, const char** name, double* total_m
 /* The SM clock a tensor-core GEMM kernel actually ran at: while profiling is enabled, one thread of
  * each of its CTAs adds the SM cycles (clock64) and nanoseconds (globaltimer) from its entry to its
  * exit on the current device; *mhz receives cycles / ns x 1000 over all its CTAs since
- * moe_profile_enable (0 when none ran; same kernel ids as moe_profile_read).  Under the GPU's
- * power cap this is the clock the kernel's work ran at, which nvidia-smi's periodic samples miss.
- * moe_profile_enable touches the current device for this (MOE_ERR_CUDA if it cannot);
- * moe_profile_sm_clock synchronises with it.  The other kernels record nothing here. */
+ * moe_profile_enable (0 when none ran, and for the grouped products, which take no such readings; same
+ * kernel ids as moe_profile_read).  Under the GPU's power cap this is the clock the kernel's work ran
+ * at, which nvidia-smi's periodic samples miss.  moe_profile_enable touches the current device for
+ * this (MOE_ERR_CUDA if it cannot); moe_profile_sm_clock synchronises with it.  The other kernels
+ * record nothing here. */
 moe_status_t moe_profile_sm_clock(int32_t kernel, double* mhz);
 
 /* Static text for a status code. */

@@ -236,7 +236,7 @@ const char* const kKernelNames[] = {
     "gemm_router_dx", "swiglu_bwd_kept", "gemm_gate_up_fp8", "quantize_e4m3", "gemm_down_fp8",
     "quantize_cols_e4m3", "gemm_bwd_dgrad_down_fp8", "gemm_bwd_recompute_swiglu_fp8", "gemm_dgrad_x_fp8",
     "router_split_wr", "to_bf16_rows", "grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "grouped_mm_i8",
-    "quantize_i8"};
+    "quantize_i8", "grouped_maps", "segments"};
 static_assert(sizeof(kKernelNames) / sizeof(kKernelNames[0]) == kKCount, "a name for every kernel id");
 
 struct Profiler {

@@ -147,7 +147,8 @@ enum KernelId : int {
   kKRoute = 0, kKScan, kKGather, kKGateUp, kKDown, kKCombine, kKBwdFused, kKWgrad, kKDgradX,
   kKDgates, kKRouterDlogits, kKRouterDwr, kKRouterReduce, kKCombineBwd, kKBwdDh, kKRouterDx, kKSwigluKept,
   kKGateUpFp8, kKQuantE4m3, kKDownFp8, kKQuantCols, kKBwdDhFp8, kKBwdFusedFp8, kKDgradXFp8, kKSplitWr,
-  kKToBf16, kKGroupedMm, kKGroupedDx, kKGroupedDw, kKGroupedI8, kKQuantI8, kKCount
+  kKToBf16, kKGroupedMm, kKGroupedDx, kKGroupedDw, kKGroupedI8, kKQuantI8, kKGroupMaps, kKSegments,
+  kKCount
 };
 void prof_mark(int id, cudaStream_t s, bool begin);
 // In-kernel SM clock of the GEMM kernels (gemm.cu): per kernel id, summed clock64 cycles and

@@ -899,8 +899,10 @@ cudaError_t launch_grouped_dw(const Grouped& c, const int32_t* begin, const int3
     CUtensorMap mx, mdy;
     if (!map_rows_mn(&mx, x, c.rows, c.K, c.ldi, p.wide_a) || !map_rows_mn(&mdy, dy, c.rows, c.N, c.ldo, p.wide_b))
       return cudaErrorInvalidValue;
+    prof_mark(kKGroupMaps, s, true);
     const cudaError_t e = launch_after(group_maps_kernel, c.G, 64, 0, 1, s, mx, mdy, end, c.rows,
                                        static_cast<CUtensorMap*>(maps));
+    prof_mark(kKGroupMaps, s, false);
     if (e != cudaSuccess) return e;
   }
   p.y = dW;
@@ -934,7 +936,9 @@ cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int3
 }
 
 cudaError_t launch_segments(const Tables* tabs, int G, int32_t* begin, int32_t* end, cudaStream_t s) {
+  prof_mark(kKSegments, s, true);
   segments_kernel<<<1, 256, 0, s>>>(tabs, G, begin, end);
+  prof_mark(kKSegments, s, false);
   return cudaGetLastError();
 }
 

@@ -118,3 +118,37 @@ def test_widest_contraction(moe, dtype, rows):
     ref = q.double() @ P[0].double().T * qs.double()[:, None] * Ps.double()
     before = steps + 3 * 2.0 ** -24
     assert ((y.double() - ref) / ref).abs().max().item() <= before + eps / 2 * (1 + before)
+
+
+def test_profile_counts_every_launch(moe):
+    """Every kernel that the grouped products launch is timed and counted, under a name of its own."""
+    rows, K, N, G = 600, 256, 136, 2
+    b, e = dev_i32([0, 250]), dev_i32([250, 600])
+    cfg = moe.grouped_config(rows, K, N, G)
+    ws = moe.grouped_workspace(cfg)
+    x, dy, W = rand((rows, K), torch.bfloat16, 1), rand((rows, N), torch.bfloat16, 2), rand((G, N, K), torch.bfloat16, 3)
+    q, qs = torch.empty(rows, K, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    P, Ps = torch.empty(G, N, K, dtype=torch.int8, device="cuda"), torch.empty(G, N, device="cuda")
+    y, dx, dW = torch.empty_like(dy), torch.empty_like(x), torch.empty_like(W)
+    layer = moe.config(T=64, d=128, f=128, E=2, k=1)
+    buf = moe.Buffers.allocate(layer)
+    idx = torch.zeros(64, 1, dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    moe.moe_dispatch(layer, idx, rand((64, 128), torch.bfloat16, 4), torch.empty(2, **i32), torch.empty(3, **i32),
+                     torch.empty(64, 1, **i32), torch.empty(64, **i32),
+                     torch.empty(buf.rows, 128, dtype=torch.bfloat16, device="cuda"), buf.ws)
+    calls = {"grouped_mm": lambda: moe.moe_grouped_mm(cfg, b, e, x, W, y, ws),
+             "grouped_mm_dx": lambda: moe.moe_grouped_mm_dx(cfg, b, e, dy, W, dx, ws),
+             "grouped_maps grouped_mm_dw": lambda: moe.moe_grouped_mm_dw(cfg, b, e, dy, x, dW, ws),
+             "quantize_i8": lambda: (moe.moe_quantize_rows_i8(x, q, qs), moe.moe_quantize_rows_i8(W, P, Ps)),
+             "grouped_mm_i8": lambda: moe.moe_grouped_mm_i8(cfg, b, e, q, qs, P, Ps, y, ws),
+             "segments": lambda: moe.moe_segments(layer, torch.empty(2, **i32), torch.empty(2, **i32), buf.ws)}
+    for names, call in calls.items():
+        moe.moe_profile_enable(True)
+        call()
+        prof = moe.moe_profile_read()
+        moe.moe_profile_enable(False)
+        ran = {n: launches for n, (ms, launches) in prof.items() if launches}
+        assert ran == {n: 2 if n == "quantize_i8" else 1 for n in names.split()}
+        assert all(prof[n][0] > 0 for n in ran)
+    assert moe.moe_check_error(ws) == 0 and moe.moe_check_error(buf.ws) == 0
