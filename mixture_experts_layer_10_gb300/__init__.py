@@ -184,13 +184,14 @@ _current_stream = None   # index of a device -> handle of its current stream
 
 
 def _bind_torch():
+    """The names above, each after those that its users take with it: another thread may look at any time."""
     global _holds, _current_device, _current_stream
     import torch
-    _holds = {BF16: (torch.bfloat16, torch.int16, torch.uint16), FP16: (torch.float16, torch.int16, torch.uint16),
-              "f32": (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,)}
     if _current_device is None:
         _current_device = torch._C._cuda_getDevice
     _current_stream = torch._C._cuda_getCurrentRawStream
+    _holds = {BF16: (torch.bfloat16, torch.int16, torch.uint16), FP16: (torch.float16, torch.int16, torch.uint16),
+              "f32": (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,)}
 
 
 def _grouped_ptr(t, shape, kind, what, on, stride=0):

@@ -1,6 +1,8 @@
 """Refusals of the grouped products (CPU: no compute call is made, every answer comes from the host's
 checks of the arguments)."""
 import ctypes
+import sys
+import types
 
 import pytest
 import torch
@@ -177,3 +179,16 @@ def test_unknown_types_are_the_librarys_to_refuse(monkeypatch, over):
     with pytest.raises(moe.MoEError) as e:
         moe.moe_grouped_mm_dw(c, b, b, dy, x, dW, ws, stream=0)
     assert e.value.code == INVALID
+
+
+def test_bindings_to_torch_are_published_whole(monkeypatch):
+    """Another thread that finds the table of types finds the other bindings too: a binding that stops half
+    way has published no table."""
+    for name in ("_holds", "_current_device", "_current_stream"):
+        monkeypatch.setattr(moe, name, None)
+    half = types.SimpleNamespace(**{n: getattr(torch, n) for n in ("bfloat16", "float16", "float32", "int8", "int16",
+                                                                    "uint16", "int32")})   # and no _C
+    monkeypatch.setitem(sys.modules, "torch", half)
+    with pytest.raises(AttributeError):
+        moe._bind_torch()
+    assert moe._holds is None and moe._current_stream is None
