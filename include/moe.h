@@ -370,6 +370,72 @@ moe_status_t moe_layer_bwd(const moe_config_t* cfg, const moe_bf16* x, const flo
                            moe_bf16* dW_gate, moe_bf16* dW_up, moe_bf16* dW_down,
                            void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* Types of the calls below. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
+
+/* ---- Expert selection ----------------------------------------------------------------------------
+ * The choice of experts from router logits, apart from the product that makes them: for routers other than the
+ * layer's softmax and top-k (sigmoid scores, a bias that balances the load, groups of experts, scaled
+ * weights), on the logits of moe_route or of the caller's own router.  The layer's other calls take what it
+ * gives: moe_dispatch the experts, moe_combine the weights; back through them, moe_select_bwd makes dlogits of
+ * the weights' gradients, moe_combine_bwd the input gradient and moe_router_wgrad the router's.
+ *
+ * For every token, with logits l [E] and the bias b [E]:
+ *   s_e     = softmax(l)_e or sigmoid(l_e)
+ *   key_e   = s_e + b_e                                  (the bias enters the keys only)
+ *   groups  of E / groups consecutive experts, scored by the sum of their group_top largest keys; the
+ *             top_groups best stay (a tie goes to the lower group)
+ *   idx     = the k largest keys among the groups that stay, larger first (a tie goes to the lower expert)
+ *   w_j     = s[idx_j], with renorm s[idx_j] / sum_m s[idx_m]; times scale
+ * The order of experts and groups is that of keys formed in 64 bits, whatever the type of the logits, and where there
+ * is no bias and no sum of two keys, that of the logits, which is the scores' own; weights and gradients are computed in 32 bits, and renormalised weights are finite and sum to scale however small the
+ * scores.
+ *
+ * Masks.  A logit of -inf masks its expert, as do a NaN and a bias of -inf or NaN: it counts in no group's
+ * score, a group of masked experts only comes last, and it is chosen only where its token has fewer than k others left
+ * (then by lower index, after them), so that idx is always k different experts.  A score of -inf is 0, and so are the
+ * weight and its gradient, whatever came back for it; a token of nothing else has weights of 0.  A NaN or
+ * +inf makes NaN of the weights that a NaN or an infinite softmax enters: all of a token with softmax not
+ * renormalised, else those of the slots that hold one, and with renorm of the whole token.
+ *
+ * The gradient, c = dweights, the selection held (the bias has none), h_j = w_j / scale:
+ *   renorm       dl of slot j's expert += w_j (c_j - sum_m c_m h_m), with sigmoid times 1 - s_j
+ *   else         sigmoid: += scale c_j s_j (1 - s_j);  softmax: dl_e = scale p_e (c_slot(e) - sum_m c_m p_m)
+ * and 0 elsewhere.  A slot whose idx is out of range has no part in it; one expert in several slots gets the sum of their
+ * terms, in slot order.
+ *
+ * Nothing is kept between calls, no workspace is needed, results are the same on every run, and calls on several
+ * streams do not disturb each other.  logits and dlogits are 16-byte aligned, the others 4-byte; outputs do not
+ * overlap inputs. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+typedef struct {
+    int32_t T;                 /* tokens, 0 .. 2^24 */
+    int32_t E, k;              /* experts, 1 .. 1024; experts of a token, 1 .. 32, at most those of top_groups groups */
+    int32_t score;             /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+    int32_t groups;            /* of experts: 1 .. 64, a divisor of E; 1: none */
+    int32_t top_groups;        /* groups that stay, 1 .. groups */
+    int32_t group_top;         /* keys summed to a group's score: 1 or 2 */
+    int32_t renorm;            /* 1: weights divided by their sum over the k slots */
+    float scale;               /* of the weights */
+    int32_t dtype;             /* of logits and dlogits: MOE_FP32, MOE_BF16 or MOE_FP16 */
+} moe_select_t;
+
+/* logits [T, E], bias [E] fp32 or NULL -> idx [T, k], weights [T, k] fp32. */
+moe_status_t moe_select(const moe_select_t* cfg, const void* logits, const float* bias, int32_t* idx, float* weights,
+                        moe_stream_t stream);
+
+/* logits [T, E], idx [T, k], dweights [T, k] fp32 -> dlogits [T, E] (dtype), overwritten. */
+moe_status_t moe_select_bwd(const moe_select_t* cfg, const void* logits, const int32_t* idx, const float* dweights,
+                            void* dlogits, moe_stream_t stream);
+
+/* The router's gradients from dlogits [T, E] fp32: dW_r = x^T dlogits [d_model, E], db_r = the sum of dlogits over
+ * the tokens [E] (nullable), both fp32 and overwritten.  The product takes dlogits in bf16, as
+ * moe_router_bwd's does; db_r sums them as they are.  Of cfg it uses T, d_model and E; ws is the workspace
+ * of this configuration. */
+moe_status_t moe_router_wgrad(const moe_config_t* cfg, const moe_bf16* x, const float* dlogits, float* dW_r,
+                              float* db_r, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* ---- Grouped products --------------------------------------------------------------------------
  * Matrix products over rows grouped by expert, group g having a weight of its own and any number of
  * rows: for an expert FFN other than the layer's SwiGLU one (another activation, a bias, one matrix,
@@ -401,8 +467,6 @@ moe_status_t moe_layer_bwd(const moe_config_t* cfg, const moe_bf16* x, const flo
  * additions to an fp32 dW (accumulate, and those parts) take subnormal values as zero.  NaN and infinities
  * stay within the rows (moe_grouped_mm, _dx, _i8) or the group (_dw) that hold them.  Results are the same
  * on every run. */
-typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
-
 typedef struct {
     int64_t rows;              /* rows of x, y, dx, dy (0 allowed), <= 2^28 */
     int32_t n_in, n_out;       /* widths of x and y: multiples of 8, 8 .. 65536 */

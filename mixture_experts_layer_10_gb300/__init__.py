@@ -30,7 +30,7 @@ EXPORTS = ("moe_workspace_size", "moe_perm_rows", "moe_workspace_init", "moe_rou
            "moe_keep_rows_for_budget", "moe_keep_rows_for_free_memory", "moe_quantize_cols_e4m3",
            "moe_layer_bwd_fp8", "moe_saved_layout", "moe_profile_sm_clock", "moe_grouped_workspace_size",
            "moe_grouped_workspace_init", "moe_segments", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
-           "moe_quantize_rows_i8", "moe_grouped_mm_i8")
+           "moe_quantize_rows_i8", "moe_grouped_mm_i8", "moe_select", "moe_select_bwd", "moe_router_wgrad")
 
 
 class moe_config_t(ctypes.Structure):
@@ -45,6 +45,15 @@ class moe_grouped_t(ctypes.Structure):
                 ("groups", ctypes.c_int32), ("dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
                 ("accumulate", ctypes.c_int32), ("in_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
 
+
+class moe_select_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+# moe_score_t
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 # moe_dtype_t
 BF16, FP16, FP32 = 0, 1, 2
@@ -72,6 +81,7 @@ def load(path: str | None = None):
     lib = ctypes.CDLL(path)
     cfgp = ctypes.POINTER(moe_config_t)
     grpp = ctypes.POINTER(moe_grouped_t)
+    selp = ctypes.POINTER(moe_select_t)
     sig = {
         "moe_workspace_size": [cfgp, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)],
         "moe_perm_rows": [cfgp, ctypes.POINTER(ctypes.c_int64)],
@@ -113,6 +123,9 @@ def load(path: str | None = None):
         "moe_grouped_mm_dw": [grpp, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
         "moe_quantize_rows_i8": [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P, _P, _P],
         "moe_grouped_mm_i8": [grpp, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+        "moe_select": [selp, _P, _P, _P, _P, _P],
+        "moe_select_bwd": [selp, _P, _P, _P, _P, _P],
+        "moe_router_wgrad": [cfgp, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
         "moe_status_string": [ctypes.c_int],
     }
     for name, args in sig.items():
@@ -151,6 +164,18 @@ def grouped_config(rows: int, n_in: int, n_out: int, groups: int, dtype=BF16, dw
     return moe_grouped_t(int(rows), int(n_in), int(n_out), int(groups), code,
                          code if dw_dtype is None else dtype_code(dw_dtype), int(accumulate), int(in_stride),
                          int(out_stride))
+
+
+def select_config(T: int, E: int, k: int, score="softmax", groups: int = 1, top_groups: int | None = None,
+                  group_top: int = 1, renorm: int = 0, scale: float = 1.0, dtype=FP32) -> moe_select_t:
+    """Description of a selection of k of E experts for T tokens; score is "softmax" or "sigmoid" (or a moe_score_t
+    code), dtype that of the logits (a torch dtype or a moe_dtype_t code); all groups stay unless top_groups
+    says how many."""
+    code = SCORES.get(score, score)
+    if not isinstance(code, int):
+        raise ValueError(f"no score {score!r}")
+    return moe_select_t(int(T), int(E), int(k), code, int(groups), int(groups if top_groups is None else top_groups),
+                        int(group_top), int(renorm), float(scale), dtype_code(dtype))
 
 
 def grouped_workspace(cfg: moe_grouped_t, device="cuda", stream=None):
@@ -336,6 +361,39 @@ def moe_router_bwd(cfg, x, W_r, b_r, idx, gates, dgates, dlogits, dW_r, db_r, ws
 def moe_combine_bwd(cfg, dx_perm, dlogits, W_r, dx, ws, stream=None):
     _call("moe_combine_bwd", ctypes.byref(cfg), _ptr(dx_perm), _ptr(dlogits), _ptr(W_r), _ptr(dx),
           _ptr(ws), ws.numel(), _stream(stream))
+
+
+def _select_ptrs(c, logits, what):
+    """Device of a selection's logits, on which the call has to run, and the kind of their type."""
+    on = logits.get_device()
+    _on_current(on, logits, what)
+    return on, "f32" if c.dtype == FP32 else c.dtype
+
+
+def moe_select(cfg, logits, bias, idx, weights, stream=None):
+    """logits [T, E], bias [E] fp32 or None -> idx [T, k] int32, weights [T, k] fp32."""
+    c = cfg
+    on, kind = _select_ptrs(c, logits, "logits")
+    _call("moe_select", ctypes.byref(c), _grouped_ptr(logits, (c.T, c.E), kind, "logits", on),
+          _grouped_ptr(bias, (c.E,), "f32", "bias", on), _grouped_ptr(idx, (c.T, c.k), "i32", "idx", on),
+          _grouped_ptr(weights, (c.T, c.k), "f32", "weights", on), _current_stream(on) if stream is None else _stream(stream))
+
+
+def moe_select_bwd(cfg, logits, idx, dweights, dlogits, stream=None):
+    """dlogits [T, E] of dweights [T, k], the selection held."""
+    c = cfg
+    on, kind = _select_ptrs(c, logits, "logits")
+    _call("moe_select_bwd", ctypes.byref(c), _grouped_ptr(logits, (c.T, c.E), kind, "logits", on),
+          _grouped_ptr(idx, (c.T, c.k), "i32", "idx", on), _grouped_ptr(dweights, (c.T, c.k), "f32", "dweights", on),
+          _grouped_ptr(dlogits, (c.T, c.E), kind, "dlogits", on), _current_stream(on) if stream is None else _stream(stream))
+
+
+def moe_router_wgrad(cfg, x, dlogits, dW_r, db_r, ws, stream=None):
+    """dW_r [d, E] = x^T dlogits and db_r [E] (or None), the sum of dlogits over the tokens."""
+    c, on = cfg, ws.get_device()
+    _call("moe_router_wgrad", ctypes.byref(c), _grouped_ptr(x, (c.T, c.d_model), BF16, "x", on),
+          _grouped_ptr(dlogits, (c.T, c.E), "f32", "dlogits", on), _grouped_ptr(dW_r, (c.d_model, c.E), "f32", "dW_r", on),
+          _grouped_ptr(db_r, (c.E,), "f32", "db_r", on), *_grouped_ws(ws, on, stream))
 
 
 def moe_quantize_rows_e4m3(src, codes, scales, stream=None):

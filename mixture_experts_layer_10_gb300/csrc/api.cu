@@ -236,7 +236,7 @@ const char* const kKernelNames[] = {
     "gemm_router_dx", "swiglu_bwd_kept", "gemm_gate_up_fp8", "quantize_e4m3", "gemm_down_fp8",
     "quantize_cols_e4m3", "gemm_bwd_dgrad_down_fp8", "gemm_bwd_recompute_swiglu_fp8", "gemm_dgrad_x_fp8",
     "router_split_wr", "to_bf16_rows", "grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "grouped_mm_i8",
-    "quantize_i8", "grouped_maps", "segments"};
+    "quantize_i8", "grouped_maps", "segments", "select", "select_bwd", "router_dlogits_rows"};
 static_assert(sizeof(kKernelNames) / sizeof(kKernelNames[0]) == kKCount, "a name for every kernel id");
 
 struct Profiler {
@@ -320,6 +320,21 @@ moe_status_t make_grouped(const moe_grouped_t* in, Grouped* c) {
   c->fp16 = m.dtype == MOE_FP16;
   c->dw_fp32 = m.dw_dtype == MOE_FP32;
   c->acc = m.accumulate == 1;
+  return MOE_OK;
+}
+
+// A validated description of a selection.
+moe_status_t make_select(const moe_select_t* in, Select* c) {
+  if (in == nullptr) return MOE_ERR_INVALID_ARG;
+  const moe_select_t& m = *in;
+  MOE_NEED(m.T >= 0 && m.T <= 1 << 24 && m.E >= 1 && m.E <= 1024 && m.k >= 1 && m.k <= 32);
+  MOE_NEED(m.groups >= 1 && m.groups <= 64 && m.E % m.groups == 0 && m.top_groups >= 1 && m.top_groups <= m.groups &&
+           (m.group_top == 1 || m.group_top == 2) && m.k <= m.top_groups * (m.E / m.groups));
+  MOE_NEED((m.score == MOE_SCORE_SOFTMAX || m.score == MOE_SCORE_SIGMOID) && (m.renorm == 0 || m.renorm == 1));
+  MOE_NEED(m.dtype == MOE_FP32 || m.dtype == MOE_BF16 || m.dtype == MOE_FP16);
+  MOE_NEED(std::isfinite(m.scale));
+  *c = Select{m.T, m.E, m.k, m.groups, m.top_groups, m.group_top, m.score == MOE_SCORE_SIGMOID, m.renorm == 1, m.scale,
+              m.dtype};
   return MOE_OK;
 }
 
@@ -766,6 +781,49 @@ moe_status_t moe_combine_bwd(const moe_config_t* cfg, const moe_bf16* dx_perm, c
   MOE_TRY(get_ws(c, ws, ws_bytes, &w));
   MOE_TRY(check_device());
   return do_combine_bwd(c, w, dx_perm, dlogits, W_r, dx, stream);
+}
+
+moe_status_t moe_select(const moe_select_t* cfg, const void* logits, const float* bias, int32_t* idx, float* weights,
+                        moe_stream_t stream) {
+  Select c;
+  MOE_TRY(make_select(cfg, &c));
+  MOE_NEED(c.T == 0 || (logits && idx && weights));
+  MOE_NEED(aligned16(logits) && aligned4(bias) && aligned4(idx) && aligned4(weights));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_select(c, logits, bias, idx, weights, stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_select_bwd(const moe_select_t* cfg, const void* logits, const int32_t* idx, const float* dweights,
+                            void* dlogits, moe_stream_t stream) {
+  Select c;
+  MOE_TRY(make_select(cfg, &c));
+  MOE_NEED(c.T == 0 || (logits && idx && dweights && dlogits));
+  MOE_NEED(aligned16(logits) && aligned16(dlogits) && aligned4(idx) && aligned4(dweights));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_select_bwd(c, logits, idx, dweights, dlogits, stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_router_wgrad(const moe_config_t* cfg, const moe_bf16* x, const float* dlogits, float* dW_r,
+                              float* db_r, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Cfg c;
+  MOE_TRY(make_cfg(cfg, &c));
+  MOE_NEED(x && dlogits && dW_r && aligned16(x) && aligned16(dlogits) && aligned16(dW_r) && aligned16(db_r));
+  Ws w;
+  MOE_TRY(get_ws(c, ws, ws_bytes, &w));
+  MOE_TRY(check_device());
+  RouterBwdArgs a{};
+  a.x = x;
+  a.dW_r = dW_r;
+  a.db_r = db_r;
+  a.dwr_part = w.at<float>(w.L.dwr_part);
+  a.db_part = w.at<float>(w.L.db_part);
+  uint16_t* dl_bf16 = w.at<uint16_t>(w.L.dl_bf16);
+  MOE_CUDA(launch_dlogits_rows(c, dlogits, w.L.Ep, dl_bf16, a.db_part, stream));
+  MOE_CUDA(launch_router_dwr(c, w.L, x, dl_bf16, a.dwr_part, w.hdr(), w.tabs(), stream));
+  MOE_CUDA(launch_router_reduce(c, w.L, a, router_saved_blocks(c), stream));
+  return MOE_OK;
 }
 
 moe_status_t moe_quantize_rows_e4m3(const moe_bf16* src, int64_t rows, int32_t cols, uint8_t* codes,

@@ -148,6 +148,7 @@ enum KernelId : int {
   kKDgates, kKRouterDlogits, kKRouterDwr, kKRouterReduce, kKCombineBwd, kKBwdDh, kKRouterDx, kKSwigluKept,
   kKGateUpFp8, kKQuantE4m3, kKDownFp8, kKQuantCols, kKBwdDhFp8, kKBwdFusedFp8, kKDgradXFp8, kKSplitWr,
   kKToBf16, kKGroupedMm, kKGroupedDx, kKGroupedDw, kKGroupedI8, kKQuantI8, kKGroupMaps, kKSegments,
+  kKSelect, kKSelectBwd, kKDlogitsRows,
   kKCount
 };
 void prof_mark(int id, cudaStream_t s, bool begin);
@@ -226,6 +227,10 @@ cudaError_t launch_router_dwr(const Cfg& c, const Layout& L, const uint16_t* x, 
                               float* dwr_part, Hdr* hdr, const Tables* tabs, cudaStream_t s);
 // dst [rows, ld] bf16 = src [rows, cols] fp32, zero for cols <= c < ld
 cudaError_t launch_to_bf16_rows(const float* src, int rows, int cols, int ld, uint16_t* dst, cudaStream_t s);
+
+// Both of dlogits' other forms in one pass: bf16 rows [T, ld], zero from E on, and router_saved_blocks(c) db partials
+cudaError_t launch_dlogits_rows(const Cfg& c, const float* dlogits, int ld, uint16_t* dl_bf16, float* db_part,
+                                cudaStream_t s);
 
 // Router logits on the tensor cores (E <= 128, k <= 8): W_r [d, E] fp32 is split into
 // hi + mid + lo bf16 parts stored K-major as wr3 [3][Ep][d].
@@ -356,6 +361,16 @@ cudaError_t launch_stream_mm(const Grouped& c, const int32_t* begin, const int32
                              const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s);
 cudaError_t launch_stream_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,
                              const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr, cudaStream_t s);
+// Expert selection from logits (select.cu)
+struct Select {            // validated description
+  int T, E, k, n, top, sum;   // n groups of experts, of which `top` stay, scored by their `sum` largest keys
+  bool sigmoid, renorm;
+  float scale;
+  int dtype;
+};
+cudaError_t launch_select(const Select& c, const void* logits, const float* bias, int32_t* idx, float* w, cudaStream_t s);
+cudaError_t launch_select_bwd(const Select& c, const void* logits, const int32_t* idx, const float* dw, void* dl,
+                              cudaStream_t s);
 cudaError_t launch_segments(const Tables* tabs, int G, int32_t* begin, int32_t* end, cudaStream_t s);
 // 8-bit integer rows: codes [rows, cols] and one fp32 scale per row (amax / 127)
 cudaError_t launch_quantize_rows_i8(const uint16_t* src, bool fp16, int64_t rows, int cols, int8_t* codes,

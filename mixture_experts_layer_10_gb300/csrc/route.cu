@@ -574,6 +574,30 @@ __global__ void to_bf16_rows_kernel(const float* __restrict__ src, int rows, int
   }
 }
 
+// dlogits [T, E] as bf16 rows [T, Ep] (zero from E on) and the sums over each block's 32 tokens, in one pass.
+// A thread has a column, or one of several shares of the tokens of a column where Ep is below the block's 256.
+__global__ void __launch_bounds__(256) dlogits_rows_kernel(const float* __restrict__ dl, int T, int E, int Ep,
+                                                           uint16_t* __restrict__ dst, float* __restrict__ db_part) {
+  __shared__ float red[256];
+  const int c = threadIdx.x % Ep, share = threadIdx.x / Ep, shares = 256 / Ep;
+  const int t0 = blockIdx.x * 32;
+  float sum = 0.f;
+  if (share < shares) {
+    for (int t = t0 + share; t < min(T, t0 + 32); t += shares) {
+      const float v = c < E ? dl[(size_t)t * E + c] : 0.f;
+      dst[(size_t)t * Ep + c] = (uint16_t)(pack_bf16(v, 0.f) & 0xFFFFu);
+      sum += v;
+    }
+  }
+  red[threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.x < E) {
+    float v = 0.f;
+    for (int h = 0; h < shares; ++h) v += red[h * Ep + threadIdx.x];
+    db_part[(size_t)blockIdx.x * E + threadIdx.x] = v;
+  }
+}
+
 }  // namespace
 
 // blocks (and db partials) of router_dlogits_saved_kernel: 32 tokens each
@@ -662,6 +686,14 @@ cudaError_t launch_to_bf16_rows(const float* src, int rows, int cols, int ld, ui
   prof_mark(kKToBf16, s, true);
   to_bf16_rows_kernel<<<blocks, 256, 0, s>>>(src, rows, cols, ld, dst);
   prof_mark(kKToBf16, s, false);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dlogits_rows(const Cfg& c, const float* dlogits, int ld, uint16_t* dl_bf16, float* db_part,
+                                cudaStream_t s) {
+  prof_mark(kKDlogitsRows, s, true);
+  dlogits_rows_kernel<<<router_saved_blocks(c), 256, 0, s>>>(dlogits, c.T, c.E, ld, dl_bf16, db_part);
+  prof_mark(kKDlogitsRows, s, false);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,634 @@
+// Expert selection from router logits: softmax or sigmoid scores s, keys s + bias, groups of experts, top-k by
+// key (ties to the lower expert), weights from the scores; and its gradient with the selection held.
+//
+// A token is held by G lanes (8, 16 or 32) of a warp, NV consecutive experts a lane, from one read of its
+// logits.  A round of the top-k takes the largest key over the lanes and retires it; the slots' weights are
+// then formed one slot a lane, from the logits themselves.
+//
+// Which expert wins must not hang on the rounding of a score, so the order is that of the keys in 64 bits:
+//   - without a bias and without sums of keys (groups scored by two) the order of the keys is the order of the
+//     logits, which are compared as they are (scores that round to the same number have an order, too);
+//   - else the keys are formed in 32 bits, and a token in which two keys that follow each other (or the two
+//     group scores at the border) are nearer than their error can bridge is done again in 64 bits.
+// The second way is rare where logits are spread (about one token in 500 at 256 experts), and the first
+// costs nothing, so that no token pays for 64-bit exponentials, of which an SM does few.
+//
+// The error of a 32-bit key.  exp's approximation is off by 2^-22 and its argument's product by |x| 2^-24,
+// relatively; of a sigmoid, s (1 - s) |x| <= 0.23 of that counts, so s is off by less than 2^-21.6 and the sum
+// with the bias by 2^-24 of itself: two keys differ wrongly by less than 2^-20.5 + 2^-23 |key|, and
+// 2^-19 max(1, |key|) is what is asked for.  A softmax's sum of at most 32 + 5 rounded additions is
+// 2^-18.7 off in one direction for all experts, so twice as much is asked for there, and for sums of two keys.
+#include <algorithm>
+#include <cfloat>
+
+#include "common.cuh"
+#include "grouped.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWarps = 4;          // of a block
+constexpr int kMaxSlots = 32;
+constexpr int kMaxExpertGroups = 64;
+
+struct SelParams {
+  const void* logits;
+  const float* bias;               // nullable
+  int32_t* idx;
+  float* w;
+  const float* dw;                 // backward
+  void* dl;
+  int64_t T;
+  int E, k;
+  int n, per, top, sum;            // expert groups, experts of one, groups kept, keys summed (1 or 2)
+  bool sigmoid, renorm;
+  float scale;
+};
+
+// ---- lanes of a token ----------------------------------------------------------------------------
+
+template <int G>
+__device__ __forceinline__ uint32_t group_mask(int lane) {
+  return G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << (lane & ~(G - 1));
+}
+
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t mask) {
+  if (G == 32) return __reduce_max_sync(0xffffffffu, v);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(mask, v, o));
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v, uint32_t mask) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float group_fmax(float v, uint32_t mask) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
+  return v;
+}
+
+// Order of floats as order of integers; finite values and infinities lie above 1.
+constexpr uint32_t kTaken = 0, kMasked = 1;
+__device__ __forceinline__ uint32_t order_of(float f) {
+  const uint32_t b = __float_as_uint(f + 0.f);   // (-0 is 0)
+  return (b & 0x80000000u) != 0 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) != 0 ? u ^ 0x80000000u : ~u);
+}
+
+// ---- logits --------------------------------------------------------------------------------------
+
+template <class T> __device__ __forceinline__ float widen1(T v);
+template <> __device__ __forceinline__ float widen1(float v) { return v; }
+template <> __device__ __forceinline__ float widen1(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float widen1(__half v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T narrow1(float v);
+template <> __device__ __forceinline__ float narrow1(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 narrow1(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half narrow1(float v) { return __float2half_rn(v); }
+
+template <class T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
+template <class T, int NV> constexpr int vec_of() { return NV * (int)sizeof(T) <= 16 ? NV : 16 / (int)sizeof(T); }
+
+// This lane's experts e0 .. e0 + NV - 1 of a row; -inf past the last.
+template <class T, int NV>
+__device__ __forceinline__ void load_row(const T* row, int e0, int E, float (&x)[NV]) {
+  constexpr int V = vec_of<T, NV>();
+  if (E % V == 0) {   // rows start on V elements (the array on 16 bytes)
+#pragma unroll
+    for (int i = 0; i < NV; i += V) {
+      Vec<T, V> r;
+      const bool in = e0 + i < E;
+      if (in) r = *reinterpret_cast<const Vec<T, V>*>(row + e0 + i);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[i + j] = in ? widen1(r.v[j]) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = e0 + i < E ? widen1(row[e0 + i]) : -INFINITY;
+  }
+}
+
+template <class T, int NV>
+__device__ __forceinline__ void store_row(T* row, int e0, int E, const float (&x)[NV]) {
+  constexpr int V = vec_of<T, NV>();
+  if (E % V == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; i += V) {
+      Vec<T, V> r;
+#pragma unroll
+      for (int j = 0; j < V; ++j) r.v[j] = narrow1<T>(x[i + j]);
+      if (e0 + i < E) *reinterpret_cast<Vec<T, V>*>(row + e0 + i) = r;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (e0 + i < E) row[e0 + i] = narrow1<T>(x[i]);
+  }
+}
+
+// (a logit that is -inf masks its expert; NaN too, as far as the selection goes)
+__device__ __forceinline__ bool masked(float x) { return !(x > -INFINITY); }
+
+__device__ __forceinline__ float sigmoid32(float x) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
+
+// ---- the same in 64 bits, for a token whose order is in doubt ---------------------------------------
+
+template <int G>
+__device__ __forceinline__ void top2_merge(double& a, double& b, double oa, double ob) {
+  if (oa > a) {
+    b = fmax(a, ob);
+    a = oa;
+  } else {
+    b = fmax(b, oa);
+  }
+}
+
+// One token by its G lanes: slot j to lane j % G, element j / G.
+template <class T, int G, int NV>
+__device__ __noinline__ void select64(const SelParams& p, int64_t t, int lane, int (&sidx)[32 / G]) {
+  const uint32_t mask = group_mask<G>(lane);
+  const int li = lane & (G - 1), e0 = li * NV;
+  const T* row = static_cast<const T*>(p.logits) + t * p.E;
+  double key[NV];
+  uint32_t out = 0;   // masked experts of this lane, and taken or absent ones
+  uint32_t gone = 0;
+  double m = -INFINITY, z = 0.;
+  for (int i = 0; i < NV; ++i) {
+    const float x = e0 + i < p.E ? widen1(row[e0 + i]) : -INFINITY;
+    if (e0 + i >= p.E) gone |= 1u << i;
+    if (masked(x)) out |= 1u << i;
+    key[i] = masked(x) ? -INFINITY : (double)fminf(x, FLT_MAX);
+    m = fmax(m, key[i]);
+  }
+  if (p.sigmoid) {
+    for (int i = 0; i < NV; ++i) key[i] = 1. / (1. + exp(-key[i]));
+  } else {
+    for (int o = G / 2; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(mask, m, o));
+    for (int i = 0; i < NV; ++i) {
+      key[i] = (out >> i & 1u) != 0 ? 0. : exp(key[i] - m);
+      z += key[i];
+    }
+    for (int o = G / 2; o > 0; o >>= 1) z += __shfl_xor_sync(mask, z, o);
+    for (int i = 0; i < NV; ++i) key[i] /= z;
+  }
+  for (int i = 0; i < NV; ++i) {
+    if (p.bias != nullptr && e0 + i < p.E) key[i] += (double)p.bias[e0 + i];
+    if (!(key[i] > -INFINITY)) out |= 1u << i;   // (a bias of -inf or NaN masks, too)
+  }
+  if (p.top < p.n) {
+    double score[kMaxExpertGroups];
+    for (int g = 0; g < p.n; ++g) {
+      double a = -INFINITY, b = -INFINITY;
+      for (int i = 0; i < NV; ++i) {
+        const int e = e0 + i;
+        if (e >= g * p.per && e < (g + 1) * p.per && (out >> i & 1u) == 0) top2_merge<G>(a, b, key[i], -INFINITY);
+      }
+      for (int o = G / 2; o > 0; o >>= 1)
+        top2_merge<G>(a, b, __shfl_xor_sync(mask, a, o), __shfl_xor_sync(mask, b, o));
+      score[g] = p.sum == 2 && b > -INFINITY ? a + b : a;
+    }
+    for (int g = 0; g < p.n; ++g) {
+      int above = 0;
+      for (int h = 0; h < p.n; ++h) above += score[h] > score[g] || (score[h] == score[g] && h < g);
+      if (above < p.top) continue;
+      for (int i = 0; i < NV; ++i)
+        if (e0 + i >= g * p.per && e0 + i < (g + 1) * p.per) gone |= 1u << i;
+    }
+  }
+  for (int r = 0; r < p.k; ++r) {
+    // first the experts that are not masked, then those that are
+    double v = -INFINITY;
+    int e = 0x7fffffff, cls = 2;
+    for (int i = 0; i < NV; ++i) {
+      if ((gone >> i & 1u) != 0) continue;
+      const int c = out >> i & 1u;
+      if (c < cls || (c == 0 && cls == 0 && key[i] > v)) {
+        cls = c;
+        v = key[i];
+        e = e0 + i;
+      }
+    }
+    for (int o = G / 2; o > 0; o >>= 1) {
+      const double ov = __shfl_xor_sync(mask, v, o);
+      const int oe = __shfl_xor_sync(mask, e, o), oc = __shfl_xor_sync(mask, cls, o);
+      const bool tie = oc == cls && (oc != 0 || ov == v);
+      if (oc < cls || (oc == 0 && cls == 0 && ov > v) || (tie && oe < e)) {
+        v = ov;
+        e = oe;
+        cls = oc;
+      }
+    }
+    if (e >= e0 && e < e0 + NV) gone |= 1u << (e - e0);
+    if (r % G == li) sidx[r / G] = e;
+  }
+}
+
+// ---- selection -----------------------------------------------------------------------------------
+
+// kKeys: keys are scores (with a bias, or summed), else logits.
+template <class T, int G, int NV, bool kKeys>
+__global__ void __launch_bounds__(32 * kWarps) select_kernel(const __grid_constant__ SelParams p) {
+  constexpr int kTok = 32 / G;       // tokens of a warp
+  constexpr int kSlots = 32 / G;     // slots of a lane
+  __shared__ uint32_t keys[kWarps][32 * NV];
+  __shared__ uint32_t scores[kWarps][kTok][kMaxExpertGroups];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & (G - 1), e0 = li * NV;
+  constexpr uint32_t mask = 0xffffffffu;       // (all tokens of a warp take the same way)
+  const uint32_t mine = group_mask<G>(lane);
+  const int64_t at = ((int64_t)blockIdx.x * kWarps + warp) * kTok + lane / G;
+  const int64_t t = min(at, p.T - 1);   // (lanes past the last token do its work again and store nothing)
+  const T* row = static_cast<const T*>(p.logits) + t * p.E;
+  after_previous_kernel();
+
+  float x[NV];
+  load_row<T, NV>(row, e0, p.E, x);
+  const bool softmax_all = !p.sigmoid && (kKeys || !p.renorm);
+  float m = -FLT_MAX, z = 0.f, rz = 0.f;
+  bool broken = false;   // a NaN or +inf: the selection goes by the rest, or as if it were the largest number
+  uint32_t u[NV];
+  if (softmax_all) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, x[i]);
+    m = fminf(group_fmax<G>(m, mask), FLT_MAX);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z += __expf(x[i] - m);
+    z = group_sum<G>(z, mask);
+    broken = !(z <= FLT_MAX);
+    if (__any_sync(mask, broken)) {
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) z += masked(x[i]) ? 0.f : __expf(fminf(x[i], FLT_MAX) - m);
+      z = group_sum<G>(z, mask);
+    }
+    rz = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float key = x[i];
+    bool no = masked(x[i]);
+    if (kKeys) {
+      key = p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x[i])) : __expf(fminf(x[i], FLT_MAX) - m) * rz;
+      if (p.bias != nullptr && e0 + i < p.E) key += __ldg(p.bias + e0 + i);
+      no = no || masked(key);
+    }
+    u[i] = e0 + i >= p.E ? kTaken : (no ? kMasked : order_of(key));
+  }
+
+  bool doubt = false;   // the same in all lanes of a token
+  const float tol = p.sigmoid ? 0x1p-19f : 0x1p-18f;
+  if (p.top < p.n) {
+    // scores of the groups: of masked experts nothing is added, and a group of none else comes last
+    const int lanes = p.per / NV;   // of a group
+    if (p.per % NV == 0 && (lanes & (lanes - 1)) == 0) {
+      uint32_t a = kTaken, b = kTaken;   // the largest two keys of the lane, then of the group
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        b = max(b, min(a, u[i]));
+        a = max(a, u[i]);
+      }
+      for (int o = lanes / 2; o > 0; o >>= 1) {
+        const uint32_t oa = __shfl_xor_sync(mask, a, o), ob = __shfl_xor_sync(mask, b, o);
+        b = max(max(b, ob), min(a, oa));
+        a = max(a, oa);
+      }
+      float f = value_of(a);
+      if (p.sum == 2 && b > kMasked) f += value_of(b);
+      const uint32_t s = a > kMasked ? order_of(f) : kMasked;
+      const int g = e0 / p.per;   // (of a lane past the last expert: no group's)
+      int above = 0;
+      for (int h = 0; h < p.n; ++h) {
+        const uint32_t o = __shfl_sync(mask, s, h * lanes, G);
+        above += o > s || (o == s && h < g);
+      }
+      const bool keep = above < p.top;
+      if (kKeys) {
+        const uint32_t last = __ballot_sync(mask, e0 < p.E && above == p.top - 1) & mine;
+        const uint32_t next = __ballot_sync(mask, e0 < p.E && above == p.top) & mine;
+        const uint32_t sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
+        const float fl = value_of(sl);
+        doubt = sn > kMasked && fl - value_of(sn) <= 2.f * tol * fmaxf(1.f, fabsf(fl));
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (!keep) u[i] = kTaken;
+    } else {
+      // groups that do not fall on lanes: through shared memory, a group a lane
+      uint32_t* kr = keys[warp] + (lane / G) * (G * NV);
+      uint32_t* sr = scores[warp][lane / G];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) kr[e0 + i] = u[i];
+      __syncwarp();
+      for (int g = li; g < p.n; g += G) {
+        uint32_t a = kTaken, b = kTaken;
+        for (int e = g * p.per; e < (g + 1) * p.per; ++e) {
+          const uint32_t v = kr[e];
+          b = max(b, min(a, v));
+          a = max(a, v);
+        }
+        float f = value_of(a);
+        if (p.sum == 2 && b > kMasked) f += value_of(b);
+        sr[g] = a > kMasked ? order_of(f) : kMasked;
+      }
+      __syncwarp();
+      uint32_t lo = 0xffffffffu, hi = 0;   // the lowest score kept, the highest dropped
+      for (int g = li; g < p.n; g += G) {
+        const uint32_t s = sr[g];
+        int above = 0;
+        for (int h = 0; h < p.n; ++h) {
+          const uint32_t o = sr[h];
+          above += o > s || (o == s && h < g);
+        }
+        if (above < p.top) {
+          lo = min(lo, s);
+        } else {
+          hi = max(hi, s);
+          for (int e = g * p.per; e < (g + 1) * p.per; ++e) kr[e] = kTaken;
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) u[i] = kr[e0 + i];
+      if (kKeys) {
+        lo = ~group_max<G>(~lo, mask);
+        hi = group_max<G>(hi, mask);
+        const float fl = value_of(lo);
+        doubt = hi > kMasked && fl - value_of(hi) <= 2.f * tol * fmaxf(1.f, fabsf(fl));
+      }
+    }
+  }
+
+  int sidx[kSlots];
+  uint32_t before = kTaken;   // the key of the slot before
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    sidx[q] = 0;
+    for (int rr = 0; rr < G; ++rr) {
+      const int r = q * G + rr;
+      if (r > p.k || (r == p.k && !kKeys)) break;   // (one more than the slots, for the border)
+      uint32_t best = u[0];
+#pragma unroll
+      for (int i = 1; i < NV; ++i) best = max(best, u[i]);
+      const uint32_t v = group_max<G>(best, mask);
+      if (kKeys) {
+        if (r > 0 && v > kMasked) {
+          const float fb = value_of(before);
+          doubt |= fb - value_of(v) <= tol * fmaxf(1.f, fabsf(fb));
+        }
+        before = v;
+        if (r == p.k) break;
+      }
+      const int owner = __ffs(__ballot_sync(mask, best == v) & mine) - 1;
+      int il = 0;
+#pragma unroll
+      for (int i = NV - 1; i >= 0; --i)
+        if (u[i] == v) il = i;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (lane == owner && i == il) u[i] = kTaken;
+      const int e = __shfl_sync(mask, e0 + il, owner);
+      if (rr == li) sidx[q] = e;
+    }
+  }
+  if (kKeys && p.k == kMaxSlots) {   // the border's key of a full set of slots
+    uint32_t best = u[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) best = max(best, u[i]);
+    const uint32_t v = group_max<G>(best, mask);
+    const float fb = value_of(before);
+    doubt |= v > kMasked && fb - value_of(v) <= tol * fmaxf(1.f, fabsf(fb));
+  }
+  if (kKeys && doubt) select64<T, G, NV>(p, t, lane, sidx);
+  __syncwarp();
+
+  // weights, a slot a lane
+  float xs[kSlots], M = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const bool slot = q * G + li < p.k;
+    xs[q] = slot ? widen1(row[sidx[q]]) : -INFINITY;
+    M = fmaxf(M, xs[q]);
+  }
+  if (broken) rz = __int_as_float(0x7fffffff);
+  float s[kSlots], sum = 0.f;
+  if (p.renorm) M = group_fmax<G>(M, mask);
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const bool slot = q * G + li < p.k;
+    if (!p.renorm) {
+      s[q] = p.sigmoid ? sigmoid32(xs[q]) : expf(xs[q] - m) * rz;
+    } else if (p.sigmoid && M >= -40.f) {
+      s[q] = sigmoid32(xs[q]);
+    } else {   // (a sigmoid below e^-40 is the exponential to 2^-57)
+      s[q] = M == -INFINITY ? (xs[q] == -INFINITY ? 0.f : xs[q]) : expf(xs[q] - M);
+    }
+    if (!slot) s[q] = 0.f;
+    sum += s[q];
+  }
+  if (p.renorm) {
+    sum = group_sum<G>(sum, mask);
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) s[q] = sum == 0.f ? 0.f : __fdiv_rn(s[q], sum);
+  }
+  if (at >= p.T) return;
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int j = q * G + li;
+    if (j >= p.k) continue;
+    p.idx[t * p.k + j] = sidx[q];
+    p.w[t * p.k + j] = s[q] * p.scale;
+  }
+}
+
+// ---- gradient ------------------------------------------------------------------------------------
+
+// d_j, a slot a lane, then each expert's sum over the slots that chose it, in slot order, by the lane that holds it:
+//   renormalised      d_j = w_j (c_j - sum_m c_m h_m), sigmoid: times 1 - s_j
+//   not renormalised  d_j = scale c_j s_j (1 - s_j); softmax: d_j = scale c_j p_j, and less
+//                     p_e scale sum_j c_j p_j for every expert
+template <class T, int G, int NV>
+__global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_constant__ SelParams p) {
+  constexpr int kTok = 32 / G, kSlots = 32 / G;
+  constexpr uint32_t mask = 0xffffffffu;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & (G - 1), e0 = li * NV;
+  const int64_t at = ((int64_t)blockIdx.x * kWarps + warp) * kTok + lane / G;
+  const int64_t t = min(at, p.T - 1);
+  const T* row = static_cast<const T*>(p.logits) + t * p.E;
+  after_previous_kernel();
+
+  int e[kSlots];
+  float c[kSlots], xs[kSlots];
+  float M = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int j = q * G + li;
+    e[q] = -1;
+    c[q] = 0.f;
+    if (j < p.k) {
+      e[q] = p.idx[t * p.k + j];
+      c[q] = p.dw[t * p.k + j];
+    }
+    if (e[q] < 0 || e[q] >= p.E) e[q] = -1;   // (no expert: a slot without weight)
+  }
+  float v[NV];
+  const bool dense = !p.sigmoid && !p.renorm;
+  float m = -FLT_MAX, rz = 0.f;
+  if (dense) {
+    load_row<T, NV>(row, e0, p.E, v);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, v[i]);
+    m = group_fmax<G>(m, mask);
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = __expf(v[i] - m);
+      z += v[i];
+    }
+    z = group_sum<G>(z, mask);
+    rz = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
+  }
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    xs[q] = e[q] >= 0 ? widen1(row[e[q]]) : -INFINITY;
+    if (xs[q] == -INFINITY) c[q] = 0.f;   // (whatever the gradient of a weight that is nothing)
+    M = fmaxf(M, xs[q]);
+  }
+  if (p.renorm) M = group_fmax<G>(M, mask);
+  float h[kSlots], sum = 0.f, dot = 0.f;
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    if (!p.renorm) h[q] = p.sigmoid ? sigmoid32(xs[q]) : __expf(xs[q] - m) * rz;
+    else if (p.sigmoid && M >= -40.f) h[q] = sigmoid32(xs[q]);
+    else h[q] = M == -INFINITY ? 0.f : expf(xs[q] - M);
+    if (e[q] < 0) h[q] = 0.f;
+    sum += h[q];
+  }
+  if (p.renorm) {
+    sum = group_sum<G>(sum, mask);
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) h[q] = sum == 0.f ? 0.f : __fdiv_rn(h[q], sum);
+  }
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) dot += c[q] * h[q];
+  if (p.renorm || dense) dot = group_sum<G>(dot, mask);
+  float d[kSlots];
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    d[q] = h[q] == 0.f ? 0.f : p.scale * h[q] * (p.renorm ? c[q] - dot : c[q]);
+    if (p.sigmoid) d[q] *= sigmoid32(-xs[q]);   // (of a slot without an expert 1)
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = dense ? -(v[i] * rz) * (p.scale * dot) : 0.f;
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q)
+    for (int rr = 0; rr < G; ++rr) {
+      if (q * G + rr >= p.k) break;
+      const int at_e = __shfl_sync(mask, e[q], rr, G) - e0;
+      const float add = __shfl_sync(mask, d[q], rr, G);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (at_e == i) v[i] += add;
+    }
+  if (at < p.T) store_row<T, NV>(static_cast<T*>(p.dl) + t * p.E, e0, p.E, v);
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+
+SelParams params_of(const Select& c) {
+  SelParams p{};
+  p.T = c.T;
+  p.E = c.E;
+  p.k = c.k;
+  p.n = c.n;
+  p.per = c.E / c.n;
+  p.top = c.top;
+  p.sum = c.sum;
+  p.sigmoid = c.sigmoid;
+  p.renorm = c.renorm;
+  p.scale = c.scale;
+  return p;
+}
+
+// A functor's call<T, G, NV>() for the type of the logits and the number of experts.
+template <class T, class F>
+cudaError_t by_experts(int E, F f) {
+  if (E <= 8) return f.template call<T, 8, 1>();
+  if (E <= 16) return f.template call<T, 8, 2>();
+  if (E <= 32) return f.template call<T, 8, 4>();
+  if (E <= 64) return f.template call<T, 16, 4>();
+  if (E <= 128) return f.template call<T, 16, 8>();
+  if (E <= 256) return f.template call<T, 32, 8>();
+  if (E <= 512) return f.template call<T, 32, 16>();
+  return f.template call<T, 32, 32>();
+}
+
+template <class F>
+cudaError_t by_type(const Select& c, F f) {
+  if (c.dtype == MOE_BF16) return by_experts<__nv_bfloat16>(c.E, f);
+  if (c.dtype == MOE_FP16) return by_experts<__half>(c.E, f);
+  return by_experts<float>(c.E, f);
+}
+
+int64_t blocks_of(int64_t T, int per_warp) { return (T + kWarps * per_warp - 1) / (kWarps * per_warp); }
+
+struct Forward {
+  const SelParams& p;
+  cudaStream_t s;
+  template <class T, int G, int NV>
+  cudaError_t call() const {
+    const bool keys = p.bias != nullptr || (p.top < p.n && p.sum == 2);
+    const int64_t blocks = blocks_of(p.T, 32 / G);
+    return keys ? launch_after(select_kernel<T, G, NV, true>, blocks, 32 * kWarps, 0, 1, s, p)
+                : launch_after(select_kernel<T, G, NV, false>, blocks, 32 * kWarps, 0, 1, s, p);
+  }
+};
+
+struct Backward {
+  const SelParams& p;
+  cudaStream_t s;
+  template <class T, int G, int NV>
+  cudaError_t call() const {
+    return launch_after(select_bwd_kernel<T, G, NV>, blocks_of(p.T, 32 / G), 32 * kWarps, 0, 1, s, p);
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_select(const Select& c, const void* logits, const float* bias, int32_t* idx, float* w,
+                          cudaStream_t s) {
+  if (c.T == 0) return cudaSuccess;
+  SelParams p = params_of(c);
+  p.logits = logits;
+  p.bias = bias;
+  p.idx = idx;
+  p.w = w;
+  prof_mark(kKSelect, s, true);
+  const cudaError_t e = by_type(c, Forward{p, s});
+  prof_mark(kKSelect, s, false);
+  return e;
+}
+
+cudaError_t launch_select_bwd(const Select& c, const void* logits, const int32_t* idx, const float* dw, void* dl,
+                              cudaStream_t s) {
+  if (c.T == 0) return cudaSuccess;
+  SelParams p = params_of(c);
+  p.logits = logits;
+  p.idx = const_cast<int32_t*>(idx);
+  p.dw = dw;
+  p.dl = dl;
+  prof_mark(kKSelectBwd, s, true);
+  const cudaError_t e = by_type(c, Backward{p, s});
+  prof_mark(kKSelectBwd, s, false);
+  return e;
+}
+
+}  // namespace moe
