@@ -444,6 +444,7 @@ moe_status_t moe_router_wgrad(const moe_config_t* cfg, const moe_bf16* x, const 
  *   moe_grouped_mm_dx   dx_r = W[g]^T dy_r
  *   moe_grouped_mm_dw   dW[g] = sum over the group's rows of dy_r x_r^T
  *   moe_grouped_mm_i8   y_r  = s_r (P[g] q_r) t[g]            8-bit integers q, P with their scales s, t
+ *   moe_grouped_mm_mxf4 y_r  = P[g] q_r                       4-bit floating point with a scale for 32 values
  *
  * Groups.  row_begin, row_end [groups] int32 on the device: group g is rows row_begin[g] ..
  * row_end[g] - 1.  Groups come in row order and do not overlap (0 <= row_begin[g] <= row_end[g] <=
@@ -523,6 +524,33 @@ moe_status_t moe_quantize_rows_i8(const void* src, int32_t dtype, int64_t rows, 
 moe_status_t moe_grouped_mm_i8(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
                                const int8_t* codes, const float* scales, const int8_t* Wq, const float* W_scale,
                                void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Microscaled 4-bit floating point (OCP Microscaling Formats 1.0, MXFP4): every 32 consecutive values of a row share
+ * one power of two X, and each is an e2m1 code, 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with a sign, times X.
+ *   codes   [rows, cols / 2] bytes, two codes to a byte, the value of the lower index in the low four bits
+ *             (magnitude in the low three of them, in the order above; sign in the fourth)
+ *   scales  [rows, stride] bytes, the first cols / 32 of a row its X as E8M0: 2^(byte - 127); 255 is NaN.  stride,
+ *             from moe_mx_scale_stride, is cols / 32 rounded up to 16
+ * For activations and for weights alike (weights [groups, n_out, n_in] are groups * n_out rows).
+ *
+ * moe_quantize_rows_mxf4: src [rows, cols] (dtype MOE_BF16, MOE_FP16 or MOE_FP32), X = 2^(floor(log2(largest
+ * magnitude)) - 2), at least 2^-127 (and that for a block of zeros), code = v / X to the nearest, ties to the even
+ * code, at most 6 in magnitude.  A NaN or an infinity makes its block's X NaN, with codes of 0.  Bytes of a row of
+ * scales past cols / 32 are set to 0.  cols a multiple of 32, at most 65536; rows at most 2^28; all
+ * pointers 16-byte aligned. */
+moe_status_t moe_mx_scale_stride(int32_t cols, int32_t* stride);
+moe_status_t moe_quantize_rows_mxf4(const void* src, int32_t dtype, int64_t rows, int32_t cols, uint8_t* codes,
+                                    uint8_t* scales, moe_stream_t stream);
+
+/* codes [rows, n_in / 2] with scales [rows, stride], Wq [groups, n_out, n_in / 2] with W_scale [groups, n_out,
+ * stride] -> y [rows, n_out] (dtype).  n_in and in_stride (in values, of the codes' rows) multiples of 32; the scales'
+ * rows are stride bytes apart whatever in_stride is, and their bytes past n_in / 32 are not used.  Rows, weights, codes and
+ * scales are 16-byte aligned.  Products with both scales are exact and summed in fp32 by the tensor cores (they
+ * lose what moe_grouped_mm's sums lose), products below fp32's range may count as 0, and a scale of NaN makes NaN of
+ * the outputs of its row or of its weight's output channel. */
+moe_status_t moe_grouped_mm_mxf4(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
+                                 const uint8_t* codes, const uint8_t* scales, const uint8_t* Wq, const uint8_t* W_scale,
+                                 void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Synchronise `stream`, return the first device-side error recorded in ws since the last check
  * (MOE_OK if none) and clear it.  Returns MOE_ERR_CUDA if the stream itself reports an error. */

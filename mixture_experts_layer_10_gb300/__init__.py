@@ -30,7 +30,8 @@ EXPORTS = ("moe_workspace_size", "moe_perm_rows", "moe_workspace_init", "moe_rou
            "moe_keep_rows_for_budget", "moe_keep_rows_for_free_memory", "moe_quantize_cols_e4m3",
            "moe_layer_bwd_fp8", "moe_saved_layout", "moe_profile_sm_clock", "moe_grouped_workspace_size",
            "moe_grouped_workspace_init", "moe_segments", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
-           "moe_quantize_rows_i8", "moe_grouped_mm_i8", "moe_select", "moe_select_bwd", "moe_router_wgrad")
+           "moe_quantize_rows_i8", "moe_grouped_mm_i8", "moe_select", "moe_select_bwd", "moe_router_wgrad",
+           "moe_mx_scale_stride", "moe_quantize_rows_mxf4", "moe_grouped_mm_mxf4")
 
 
 class moe_config_t(ctypes.Structure):
@@ -123,6 +124,9 @@ def load(path: str | None = None):
         "moe_grouped_mm_dw": [grpp, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
         "moe_quantize_rows_i8": [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P, _P, _P],
         "moe_grouped_mm_i8": [grpp, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+        "moe_mx_scale_stride": [ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
+        "moe_quantize_rows_mxf4": [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P, _P, _P],
+        "moe_grouped_mm_mxf4": [grpp, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
         "moe_select": [selp, _P, _P, _P, _P, _P],
         "moe_select_bwd": [selp, _P, _P, _P, _P, _P],
         "moe_router_wgrad": [cfgp, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
@@ -216,7 +220,8 @@ def _bind_torch():
         _current_device = torch._C._cuda_getDevice
     _current_stream = torch._C._cuda_getCurrentRawStream
     _holds = {BF16: (torch.bfloat16, torch.int16, torch.uint16), FP16: (torch.float16, torch.int16, torch.uint16),
-              "f32": (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,)}
+              "f32": (torch.float32,), "i32": (torch.int32,), "i8": (torch.int8,),
+              "u8": (torch.uint8,)}
 
 
 def _grouped_ptr(t, shape, kind, what, on, stride=0):
@@ -516,6 +521,40 @@ def moe_grouped_mm_i8(cfg, row_begin, row_end, codes, scales, Wq, W_scale, y, ws
           _grouped_ptr(scales, (c.rows,), "f32", "scales", on),
           _grouped_ptr(Wq, (c.groups, c.n_out, c.n_in), "i8", "Wq", on),
           _grouped_ptr(W_scale, (c.groups, c.n_out), "f32", "W_scale", on),
+          _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws, on, stream))
+
+
+def moe_mx_scale_stride(cols: int) -> int:
+    """Bytes from one row of 4-bit values' scales to the next: cols / 32 rounded up to 16."""
+    n = ctypes.c_int32()
+    _call("moe_mx_scale_stride", int(cols), ctypes.byref(n))
+    return n.value
+
+
+def moe_quantize_rows_mxf4(src, codes, scales, stream=None):
+    """src [.., rows, cols] bf16, fp16 or fp32 -> codes [.., rows, cols / 2] and scales [.., rows,
+    moe_mx_scale_stride(cols)], both uint8."""
+    cols = src.shape[-1]
+    rows = src.numel() // cols if cols else 0
+    code, on = dtype_code(src.dtype), src.get_device()
+    _on_current(on, src, "src")
+    lead = tuple(src.shape[:-1])
+    _call("moe_quantize_rows_mxf4", _grouped_ptr(src, tuple(src.shape), "f32" if code == FP32 else code, "src", on), code,
+          int(rows), int(cols), _grouped_ptr(codes, (*lead, cols // 2), "u8", "codes", on),
+          _grouped_ptr(scales, (*lead, (cols // 32 + 15) // 16 * 16), "u8", "scales", on),
+          _current_stream(on) if stream is None else _stream(stream))
+
+
+def moe_grouped_mm_mxf4(cfg, row_begin, row_end, codes, scales, Wq, W_scale, y, ws, stream=None):
+    """y = x W[g]^T of 4-bit values with their scales, as moe_quantize_rows_mxf4 gives them."""
+    c, n, on = cfg, (cfg.groups,), ws.get_device()
+    lds = (c.n_in // 32 + 15) // 16 * 16
+    _call("moe_grouped_mm_mxf4", ctypes.byref(c), _grouped_ptr(row_begin, n, "i32", "row_begin", on),
+          _grouped_ptr(row_end, n, "i32", "row_end", on),
+          _grouped_ptr(codes, (c.rows, c.n_in // 2), "u8", "codes", on, c.in_stride // 2),
+          _grouped_ptr(scales, (c.rows, lds), "u8", "scales", on),
+          _grouped_ptr(Wq, (c.groups, c.n_out, c.n_in // 2), "u8", "Wq", on),
+          _grouped_ptr(W_scale, (c.groups, c.n_out, lds), "u8", "W_scale", on),
           _grouped_ptr(y, (c.rows, c.n_out), c.dtype, "y", on, c.out_stride), *_grouped_ws(ws, on, stream))
 
 

@@ -236,7 +236,8 @@ const char* const kKernelNames[] = {
     "gemm_router_dx", "swiglu_bwd_kept", "gemm_gate_up_fp8", "quantize_e4m3", "gemm_down_fp8",
     "quantize_cols_e4m3", "gemm_bwd_dgrad_down_fp8", "gemm_bwd_recompute_swiglu_fp8", "gemm_dgrad_x_fp8",
     "router_split_wr", "to_bf16_rows", "grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "grouped_mm_i8",
-    "quantize_i8", "grouped_maps", "segments", "select", "select_bwd", "router_dlogits_rows"};
+    "quantize_i8", "grouped_maps", "segments", "select", "select_bwd", "router_dlogits_rows",
+    "quantize_mxf4", "grouped_mm_mxf4"};
 static_assert(sizeof(kKernelNames) / sizeof(kKernelNames[0]) == kKCount, "a name for every kernel id");
 
 struct Profiler {
@@ -1147,6 +1148,40 @@ moe_status_t moe_grouped_mm_i8(const moe_grouped_t* cfg, const int32_t* row_begi
   MOE_TRY(check_device());
   MOE_CUDA(launch_grouped_i8(c, row_begin, row_end, codes, scales, Wq, W_scale, static_cast<uint16_t*>(y), hdr,
                              stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_mx_scale_stride(int32_t cols, int32_t* stride) {
+  MOE_NEED(stride != nullptr && cols >= 32 && cols <= 65536 && cols % 32 == 0);
+  *stride = mx_scale_stride(cols);
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_rows_mxf4(const void* src, int32_t dtype, int64_t rows, int32_t cols, uint8_t* codes,
+                                    uint8_t* scales, moe_stream_t stream) {
+  MOE_NEED(dtype == MOE_BF16 || dtype == MOE_FP16 || dtype == MOE_FP32);
+  MOE_NEED(rows >= 0 && rows <= (int64_t)1 << 28 && cols >= 32 && cols <= 65536 && cols % 32 == 0);
+  MOE_NEED(rows == 0 || (src && codes && scales));
+  MOE_NEED(aligned16(src) && aligned16(codes) && aligned16(scales));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_quantize_rows_mxf4(src, dtype, rows, cols, codes, scales, stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_mm_mxf4(const moe_grouped_t* cfg, const int32_t* row_begin, const int32_t* row_end,
+                                 const uint8_t* codes, const uint8_t* scales, const uint8_t* Wq, const uint8_t* W_scale,
+                                 void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Grouped c;
+  Hdr* hdr = nullptr;
+  MOE_TRY(make_grouped(cfg, &c));
+  MOE_NEED(c.K % 32 == 0 && c.ldi % 32 == 0);
+  MOE_NEED(row_begin && row_end && aligned4(row_begin) && aligned4(row_end));
+  MOE_NEED(Wq && W_scale && aligned16(Wq) && aligned16(W_scale) && (c.rows == 0 || (codes && scales && y)) &&
+           aligned16(codes) && aligned16(scales) && aligned16(y));
+  MOE_TRY(get_grouped_ws(c, ws, ws_bytes, &hdr));
+  MOE_TRY(check_device());
+  MOE_CUDA(launch_grouped_mxf4(c, row_begin, row_end, codes, scales, Wq, W_scale, static_cast<uint16_t*>(y), hdr,
+                               stream));
   return MOE_OK;
 }
 

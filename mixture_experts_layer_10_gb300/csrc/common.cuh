@@ -148,7 +148,7 @@ enum KernelId : int {
   kKDgates, kKRouterDlogits, kKRouterDwr, kKRouterReduce, kKCombineBwd, kKBwdDh, kKRouterDx, kKSwigluKept,
   kKGateUpFp8, kKQuantE4m3, kKDownFp8, kKQuantCols, kKBwdDhFp8, kKBwdFusedFp8, kKDgradXFp8, kKSplitWr,
   kKToBf16, kKGroupedMm, kKGroupedDx, kKGroupedDw, kKGroupedI8, kKQuantI8, kKGroupMaps, kKSegments,
-  kKSelect, kKSelectBwd, kKDlogitsRows,
+  kKSelect, kKSelectBwd, kKDlogitsRows, kKQuantMxf4, kKGroupedMxf4,
   kKCount
 };
 void prof_mark(int id, cudaStream_t s, bool begin);
@@ -361,6 +361,13 @@ cudaError_t launch_stream_mm(const Grouped& c, const int32_t* begin, const int32
                              const uint16_t* W, uint16_t* y, Hdr* hdr, cudaStream_t s);
 cudaError_t launch_stream_i8(const Grouped& c, const int32_t* begin, const int32_t* end, const int8_t* q,
                              const float* qs, const int8_t* Wq, const float* Ws, uint16_t* y, Hdr* hdr, cudaStream_t s);
+// 4-bit rows: codes [rows, cols / 2] and scale exponents [rows, mx_scale_stride(cols)], and their products.
+inline int mx_scale_stride(int cols) { return (cols / 32 + 15) / 16 * 16; }
+cudaError_t launch_quantize_rows_mxf4(const void* src, int dtype, int64_t rows, int cols, uint8_t* codes,
+                                      uint8_t* scales, cudaStream_t s);
+cudaError_t launch_grouped_mxf4(const Grouped& c, const int32_t* begin, const int32_t* end, const uint8_t* q,
+                                const uint8_t* qx, const uint8_t* Wq, const uint8_t* Wx, uint16_t* y, Hdr* hdr,
+                                cudaStream_t s);
 // Expert selection from logits (select.cu)
 struct Select {            // validated description
   int T, E, k, n, top, sum;   // n groups of experts, of which `top` stay, scored by their `sum` largest keys

@@ -56,7 +56,7 @@ namespace moe {
 
 namespace {
 
-enum Op { kMm, kDx, kDw, kI8 };
+enum Op { kMm, kDx, kDw, kI8, kMx };
 
 constexpr int kBM = 128;                     // rows of the M side a CTA holds
 constexpr int kTile = 256;                   // pair tile, both sides
@@ -69,15 +69,24 @@ constexpr int kRun = 2048;                   // rows of a run of the weight grad
 constexpr int kTmemCols = 512;
 constexpr int kAhead = 4;                    // raw stages of weights fetched to L2 ahead (8-bit integers)
 
+constexpr int kMxRows = 192;                 // 4-bit: rows of a tile (two accumulators leave the scales 128 columns)
+constexpr int kMxWide = 128;                 // 4-bit: bytes of a row in a stage, 256 values
+constexpr int kMxBlocks = 8;                 // and their scales
+constexpr uint32_t kMxScales = 3 * 1024;     // a stage's scales: 128 rows of the weight, 256 rows, 8 bytes each
+constexpr int kAheadMx = 4;                  // 4-bit: times 16 scales of a row on their way
+constexpr int kMxCols = 24;                  // their TMEM columns: 2 words x (4 + 8)
+
 template <int kOp>
 struct Shape {
-  static constexpr int kStages = kOp == kI8 ? 4 : 6;
+  static constexpr int kStages = kOp == kI8 ? 4 : (kOp == kMx ? 5 : 6);
+  static constexpr int kRows = kOp == kMx ? kMxRows : kTile;   // N side of a tile
+  static constexpr uint32_t kScales = kOp == kMx ? kMxScales : 0;
   static constexpr int kRaw = kOp == kI8 ? 2 : 0;          // 8-bit integers: stages of codes, two K blocks each,
   static constexpr int kTeams = 4, kTeam = 4;              // and the teams of warps that widen them
-  static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : 0;
+  static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : (kOp == kMx ? 4 : 0);
   static constexpr int kEpiWarps = kOp == kDw ? 8 : 4;
   static constexpr int kThreads = 32 * (2 + kEpiWarps + kExtra);
-  static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + 512 + sizeof(GroupTab);
+  static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kStages * kScales + 512 + sizeof(GroupTab);
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
@@ -88,8 +97,10 @@ struct Params {
   const int32_t *begin, *end;
   void* y;
   const float *qs, *ws;       // scales of the rows and of the output channels (8-bit integers)
+  const uint8_t *qx, *wx;     // scale exponents of the rows and of the weights (4-bit), [.., ldx]
+  int blocks, ldx;            // of a row: scales, and bytes from one row's to the next's
   int64_t rows, ldy;
-  int depth;                  // contraction length (rows times a weight)
+  int depth;                  // contraction length (rows times a weight; 4-bit: its bytes)
   int width;                  // features of the output row; weight gradient: columns of dW (n_in)
   int M;                      // weight gradient: rows of a dW (n_out)
   int G, nf, mf;              // whole tiles across width; weight gradient: all tiles across width and M
@@ -111,6 +122,7 @@ struct Job {
 // Rows times a weight: tile t -> group, row tile, feature tile.  Groups in order; within a group,
 // chunks of up to 16 row tiles x all feature tiles with the row tile fastest, so that the pairs at work
 // share a panel of each operand in L2.
+template <int kRowTile>
 __device__ __forceinline__ Job row_job(const Params& p, const GroupTab& s, int t) {
   // the tiles of the last, narrower feature tile (if there is one) come after all others: what is
   // left to do while the last pairs finish is then short
@@ -131,8 +143,8 @@ __device__ __forceinline__ Job row_job(const Params& p, const GroupTab& s, int t
   const int r = local - c * kChunkM * nf;
   Job j{};
   j.g = lo;
-  j.row = s.begin[lo] + (c * kChunkM + r % cm) * kTile;
-  j.n = min(kTile, s.end[lo] - j.row);
+  j.row = s.begin[lo] + (c * kChunkM + r % cm) * kRowTile;
+  j.n = min(kRowTile, s.end[lo] - j.row);
   j.f0 = narrow ? p.nf * kTile : r / cm * kTile;
   return j;
 }
@@ -157,7 +169,7 @@ __device__ __forceinline__ Job dw_job(const Params& p, const GroupTab& s, int t,
   return j;
 }
 
-// The rows' box for a half of n rows: 0 (128 rows), 1 (64) or 2 (32).
+// The rows' box for a half of n rows: 0 (128 rows, 4-bit: 96), 1 (64) or 2 (32).
 __device__ __forceinline__ int box_of(int half) { return half > 64 ? 0 : (half > 32 ? 1 : 2); }
 
 // One pair's walk over its tiles, the same in every role of both CTAs: rows times a weight has one job a
@@ -172,8 +184,9 @@ struct Walk {
   __device__ bool next(Job& j) {
     if (kOp != kDw) {
       if (t >= ntiles) return false;
-      j = row_job(p, s, t);
-      j.kits = (p.depth + kBK - 1) / kBK;
+      constexpr int kDeep = kOp == kMx ? kMxWide : kBK;
+      j = row_job<Shape<kOp>::kRows>(p, s, t);
+      j.kits = (p.depth + kDeep - 1) / kDeep;
       t += step;
       return true;
     }
@@ -394,7 +407,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = smem;
   uint8_t* raws = stages + kStages * kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(raws + S::kRaw * kStage);
+  uint8_t* scales = raws + S::kRaw * kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kStages * S::kScales);
   uint64_t* empty = full + 6;
   uint64_t* raw = empty + 6;
   uint64_t* rempty = raw + 6;
@@ -403,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  GroupTab& tab = *reinterpret_cast<GroupTab*>(raws + S::kRaw * kStage + 512);
+  GroupTab& tab = *reinterpret_cast<GroupTab*>(scales + kStages * S::kScales + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -412,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     for (int s = 0; s < 6; ++s) {
       mbar_init(&full[s], kOp == kI8 ? 2 * S::kTeam : 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&raw[s], 1);
+      mbar_init(&raw[s], kOp == kMx ? 2 * S::kExtra : 1);
       mbar_init(&rempty[s], S::kTeams * S::kTeam);
     }
     for (int a = 0; a < 2; ++a) {
@@ -432,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     tmem_relinquish_pair();
   }
   after_previous_kernel();
-  const int rtiles = load_groups(tab, p.begin, p.end, p.G, p.rows, kTile, p.hdr);
+  const int rtiles = load_groups(tab, p.begin, p.end, p.G, p.rows, S::kRows, p.hdr);
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // both CTAs' barriers exist before any remote arrival
@@ -485,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       } else {
         while (ok && !*abort_flag && walk.next(j)) {
           const int half = ((j.n + 31) / 32 * 32) / 2, bx = kOp == kDw ? 0 : box_of(half);
-          const uint32_t bytes = kHalf + (kOp == kDw ? kHalf : (128u >> bx) * 128u);
+          const uint32_t bytes = kHalf + (kOp == kDw ? kHalf : (kOp == kMx && bx == 0 ? 96u : 128u >> bx) * 128u);
           const CUtensorMap* ma = &p.a;
           const CUtensorMap* mb = &p.b[bx];
           if constexpr (kOp == kDw) {
@@ -523,16 +537,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
                 }
               } else {
                 const int f = j.f0 + kBM * rank;
-                if (kOp == kMm) {
-                  tma_load_3d_pair(st, ma, bar, kit * kBK, f, j.g);
+                if (kOp == kMm || kOp == kMx) {
+                  tma_load_3d_pair(st, ma, bar, kit * (kOp == kMx ? kMxWide : kBK), f, j.g);
                 } else {
                   tma_load_3d_pair(st, ma, bar, f, kit * kBK, j.g);
                   tma_load_3d_pair(st + kBox, ma, bar, f + 64, kit * kBK, j.g);
                 }
-                tma_load_2d_pair(st + kHalf, mb, bar, kit * kBK, j.row + half * rank);
+                tma_load_2d_pair(st + kHalf, mb, bar, kit * (kOp == kMx ? kMxWide : kBK), j.row + half * rank);
               }
             }
-            if (rank == 0 && uses >= kStages) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 1));
+            if (kOp != kMx && rank == 0 && uses >= kStages) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 1));
             ++uses;
             if (++slot == kStages) {
               slot = 0;
@@ -556,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
         const uint32_t idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(n >> 3) << 17);
         more = walk.next(j);   // the next job, worked out while this one's products run
         if (kits == 0) continue;
-        const uint32_t dt = tmem_base + (uint32_t)(acc * kTile);
+        const uint32_t dt = tmem_base + (uint32_t)(acc * S::kRows);
         if (!wait_nap<20>(&tempty[acc], acc_phase ^ 1, limit, abort_flag)) {
           fail(kSiteGroupedMma);
           break;
@@ -568,15 +582,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
             ok = false;
             break;
           }
+          if (kOp == kMx && !wait_nap<20, true>(&raw[slot], phase, limit, abort_flag)) {
+            fail(kSiteGroupedMma);
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint32_t sa = smem_u32(stages + (size_t)slot * kStage);
+          if constexpr (kOp == kMx) {
+            // the stage's scales have TMEM columns of their own, free since the stage was last read
+            const uint32_t sf = tmem_base + 2 * S::kRows + slot * kMxCols, ss = smem_u32(scales + slot * kMxScales);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
+            for (int w = 0; w < 2; ++w) {
+              tmem_copy_scales_pair(sf + w * 4, sdesc_scales(ss + w * 512));
+              tmem_copy_scales_pair(sf + 8 + w * 8, sdesc_scales(ss + 1024 + w * 1024));
+              if (n > 128) tmem_copy_scales_pair(sf + 12 + w * 8, sdesc_scales(ss + 1536 + w * 1024));
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_mxf4_pair(dt, sdesc_kmajor(sa + kk * 32), sdesc_kmajor(sa + kHalf + kk * 32),
+                             idesc | idesc_scales((kk & 1) * 2), sf + (kk >> 1) * 4, sf + 8 + (kk >> 1) * 8, (kit | kk) != 0);
+          }
+#pragma unroll
+          for (int kk = 0; kOp != kMx && kk < kBK / 16; ++kk) {
             const uint64_t da = kOp == kMm || kOp == kI8 ? sdesc_kmajor(sa + kk * 32) : sdesc_mnmajor(sa + kk * 2048, kBox);
             const uint64_t db = kOp == kDw ? sdesc_mnmajor(sa + kHalf + kk * 2048, kBox) : sdesc_kmajor(sa + kHalf + kk * 32);
             umma_bf16_pair(dt, da, db, idesc, (kit | kk) != 0);
           }
-          if (kOp == kI8) umma_commit_both(&empty[slot]);
+          if (kOp == kI8 || kOp == kMx) umma_commit_both(&empty[slot]);
           else umma_commit_pair(smem_u32(&empty[slot]));
           if (++slot == kStages) {
             slot = 0;
@@ -608,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       tc_fence_after();
       return true;
     };
-    auto acc_addr = [&]() { return tmem_base + (uint32_t)(acc * kTile) + ((uint32_t)(q * 32) << 16); };
+    auto acc_addr = [&]() { return tmem_base + (uint32_t)(acc * S::kRows) + ((uint32_t)(q * 32) << 16); };
     auto release_acc = [&]() {
       tc_fence_before();
       __syncwarp();
@@ -712,6 +745,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       block += kits;
       rblock += rkits;
     }
+  } else if constexpr (kOp == kMx) {
+    // Scales: a thread has a row of the weight's 128 and two of the tile's; it brings 16 bytes of each, which are two
+    // stages', while the two before are on their way, and puts its words where the copy to TMEM wants them: row r
+    // in 16-byte line r % 32, word r / 32.  Bytes past the last scale of a row are zero, whatever they held.
+    const int r = threadIdx.x - 32 * (2 + S::kEpiWarps);
+    const uint32_t to = (r & 31) * 16 + (r >> 5) * 4;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    auto fetch = [&](const uint8_t* from, int at) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (from == nullptr || at >= p.blocks) return v;
+      v = __ldg(reinterpret_cast<const uint4*>(from + at));
+      const int left = p.blocks - at;
+      if (left < 16) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int bytes = min(4, max(0, left - 4 * i));
+          w[i] &= bytes == 4 ? 0xffffffffu : (1u << (8 * bytes)) - 1u;
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      return v;
+    };
+    // what is on its way: kAheadMx times 16 bytes of each row, of the tiles to come too
+    struct Pair {
+      uint4 a, b, c;
+      int stages;
+    } ring[kAheadMx];
+    int kit = 0, kits = 0;
+    const uint8_t *pa = nullptr, *pb = nullptr, *pc = nullptr;
+    auto next_pair = [&](Pair& v) {
+      if (kit >= kits) {
+        kit = kits = 0;
+        if (walk.next(j)) {
+          const int f = j.f0 + kBM * rank + r;
+          pa = f < p.width ? p.wx + ((int64_t)j.g * p.width + f) * p.ldx : nullptr;
+          pb = r < j.n ? p.qx + ((int64_t)j.row + r) * p.ldx : nullptr;
+          pc = r + 128 < j.n ? p.qx + ((int64_t)j.row + r + 128) * p.ldx : nullptr;
+          kits = j.kits;
+        }
+      }
+      v.stages = min(2, kits - kit);
+      if (v.stages == 0) return;
+      v.a = fetch(pa, kit * kMxBlocks);
+      v.b = fetch(pb, kit * kMxBlocks);
+      v.c = fetch(pc, kit * kMxBlocks);
+      kit += 2;
+    };
+#pragma unroll
+    for (int d = 0; d < kAheadMx; ++d) next_pair(ring[d]);
+    while (ok) {
+#pragma unroll
+      for (int d = 0; d < kAheadMx; ++d) {
+        Pair& v = ring[d];
+        if (v.stages == 0) ok = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || h >= v.stages) continue;
+          ok = __all_sync(0xffffffffu, wait_nap<20>(&empty[slot], phase ^ 1, limit, abort_flag));
+          if (!ok) {
+            if (lane == 0) fail(kSiteGroupedStage);
+            continue;
+          }
+          uint8_t* st = scales + slot * kMxScales + to;
+          *reinterpret_cast<uint32_t*>(st) = h ? v.a.z : v.a.x;
+          *reinterpret_cast<uint32_t*>(st + 512) = h ? v.a.w : v.a.y;
+          *reinterpret_cast<uint32_t*>(st + 1024) = h ? v.b.z : v.b.x;
+          *reinterpret_cast<uint32_t*>(st + 2048) = h ? v.b.w : v.b.y;
+          *reinterpret_cast<uint32_t*>(st + 1536) = h ? v.c.z : v.c.x;
+          *reinterpret_cast<uint32_t*>(st + 2560) = h ? v.c.w : v.c.y;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            fence_release_smem();
+            mbar_arrive_cluster_relaxed(cluster_addr(&raw[slot], 0));
+          }
+          if (++slot == kStages) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) next_pair(v);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -762,6 +881,16 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base
   const cuuint32_t es[4] = {1, 1, 1, 1};
   return fn && fn(m, type, rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of 4-bit values [rows, bytes] as K-major boxes of 128 bytes x 96, 64 and 32 rows.
+bool map_mx_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t bytes, uint64_t ld) {
+  const cuuint64_t dims[2] = {bytes, rows}, strides[1] = {ld};
+  for (uint32_t i = 0; i < kBoxes; ++i) {
+    const cuuint32_t box[2] = {kMxWide, 96 - 32 * i};
+    if (!encode(&m[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
+  }
+  return true;
 }
 
 constexpr CUtensorMapDataType k16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;   // (fp16 values too: bits are copied)
@@ -853,7 +982,7 @@ cudaError_t launch(const Params& p, int64_t most_tiles, int id, cudaStream_t s) 
 }
 
 // The most row tiles the rows can make.
-int64_t most_row_tiles(const Grouped& c) { return c.rows / kTile + std::min<int64_t>(c.G, c.rows); }
+int64_t most_row_tiles(const Grouped& c, int tile = kTile) { return c.rows / tile + std::min<int64_t>(c.G, c.rows); }
 
 }  // namespace
 
@@ -933,6 +1062,27 @@ cudaError_t launch_grouped_i8(const Grouped& c, const int32_t* begin, const int3
   p.narrow = c.N % kTile != 0;
   p.idesc = idesc_of(true, false, false);   // widened codes are fp16, whatever y's type
   return launch<kI8>(p, most_row_tiles(c) * (p.nf + p.narrow), kKGroupedI8, s);
+}
+
+cudaError_t launch_grouped_mxf4(const Grouped& c, const int32_t* begin, const int32_t* end, const uint8_t* q,
+                                const uint8_t* qx, const uint8_t* Wq, const uint8_t* Wx, uint16_t* y, Hdr* hdr,
+                                cudaStream_t s) {
+  if (c.rows == 0) return cudaSuccess;
+  Params p = params_of(c, begin, end, hdr);
+  if (!map_weight(&p.a, Wq, true, c.G, c.N, c.K / 2) || !map_mx_rows(p.b, q, c.rows, c.K / 2, c.ldi / 2))
+    return cudaErrorInvalidValue;
+  p.y = y;
+  p.ldy = c.ldo;
+  p.qx = qx;
+  p.wx = Wx;
+  p.blocks = c.K / 32;
+  p.ldx = mx_scale_stride(c.K);
+  p.depth = c.K / 2;
+  p.width = c.N;
+  p.nf = c.N / kTile;
+  p.narrow = c.N % kTile != 0;
+  p.idesc = idesc_mxf4(kTile, kMxRows);
+  return launch<kMx>(p, most_row_tiles(c, kMxRows) * (p.nf + p.narrow), kKGroupedMxf4, s);
 }
 
 cudaError_t launch_segments(const Tables* tabs, int G, int32_t* begin, int32_t* end, cudaStream_t s) {

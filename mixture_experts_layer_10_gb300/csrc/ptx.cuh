@@ -325,6 +325,24 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+// The pair MMA with 4-bit floating-point operands (e2m1, two to a byte) and a power-of-two scale for every 32
+// products' factors (kind::mxf4, K = 64 per instruction: the same 32 bytes of each K-major row).  The scales lie in
+// the TMEM of both CTAs at sfa (each CTA its own 128 rows of A) and sfb (all N rows of B).
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Scales of 128 rows from shared memory to four TMEM columns, in both CTAs (each from its own shared memory): 32
+// lanes of 16 bytes, given to all four lane quarters.  Before the MMAs that this thread issues after it.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+
 // Arrive once on the mbarrier at shared::cluster address `cbar` (this CTA's or the peer's) when
 // every pair MMA this thread issued so far has completed.
 __device__ __forceinline__ void umma_commit_pair(uint32_t cbar) {
@@ -449,6 +467,18 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
 // kind::f8f6f4 with E4M3 A and B (format code 0 in bits 7-9 and 10-12), fp32 accumulator, K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// kind::mxf4, e2m1 A and B (format code 1), e8m0 scales (bit 23), K-major: bits 17-22 N >> 3, 27-28 M >> 7.
+// Which two bytes of a scale word an instruction takes: idesc_scales(0 or 2), bits 4-5 (B) and 29-30 (A).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
+}
+__host__ __device__ constexpr uint32_t idesc_scales(uint32_t id) { return (id << 4) | (id << 29); }
+
+// Source of tmem_copy_scales: 32 rows of 16 bytes on end, no swizzle (8-row groups 128 bytes apart).
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
 }
 
 }  // namespace moe
