@@ -72,7 +72,8 @@ constexpr int kAhead = 4;                    // raw stages of weights fetched to
 constexpr int kMxRows = 192;                 // 4-bit: rows of a tile (two accumulators leave the scales 128 columns)
 constexpr int kMxWide = 128;                 // 4-bit: bytes of a row in a stage, 256 values
 constexpr int kMxBlocks = 8;                 // and their scales
-constexpr uint32_t kMxScales = 3 * 1024;     // a stage's scales: 128 rows of the weight, 256 rows, 8 bytes each
+constexpr int kMxHand = 128 + kMxRows;       // rows whose scales a CTA needs: its rows of the weight, the tile's
+constexpr uint32_t kMxScales = 2 * 16 * kMxHand;   // two hand-overs of 16 bytes each
 constexpr int kAheadMx = 4;                  // 4-bit: times 16 scales of a row on their way
 constexpr int kMxCols = 24;                  // their TMEM columns: 2 words x (4 + 8)
 
@@ -80,13 +81,13 @@ template <int kOp>
 struct Shape {
   static constexpr int kStages = kOp == kI8 ? 4 : (kOp == kMx ? 5 : 6);
   static constexpr int kRows = kOp == kMx ? kMxRows : kTile;   // N side of a tile
-  static constexpr uint32_t kScales = kOp == kMx ? kMxScales : 0;
+  static constexpr uint32_t kScales = kOp == kMx ? kMxScales : 0;   // shared memory for them
   static constexpr int kRaw = kOp == kI8 ? 2 : 0;          // 8-bit integers: stages of codes, two K blocks each,
   static constexpr int kTeams = 4, kTeam = 4;              // and the teams of warps that widen them
   static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : (kOp == kMx ? 4 : 0);
   static constexpr int kEpiWarps = kOp == kDw ? 8 : 4;
   static constexpr int kThreads = 32 * (2 + kEpiWarps + kExtra);
-  static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kStages * kScales + 512 + sizeof(GroupTab);
+  static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kScales + 512 + sizeof(GroupTab);
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
@@ -408,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   uint8_t* stages = smem;
   uint8_t* raws = stages + kStages * kStage;
   uint8_t* scales = raws + S::kRaw * kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kStages * S::kScales);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + S::kScales);
   uint64_t* empty = full + 6;
   uint64_t* raw = empty + 6;
   uint64_t* rempty = raw + 6;
@@ -417,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  GroupTab& tab = *reinterpret_cast<GroupTab*>(scales + kStages * S::kScales + 512);
+  GroupTab& tab = *reinterpret_cast<GroupTab*>(scales + S::kScales + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -590,14 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
           tc_fence_after();
           const uint32_t sa = smem_u32(stages + (size_t)slot * kStage);
           if constexpr (kOp == kMx) {
-            // the stage's scales have TMEM columns of their own, free since the stage was last read
-            const uint32_t sf = tmem_base + 2 * S::kRows + slot * kMxCols, ss = smem_u32(scales + slot * kMxScales);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              tmem_copy_scales_pair(sf + w * 4, sdesc_scales(ss + w * 512));
-              tmem_copy_scales_pair(sf + 8 + w * 8, sdesc_scales(ss + 1024 + w * 1024));
-              if (n > 128) tmem_copy_scales_pair(sf + 12 + w * 8, sdesc_scales(ss + 1536 + w * 1024));
-            }
+            const uint32_t sf = tmem_base + 2 * S::kRows + slot * kMxCols;   // the stage's own columns of scales
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_mxf4_pair(dt, sdesc_kmajor(sa + kk * 32), sdesc_kmajor(sa + kHalf + kk * 32),
@@ -746,17 +740,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       rblock += rkits;
     }
   } else if constexpr (kOp == kMx) {
-    // Scales: a thread has a row of the weight's 128 and two of the tile's; it brings 16 bytes of each, which are two
-    // stages', while the two before are on their way, and puts its words where the copy to TMEM wants them: row r
-    // in 16-byte line r % 32, word r / 32.  Bytes past the last scale of a row are zero, whatever they held.
-    const int r = threadIdx.x - 32 * (2 + S::kEpiWarps);
-    const uint32_t to = (r & 31) * 16 + (r >> 5) * 4;
-    int slot = 0;
+    // Scales go to TMEM from registers, while the tensor cores work.  (Their copies from shared memory, tcgen05.cp, take
+    // turns with the products: 56 cycles each, six a stage of 384.)  They lie there as row r in lane r % 32 of all four
+    // lane quarters, column r / 32, a word for 128 values; so each of the four warps, which may write one
+    // quarter, needs every row's.  A thread brings 16 bytes of a row of the weight's 128 and of one or two of the
+    // tile's, which are two stages', and hands them to all four warps through shared memory.
+    const int r = threadIdx.x - 32 * (2 + S::kEpiWarps), q = warp & 3;
+    int slot = 0, turn = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true;   // (a warp that gives up goes on through the hand-overs, so that no other waits for it in vain)
+    // 16 bytes of a row; 0 past its last scale, whatever is there
     auto fetch = [&](const uint8_t* from, int at) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (from == nullptr || at >= p.blocks) return v;
+      if (from == nullptr) return v;
       v = __ldg(reinterpret_cast<const uint4*>(from + at));
       const int left = p.blocks - at;
       if (left < 16) {
@@ -797,38 +793,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     };
 #pragma unroll
     for (int d = 0; d < kAheadMx; ++d) next_pair(ring[d]);
-    while (ok) {
+    for (bool more = true; more;) {
 #pragma unroll
       for (int d = 0; d < kAheadMx; ++d) {
         Pair& v = ring[d];
-        if (v.stages == 0) ok = false;
+        if (v.stages == 0) more = false;
+        if (!more) break;
+        uint4* hand = reinterpret_cast<uint4*>(scales) + turn * kMxHand;
+        turn ^= 1;
+        hand[r] = v.a;
+        hand[128 + r] = v.b;
+        if (r < kMxRows - 128) hand[256 + r] = v.c;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int stages = v.stages;
+        next_pair(v);
+        uint4 a[4], b[kMxRows / 32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a[c] = hand[32 * c + lane];
+#pragma unroll
+        for (int c = 0; c < kMxRows / 32; ++c) b[c] = hand[128 + 32 * c + lane];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!ok || h >= v.stages) continue;
-          ok = __all_sync(0xffffffffu, wait_nap<20>(&empty[slot], phase ^ 1, limit, abort_flag));
-          if (!ok) {
-            if (lane == 0) fail(kSiteGroupedStage);
-            continue;
+          if (h >= stages) break;
+          if (ok) {
+            ok = __all_sync(0xffffffffu, wait_nap<20>(&empty[slot], phase ^ 1, limit, abort_flag));
+            if (!ok && lane == 0) fail(kSiteGroupedStage);
           }
-          uint8_t* st = scales + slot * kMxScales + to;
-          *reinterpret_cast<uint32_t*>(st) = h ? v.a.z : v.a.x;
-          *reinterpret_cast<uint32_t*>(st + 512) = h ? v.a.w : v.a.y;
-          *reinterpret_cast<uint32_t*>(st + 1024) = h ? v.b.z : v.b.x;
-          *reinterpret_cast<uint32_t*>(st + 2048) = h ? v.b.w : v.b.y;
-          *reinterpret_cast<uint32_t*>(st + 1536) = h ? v.c.z : v.c.x;
-          *reinterpret_cast<uint32_t*>(st + 2560) = h ? v.c.w : v.c.y;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            fence_release_smem();
-            mbar_arrive_cluster_relaxed(cluster_addr(&raw[slot], 0));
+          if (ok) {
+            tc_fence_after();
+            const uint32_t sf = tmem_base + 2 * S::kRows + slot * kMxCols + ((uint32_t)(q * 32) << 16);
+            uint32_t wa[8], wb[16] = {};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              wa[c] = h ? a[c].z : a[c].x;
+              wa[4 + c] = h ? a[c].w : a[c].y;
+            }
+#pragma unroll
+            for (int c = 0; c < kMxRows / 32; ++c) {
+              wb[c] = h ? b[c].z : b[c].x;
+              wb[8 + c] = h ? b[c].w : b[c].y;
+            }
+            tmem_st8(sf, wa);
+            tmem_st16(sf + 8, wb);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&raw[slot], 0));   // (the writes have completed)
           }
           if (++slot == kStages) {
             slot = 0;
             phase ^= 1;
           }
         }
-        if (ok) next_pair(v);
       }
     }
   }
