@@ -73,8 +73,9 @@ constexpr int kMxRows = 192;                 // 4-bit: rows of a tile (two accum
 constexpr int kMxWide = 128;                 // 4-bit: bytes of a row in a stage, 256 values
 constexpr int kMxBlocks = 8;                 // and their scales
 constexpr int kMxHand = 128 + kMxRows;       // rows whose scales a CTA needs: its rows of the weight, the tile's
-constexpr uint32_t kMxScales = 2 * 16 * kMxHand;   // two hand-overs of 16 bytes each
-constexpr int kAheadMx = 4;                  // 4-bit: times 16 scales of a row on their way
+constexpr int kMxTeams = 2;                  // of four warps, which take turns at two stages each
+constexpr uint32_t kMxScales = kMxTeams * 2 * 16 * kMxHand;   // two hand-overs a team, of 16 bytes a row
+constexpr int kAheadMx = 2;                  // 4-bit: times 16 scales of a row on their way in a team
 constexpr int kMxCols = 24;                  // their TMEM columns: 2 words x (4 + 8)
 
 template <int kOp>
@@ -84,7 +85,7 @@ struct Shape {
   static constexpr uint32_t kScales = kOp == kMx ? kMxScales : 0;   // shared memory for them
   static constexpr int kRaw = kOp == kI8 ? 2 : 0;          // 8-bit integers: stages of codes, two K blocks each,
   static constexpr int kTeams = 4, kTeam = 4;              // and the teams of warps that widen them
-  static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : (kOp == kMx ? 4 : 0);
+  static constexpr int kExtra = kOp == kI8 ? kTeams * kTeam : (kOp == kMx ? 4 * kMxTeams : 0);
   static constexpr int kEpiWarps = kOp == kDw ? 8 : 4;
   static constexpr int kThreads = 32 * (2 + kEpiWarps + kExtra);
   static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kScales + 512 + sizeof(GroupTab);
@@ -427,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     for (int s = 0; s < 6; ++s) {
       mbar_init(&full[s], kOp == kI8 ? 2 * S::kTeam : 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&raw[s], kOp == kMx ? 2 * S::kExtra : 1);
+      mbar_init(&raw[s], kOp == kMx ? 2 * 4 : 1);
       mbar_init(&rempty[s], S::kTeams * S::kTeam);
     }
     for (int a = 0; a < 2; ++a) {
@@ -745,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     // lane quarters, column r / 32, a word for 128 values; so each of the four warps, which may write one
     // quarter, needs every row's.  A thread brings 16 bytes of a row of the weight's 128 and of one or two of the
     // tile's, which are two stages', and hands them to all four warps through shared memory.
-    const int r = threadIdx.x - 32 * (2 + S::kEpiWarps), q = warp & 3;
+    const int team = (warp - 2 - S::kEpiWarps) / 4, r = (threadIdx.x - 32 * (2 + S::kEpiWarps)) & 127, q = warp & 3;
     int slot = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;   // (a warp that gives up goes on through the hand-overs, so that no other waits for it in vain)
@@ -769,11 +770,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     // what is on its way: kAheadMx times 16 bytes of each row, of the tiles to come too
     struct Pair {
       uint4 a, b, c;
-      int stages;
+      int before, stages;   // the other team's stages before it, and its own
     } ring[kAheadMx];
     int kit = 0, kits = 0;
     const uint8_t *pa = nullptr, *pb = nullptr, *pc = nullptr;
-    auto next_pair = [&](Pair& v) {
+    // the next two stages, or the last one, of the tiles in turn
+    auto advance = [&]() {
       if (kit >= kits) {
         kit = kits = 0;
         if (walk.next(j)) {
@@ -784,12 +786,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
           kits = j.kits;
         }
       }
-      v.stages = min(2, kits - kit);
-      if (v.stages == 0) return;
-      v.a = fetch(pa, kit * kMxBlocks);
-      v.b = fetch(pb, kit * kMxBlocks);
-      v.c = fetch(pc, kit * kMxBlocks);
+      const int stages = min(2, kits - kit);
       kit += 2;
+      return stages;
+    };
+    bool others = team == 1;   // whether the other team's come next
+    auto next_pair = [&](Pair& v) {
+      v.before = others ? advance() : 0;
+      others = true;
+      v.stages = advance();
+      if (v.stages <= 0) return;
+      const int at = (kit - 2) * kMxBlocks;
+      v.a = fetch(pa, at);
+      v.b = fetch(pb, at);
+      v.c = fetch(pc, at);
     };
 #pragma unroll
     for (int d = 0; d < kAheadMx; ++d) next_pair(ring[d]);
@@ -797,15 +807,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
 #pragma unroll
       for (int d = 0; d < kAheadMx; ++d) {
         Pair& v = ring[d];
-        if (v.stages == 0) more = false;
+        if (v.stages <= 0) more = false;
         if (!more) break;
-        uint4* hand = reinterpret_cast<uint4*>(scales) + turn * kMxHand;
+        uint4* hand = reinterpret_cast<uint4*>(scales) + (2 * team + turn) * kMxHand;
         turn ^= 1;
         hand[r] = v.a;
         hand[128 + r] = v.b;
         if (r < kMxRows - 128) hand[256 + r] = v.c;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory");
         const int stages = v.stages;
+        slot += v.before;
+        if (slot >= kStages) {
+          slot -= kStages;
+          phase ^= 1;
+        }
         next_pair(v);
         uint4 a[4], b[kMxRows / 32];
 #pragma unroll
