@@ -73,9 +73,11 @@ constexpr int kMxRows = 192;                 // 4-bit: rows of a tile (two accum
 constexpr int kMxWide = 128;                 // 4-bit: bytes of a row in a stage, 256 values
 constexpr int kMxBlocks = 8;                 // and their scales
 constexpr int kMxHand = 128 + kMxRows;       // rows whose scales a CTA needs: its rows of the weight, the tile's
-constexpr int kMxTeams = 2;                  // of four warps, which take turns at two stages each
-constexpr uint32_t kMxScales = kMxTeams * 2 * 16 * kMxHand;   // two hand-overs a team, of 16 bytes a row
-constexpr int kAheadMx = 2;                  // 4-bit: times 16 scales of a row on their way in a team
+constexpr int kMxTeams = 2;                  // of four warps, which take turns at the stages
+constexpr int kMxTurn = 4;                   // stages whose scales are brought at once (32 of a row: a sector)
+constexpr int kMxPieces = (2 * kMxHand + 128 * kMxTeams - 1) / (128 * kMxTeams);   // of 16 bytes, a thread's share of them
+constexpr uint32_t kMxScales = 2 * 32 * kMxHand;   // two hand-overs
+constexpr int kAheadMx = 2;                  // 4-bit: such times that are on their way
 constexpr int kMxCols = 24;                  // their TMEM columns: 2 words x (4 + 8)
 
 template <int kOp>
@@ -426,9 +428,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
-      mbar_init(&full[s], kOp == kI8 ? 2 * S::kTeam : 1);
+      mbar_init(&full[s], kOp == kI8 ? 2 * S::kTeam : (kOp == kMx ? 1 + 2 * 4 : 1));
       mbar_init(&empty[s], 1);
-      mbar_init(&raw[s], kOp == kMx ? 2 * 4 : 1);
+      mbar_init(&raw[s], 1);
       mbar_init(&rempty[s], S::kTeams * S::kTeam);
     }
     for (int a = 0; a < 2; ++a) {
@@ -562,14 +564,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && (kOp == kMx ? elect_one() : lane == 0)) {
       int slot = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, more = walk.next(j);
+      const uint64_t desc0 = sdesc_kmajor(smem_u32(stages));
       while (ok && more && !*abort_flag) {
         const int kits = j.kits;
         const int n = kOp == kDw ? kTile : (j.n + 31) / 32 * 32;
         const uint32_t idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(n >> 3) << 17);
+        const uint32_t idesc2 = idesc | idesc_scales(2);   // (4-bit: the second pair of a word's scales)
         more = walk.next(j);   // the next job, worked out while this one's products run
         if (kits == 0) continue;
         const uint32_t dt = tmem_base + (uint32_t)(acc * S::kRows);
@@ -579,12 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
         }
         tc_fence_after();
         for (int kit = 0; kit < kits; ++kit) {
-          if (!wait_nap<20, kOp == kI8>(&full[slot], phase, limit, abort_flag)) {
-            fail(kSiteGroupedMma);
-            ok = false;
-            break;
-          }
-          if (kOp == kMx && !wait_nap<20, true>(&raw[slot], phase, limit, abort_flag)) {
+          if (!wait_nap<20, kOp == kI8 || kOp == kMx>(&full[slot], phase, limit, abort_flag)) {
             fail(kSiteGroupedMma);
             ok = false;
             break;
@@ -593,10 +592,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
           const uint32_t sa = smem_u32(stages + (size_t)slot * kStage);
           if constexpr (kOp == kMx) {
             const uint32_t sf = tmem_base + 2 * S::kRows + slot * kMxCols;   // the stage's own columns of scales
+            const uint64_t da0 = desc0 + slot * (kStage / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_mxf4_pair(dt, sdesc_kmajor(sa + kk * 32), sdesc_kmajor(sa + kHalf + kk * 32),
-                             idesc | idesc_scales((kk & 1) * 2), sf + (kk >> 1) * 4, sf + 8 + (kk >> 1) * 8, (kit | kk) != 0);
+              umma_mxf4_pair(dt, da0 + kk * 2, da0 + kHalf / 16 + kk * 2, (kk & 1) != 0 ? idesc2 : idesc, sf + (kk >> 1) * 4,
+                             sf + 8 + (kk >> 1) * 8, (kit | kk) != 0);
           }
 #pragma unroll
           for (int kk = 0; kOp != kMx && kk < kBK / 16; ++kk) {
@@ -744,18 +744,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
     // Scales go to TMEM from registers, while the tensor cores work.  (Their copies from shared memory, tcgen05.cp, take
     // turns with the products: 56 cycles each, six a stage of 384.)  They lie there as row r in lane r % 32 of all four
     // lane quarters, column r / 32, a word for 128 values; so each of the four warps, which may write one
-    // quarter, needs every row's.  A thread brings 16 bytes of a row of the weight's 128 and of one or two of the
-    // tile's, which are two stages', and hands them to all four warps through shared memory.
-    const int team = (warp - 2 - S::kEpiWarps) / 4, r = (threadIdx.x - 32 * (2 + S::kEpiWarps)) & 127, q = warp & 3;
+    // quarter, needs every row's.  A turn is four stages: two lanes bring the 32 bytes of a row (a sector of L2: 16 at a
+    // time came twice, for 18% more traffic where the copies' traffic is the bound), and the warps hand them to each
+    // other through shared memory.
+    //
+    // Two teams of four warps take every other stage of a turn, so that one's way through the barriers runs beside the
+    // other's.  A barrier's phase must not pass a waiter by, so a team's wait for a stage's last use has to follow one
+    // that saw the use before that complete: a team's next stage is at most the third on (a turn of one stage
+    // is the first team's, and so is the stage before and the one after), and a stage's uses lie kStages apart.
+    static_assert(kMxTeams == 2 && kStages >= 3, "waits of a team");
+    const int r = threadIdx.x - 32 * (2 + S::kEpiWarps), team = r >> 7, q = warp & 3;
     int slot = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;   // (a warp that gives up goes on through the hand-overs, so that no other waits for it in vain)
     // 16 bytes of a row; 0 past its last scale, whatever is there
     auto fetch = [&](const uint8_t* from, int at) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (from == nullptr) return v;
-      v = __ldg(reinterpret_cast<const uint4*>(from + at));
       const int left = p.blocks - at;
+      if (from == nullptr || left <= 0) return v;
+      v = __ldg(reinterpret_cast<const uint4*>(from + at));
       if (left < 16) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -767,93 +774,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       }
       return v;
     };
-    // what is on its way: kAheadMx times 16 bytes of each row, of the tiles to come too
-    struct Pair {
-      uint4 a, b, c;
-      int before, stages;   // the other team's stages before it, and its own
+    struct Turn {
+      uint4 v[kMxPieces];
+      int stages;
     } ring[kAheadMx];
     int kit = 0, kits = 0;
-    const uint8_t *pa = nullptr, *pb = nullptr, *pc = nullptr;
-    // the next two stages, or the last one, of the tiles in turn
-    auto advance = [&]() {
+    const uint8_t* from[kMxPieces] = {};
+    auto next_turn = [&](Turn& t) {
       if (kit >= kits) {
         kit = kits = 0;
         if (walk.next(j)) {
-          const int f = j.f0 + kBM * rank + r;
-          pa = f < p.width ? p.wx + ((int64_t)j.g * p.width + f) * p.ldx : nullptr;
-          pb = r < j.n ? p.qx + ((int64_t)j.row + r) * p.ldx : nullptr;
-          pc = r + 128 < j.n ? p.qx + ((int64_t)j.row + r + 128) * p.ldx : nullptr;
+#pragma unroll
+          for (int i = 0; i < kMxPieces; ++i) {
+            const int row = 64 * kMxTeams * i + (r >> 1), f = j.f0 + kBM * rank + row, n = row - 128;   // (of the weight, of the tile)
+            if (row < 128) from[i] = f < p.width ? p.wx + ((int64_t)j.g * p.width + f) * p.ldx : nullptr;
+            else from[i] = n < j.n ? p.qx + ((int64_t)j.row + n) * p.ldx : nullptr;
+          }
           kits = j.kits;
         }
       }
-      const int stages = min(2, kits - kit);
-      kit += 2;
-      return stages;
-    };
-    bool others = team == 1;   // whether the other team's come next
-    auto next_pair = [&](Pair& v) {
-      v.before = others ? advance() : 0;
-      others = true;
-      v.stages = advance();
-      if (v.stages <= 0) return;
-      const int at = (kit - 2) * kMxBlocks;
-      v.a = fetch(pa, at);
-      v.b = fetch(pb, at);
-      v.c = fetch(pc, at);
+      t.stages = min(kMxTurn, kits - kit);
+      if (t.stages <= 0) return;
+#pragma unroll
+      for (int i = 0; i < kMxPieces; ++i) t.v[i] = fetch(from[i], kit * kMxBlocks + (r & 1) * 16);
+      kit += kMxTurn;
     };
 #pragma unroll
-    for (int d = 0; d < kAheadMx; ++d) next_pair(ring[d]);
+    for (int d = 0; d < kAheadMx; ++d) next_turn(ring[d]);
     for (bool more = true; more;) {
 #pragma unroll
       for (int d = 0; d < kAheadMx; ++d) {
-        Pair& v = ring[d];
-        if (v.stages <= 0) more = false;
+        Turn& t = ring[d];
+        if (t.stages <= 0) more = false;
         if (!more) break;
-        uint4* hand = reinterpret_cast<uint4*>(scales) + (2 * team + turn) * kMxHand;
+        uint4* hand = reinterpret_cast<uint4*>(scales) + turn * (2 * kMxHand);   // [half][row]
         turn ^= 1;
-        hand[r] = v.a;
-        hand[128 + r] = v.b;
-        if (r < kMxRows - 128) hand[256 + r] = v.c;
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory");
-        const int stages = v.stages;
-        slot += v.before;
-        if (slot >= kStages) {
-          slot -= kStages;
-          phase ^= 1;
+#pragma unroll
+        for (int i = 0; i < kMxPieces; ++i) {
+          const int row = 64 * kMxTeams * i + (r >> 1);
+          if (row < kMxHand) hand[(r & 1) * kMxHand + row] = t.v[i];
         }
-        next_pair(v);
-        uint4 a[4], b[kMxRows / 32];
+        asm volatile("bar.sync 1, %0;" ::"n"(128 * kMxTeams) : "memory");
+        const int stages = t.stages;
+        next_turn(t);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) a[c] = hand[32 * c + lane];
-#pragma unroll
-        for (int c = 0; c < kMxRows / 32; ++c) b[c] = hand[128 + 32 * c + lane];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kMxTurn; ++h) {
           if (h >= stages) break;
-          if (ok) {
-            ok = __all_sync(0xffffffffu, wait_nap<20>(&empty[slot], phase ^ 1, limit, abort_flag));
-            if (!ok && lane == 0) fail(kSiteGroupedStage);
-          }
-          if (ok) {
-            tc_fence_after();
-            const uint32_t sf = tmem_base + 2 * S::kRows + slot * kMxCols + ((uint32_t)(q * 32) << 16);
+          if (h % kMxTeams == team) {
+            // words of the stage: 2 (h & 1) and the next of half h / 2
+            const uint2* words = reinterpret_cast<const uint2*>(hand + (h >> 1) * kMxHand) + (h & 1);
             uint32_t wa[8], wb[16] = {};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              wa[c] = h ? a[c].z : a[c].x;
-              wa[4 + c] = h ? a[c].w : a[c].y;
+              const uint2 v = words[2 * (32 * c + lane)];
+              wa[c] = v.x;
+              wa[4 + c] = v.y;
             }
 #pragma unroll
             for (int c = 0; c < kMxRows / 32; ++c) {
-              wb[c] = h ? b[c].z : b[c].x;
-              wb[8 + c] = h ? b[c].w : b[c].y;
+              const uint2 v = words[2 * (128 + 32 * c + lane)];
+              wb[c] = v.x;
+              wb[8 + c] = v.y;
             }
-            tmem_st8(sf, wa);
-            tmem_st16(sf + 8, wb);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&raw[slot], 0));   // (the writes have completed)
+            if (ok) {
+              ok = __all_sync(0xffffffffu, wait_nap<20>(&empty[slot], phase ^ 1, limit, abort_flag));
+              if (!ok && lane == 0) fail(kSiteGroupedStage);
+            }
+            if (ok) {
+              tc_fence_after();
+              const uint32_t sf = tmem_base + 2 * S::kRows + slot * kMxCols + ((uint32_t)(q * 32) << 16);
+              tmem_st8(sf, wa);
+              tmem_st16(sf + 8, wb);
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&full[slot], 0));   // (the writes have completed)
+            }
           }
           if (++slot == kStages) {
             slot = 0;

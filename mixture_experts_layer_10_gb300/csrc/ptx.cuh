@@ -337,6 +337,14 @@ __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
+// One thread of a converged warp.  (A branch on it, unlike one on the lane's number, tells the compiler that a single
+// thread runs what follows.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
 // Arrive once on the mbarrier at shared::cluster address `cbar` (this CTA's or the peer's) when
 // every pair MMA this thread issued so far has completed.
 __device__ __forceinline__ void umma_commit_pair(uint32_t cbar) {
