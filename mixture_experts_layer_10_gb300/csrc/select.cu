@@ -2,8 +2,12 @@
 // key (ties to the lower expert), weights from the scores; and its gradient with the selection held.
 //
 // A token is held by G lanes (8, 16 or 32) of a warp, NV consecutive experts a lane, from one read of its
-// logits.  A round of the top-k takes the largest key over the lanes and retires it; the slots' weights are
-// then formed one slot a lane, from the logits themselves.
+// logits.  The top-k goes by candidates: of the largest keys of both halves of the lanes' experts, sorted over the lanes, the
+// k + 1st is a bound that at least k + 1 keys reach and few more do (11 of 256 for k = 8); these are put one after the other in
+// shared memory and ranked by counting.  Cross-lane work, which bounds the kernel (with the exponentials), so does not
+// grow with k: 65536 tokens of 256 experts, k = 8, in 8 groups took 91 us with k rounds of a maximum over the lanes.
+// The rounds remain for what the bound does not serve: k + 1 beyond the lanes, fewer experts left than that, more than
+// 32 candidates.  The slots' weights are then formed one slot a lane, from the logits themselves.
 //
 // Which expert wins must not hang on the rounding of a score, so the order is that of the keys in 64 bits:
 //   - without a bias and without sums of keys (groups scored by two) the order of the keys is the order of the
@@ -143,7 +147,6 @@ __device__ __forceinline__ float sigmoid32(float x) { return __fdiv_rn(1.f, 1.f 
 
 // ---- the same in 64 bits, for a token whose order is in doubt ---------------------------------------
 
-template <int G>
 __device__ __forceinline__ void top2_merge(double& a, double& b, double oa, double ob) {
   if (oa > a) {
     b = fmax(a, ob);
@@ -151,6 +154,27 @@ __device__ __forceinline__ void top2_merge(double& a, double& b, double oa, doub
   } else {
     b = fmax(b, oa);
   }
+}
+
+// An expert's key in 64 bits; top and sum as of softmax64.
+template <class T>
+__device__ __forceinline__ double key64(const SelParams& p, const T* row, int e, double top, double sum) {
+  const double x = fminf(widen1(row[e]), FLT_MAX);
+  const double s = p.sigmoid ? 1. / (1. + exp(-x)) : exp(x - top) / sum;
+  return p.bias != nullptr ? s + (double)p.bias[e] : s;
+}
+
+// The sum of a token's exponentials, over its lanes (1 with sigmoids).
+template <class T, int G, int NV>
+__device__ __forceinline__ double softmax64(const SelParams& p, const T* row, int e0, double top, uint32_t lanes) {
+  if (p.sigmoid) return 1.;
+  double sum = 0.;
+  for (int i = 0; i < NV && e0 + i < p.E; ++i) {
+    const float x = widen1(row[e0 + i]);
+    if (!masked(x)) sum += exp((double)fminf(x, FLT_MAX) - top);
+  }
+  for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
+  return sum;
 }
 
 // One token by its G lanes: slot j to lane j % G, element j / G.
@@ -191,10 +215,10 @@ __device__ __noinline__ void select64(const SelParams& p, int64_t t, int lane, i
       double a = -INFINITY, b = -INFINITY;
       for (int i = 0; i < NV; ++i) {
         const int e = e0 + i;
-        if (e >= g * p.per && e < (g + 1) * p.per && (out >> i & 1u) == 0) top2_merge<G>(a, b, key[i], -INFINITY);
+        if (e >= g * p.per && e < (g + 1) * p.per && (out >> i & 1u) == 0) top2_merge(a, b, key[i], -INFINITY);
       }
       for (int o = G / 2; o > 0; o >>= 1)
-        top2_merge<G>(a, b, __shfl_xor_sync(mask, a, o), __shfl_xor_sync(mask, b, o));
+        top2_merge(a, b, __shfl_xor_sync(mask, a, o), __shfl_xor_sync(mask, b, o));
       score[g] = p.sum == 2 && b > -INFINITY ? a + b : a;
     }
     for (int g = 0; g < p.n; ++g) {
@@ -235,13 +259,58 @@ __device__ __noinline__ void select64(const SelParams& p, int64_t t, int lane, i
 
 // ---- selection -----------------------------------------------------------------------------------
 
+constexpr int kMaxCand = 32;       // candidates of a token
+
+// A token's share of shared memory.
+struct Cand {
+  float key[kMaxCand];
+  int e[kMaxCand];
+  double wide[kMaxCand];
+  float top[kMaxCand + 1];         // by rank
+  int who[kMaxCand];
+};
+
+// Descending over the token's lanes.
+template <int G>
+__device__ __forceinline__ float sort_lanes(float v, int li) {
+#pragma unroll
+  for (int size = 2; size <= G; size *= 2)
+#pragma unroll
+    for (int o = size / 2; o > 0; o /= 2) {
+      const float w = __shfl_xor_sync(0xffffffffu, v, o);
+      v = ((li & o) == 0) == ((li & size) == 0) ? fmaxf(v, w) : fminf(v, w);
+    }
+  return v;
+}
+
+// The largest G of two values a lane, descending over the lanes.
+template <int G>
+__device__ __forceinline__ float sort_pairs(float a, float b, int li) {
+  a = sort_lanes<G>(a, li);
+  b = sort_lanes<G>(b, li);
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, b, G - 1));   // (rises, then falls)
+#pragma unroll
+  for (int o = G / 2; o > 0; o /= 2) {
+    const float w = __shfl_xor_sync(0xffffffffu, a, o);
+    a = (li & o) == 0 ? fmaxf(a, w) : fminf(a, w);
+  }
+  return a;
+}
+
 // kKeys: keys are scores (with a bias, or summed), else logits.
 template <class T, int G, int NV, bool kKeys>
-__global__ void __launch_bounds__(32 * kWarps) select_kernel(const __grid_constant__ SelParams p) {
+__global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(const __grid_constant__ SelParams p) {
   constexpr int kTok = 32 / G;       // tokens of a warp
-  constexpr int kSlots = 32 / G;     // slots of a lane
-  __shared__ uint32_t keys[kWarps][32 * NV];
-  __shared__ uint32_t scores[kWarps][kTok][kMaxExpertGroups];
+  constexpr int kSlots = 32 / G;     // slots of a lane, and candidates
+  constexpr uint32_t kAll = NV == 32 ? 0xffffffffu : (1u << (NV & 31)) - 1u;
+  union Shared {
+    struct {
+      float keys[32 * NV];
+      float scores[kTok][kMaxExpertGroups];
+    } g;
+    Cand c[kTok];
+  };
+  __shared__ Shared shared[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & (G - 1), e0 = li * NV;
   constexpr uint32_t mask = 0xffffffffu;       // (all tokens of a warp take the same way)
   const uint32_t mine = group_mask<G>(lane);
@@ -250,164 +319,274 @@ __global__ void __launch_bounds__(32 * kWarps) select_kernel(const __grid_consta
   const T* row = static_cast<const T*>(p.logits) + t * p.E;
   after_previous_kernel();
 
-  float x[NV];
-  load_row<T, NV>(row, e0, p.E, x);
+  float key[NV];   // the logits, then the keys: -inf for masked experts
+  load_row<T, NV>(row, e0, p.E, key);
   const bool softmax_all = !p.sigmoid && (kKeys || !p.renorm);
   float m = -FLT_MAX, z = 0.f, rz = 0.f;
   bool broken = false;   // a NaN or +inf: the selection goes by the rest, or as if it were the largest number
-  uint32_t u[NV];
   if (softmax_all) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) m = fmaxf(m, x[i]);
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
     m = fminf(group_fmax<G>(m, mask), FLT_MAX);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) z += __expf(x[i] - m);
+    for (int i = 0; i < NV; ++i) z += __expf(key[i] - m);
     z = group_sum<G>(z, mask);
     broken = !(z <= FLT_MAX);
     if (__any_sync(mask, broken)) {
       z = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) z += masked(x[i]) ? 0.f : __expf(fminf(x[i], FLT_MAX) - m);
+      for (int i = 0; i < NV; ++i) z += masked(key[i]) ? 0.f : __expf(fminf(key[i], FLT_MAX) - m);
       z = group_sum<G>(z, mask);
     }
     rz = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
   }
+  uint32_t allowed = e0 >= p.E ? 0u : (p.E - e0 >= NV ? kAll : (1u << (p.E - e0)) - 1u);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float key = x[i];
-    bool no = masked(x[i]);
+    const float x = key[i];
     if (kKeys) {
-      key = p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x[i])) : __expf(fminf(x[i], FLT_MAX) - m) * rz;
-      if (p.bias != nullptr && e0 + i < p.E) key += __ldg(p.bias + e0 + i);
-      no = no || masked(key);
+      key[i] = p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x)) : __expf(fminf(x, FLT_MAX) - m) * rz;
+      if (p.bias != nullptr && e0 + i < p.E) key[i] += __ldg(p.bias + e0 + i);
     }
-    u[i] = e0 + i >= p.E ? kTaken : (no ? kMasked : order_of(key));
+    if (masked(x) || (kKeys && masked(key[i]))) key[i] = -INFINITY;
   }
 
-  bool doubt = false;   // the same in all lanes of a token
+  bool border = false, doubt = false;   // the same in all lanes of a token
   const float tol = p.sigmoid ? 0x1p-19f : 0x1p-18f;
+  auto near_by = [](float hi, float lo, float by) { return hi - lo <= by * fmaxf(1.f, fabsf(hi)); };   // (of -inf: no)
   if (p.top < p.n) {
     // scores of the groups: of masked experts nothing is added, and a group of none else comes last
     const int lanes = p.per / NV;   // of a group
     if (p.per % NV == 0 && (lanes & (lanes - 1)) == 0) {
-      uint32_t a = kTaken, b = kTaken;   // the largest two keys of the lane, then of the group
+      float a = -INFINITY, b = -INFINITY;   // the largest two keys of the lane, then of the group
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        b = max(b, min(a, u[i]));
-        a = max(a, u[i]);
+        b = fmaxf(b, fminf(a, key[i]));
+        a = fmaxf(a, key[i]);
       }
       for (int o = lanes / 2; o > 0; o >>= 1) {
-        const uint32_t oa = __shfl_xor_sync(mask, a, o), ob = __shfl_xor_sync(mask, b, o);
-        b = max(max(b, ob), min(a, oa));
-        a = max(a, oa);
+        const float oa = __shfl_xor_sync(mask, a, o), ob = __shfl_xor_sync(mask, b, o);
+        b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+        a = fmaxf(a, oa);
       }
-      float f = value_of(a);
-      if (p.sum == 2 && b > kMasked) f += value_of(b);
-      const uint32_t s = a > kMasked ? order_of(f) : kMasked;
+      const float s = p.sum == 2 && b > -INFINITY ? a + b : a;
       const int g = e0 / p.per;   // (of a lane past the last expert: no group's)
       int above = 0;
       for (int h = 0; h < p.n; ++h) {
-        const uint32_t o = __shfl_sync(mask, s, h * lanes, G);
-        above += o > s || (o == s && h < g);
+        const float o = __shfl_sync(mask, s, h * lanes, G);
+        above += h < g ? o >= s : o > s;
       }
-      const bool keep = above < p.top;
       if (kKeys) {
         const uint32_t last = __ballot_sync(mask, e0 < p.E && above == p.top - 1) & mine;
         const uint32_t next = __ballot_sync(mask, e0 < p.E && above == p.top) & mine;
-        const uint32_t sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
-        const float fl = value_of(sl);
-        doubt = sn > kMasked && fl - value_of(sn) <= 2.f * tol * fmaxf(1.f, fabsf(fl));
-      }
+        const float sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
+        // a border in doubt: the scores again, of the keys that may be among a group's largest, in 64 bits
+        if (near_by(sl, sn, 2.f * tol)) {
+          const double total = softmax64<T, G, NV>(p, row, e0, m, mine);
+          const float least = p.sum == 2 ? b : a;
+          const float from = least - 2.f * tol * fmaxf(1.f, fabsf(least));
+          uint32_t need = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (!keep) u[i] = kTaken;
+          for (int i = 0; i < NV; ++i)
+            if (key[i] > -INFINITY && (least == -INFINITY || key[i] >= from)) need |= 1u << i;
+          double da = -INFINITY, db = -INFINITY;
+          for (; need != 0; need &= need - 1)
+            top2_merge(da, db, key64(p, row, e0 + __ffs(need) - 1, m, total), -INFINITY);
+          __syncwarp(mine);
+          for (int o = lanes / 2; o > 0; o >>= 1)
+            top2_merge(da, db, __shfl_xor_sync(mine, da, o), __shfl_xor_sync(mine, db, o));
+          const double ds = p.sum == 2 && db > -INFINITY ? da + db : da;
+          above = 0;
+          for (int h = 0; h < p.n; ++h) {
+            const double o = __shfl_sync(mine, ds, h * lanes, G);
+            above += h < g ? o >= ds : o > ds;
+          }
+        }
+        __syncwarp();
+      }
+      if (above >= p.top) allowed = 0u;
     } else {
       // groups that do not fall on lanes: through shared memory, a group a lane
-      uint32_t* kr = keys[warp] + (lane / G) * (G * NV);
-      uint32_t* sr = scores[warp][lane / G];
+      float* kr = shared[warp].g.keys + (lane / G) * (G * NV);
+      float* sr = shared[warp].g.scores[lane / G];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) kr[e0 + i] = u[i];
+      for (int i = 0; i < NV; ++i) kr[e0 + i] = key[i];
       __syncwarp();
       for (int g = li; g < p.n; g += G) {
-        uint32_t a = kTaken, b = kTaken;
+        float a = -INFINITY, b = -INFINITY;
         for (int e = g * p.per; e < (g + 1) * p.per; ++e) {
-          const uint32_t v = kr[e];
-          b = max(b, min(a, v));
-          a = max(a, v);
+          const float v = kr[e];
+          b = fmaxf(b, fminf(a, v));
+          a = fmaxf(a, v);
         }
-        float f = value_of(a);
-        if (p.sum == 2 && b > kMasked) f += value_of(b);
-        sr[g] = a > kMasked ? order_of(f) : kMasked;
+        sr[g] = p.sum == 2 && b > -INFINITY ? a + b : a;
       }
       __syncwarp();
-      uint32_t lo = 0xffffffffu, hi = 0;   // the lowest score kept, the highest dropped
+      float lo = INFINITY, hi = -INFINITY;   // the lowest score kept, the highest dropped
+      uint32_t drop[2] = {0u, 0u};
       for (int g = li; g < p.n; g += G) {
-        const uint32_t s = sr[g];
+        const float s = sr[g];
         int above = 0;
-        for (int h = 0; h < p.n; ++h) {
-          const uint32_t o = sr[h];
-          above += o > s || (o == s && h < g);
-        }
+        for (int h = 0; h < p.n; ++h) above += h < g ? sr[h] >= s : sr[h] > s;
         if (above < p.top) {
-          lo = min(lo, s);
+          lo = fminf(lo, s);
         } else {
-          hi = max(hi, s);
-          for (int e = g * p.per; e < (g + 1) * p.per; ++e) kr[e] = kTaken;
+          hi = fmaxf(hi, s);
+          drop[g >> 5] |= 1u << (g & 31);
         }
       }
-      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < NV; ++i) u[i] = kr[e0 + i];
-      if (kKeys) {
-        lo = ~group_max<G>(~lo, mask);
-        hi = group_max<G>(hi, mask);
-        const float fl = value_of(lo);
-        doubt = hi > kMasked && fl - value_of(hi) <= 2.f * tol * fmaxf(1.f, fabsf(fl));
+      for (int o = G / 2; o > 0; o >>= 1) {
+        drop[0] |= __shfl_xor_sync(mask, drop[0], o);
+        drop[1] |= __shfl_xor_sync(mask, drop[1], o);
       }
+      if (kKeys) border = near_by(-group_fmax<G>(-lo, mask), group_fmax<G>(hi, mask), 2.f * tol);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int g = min((e0 + i) / p.per, p.n - 1);
+        if ((drop[g >> 5] >> (g & 31) & 1u) != 0) allowed &= ~(1u << i);
+      }
+      __syncwarp();   // (the candidates come where the keys were)
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)   // (masked ones of the groups that stay: only the rounds below choose them)
+      if ((allowed >> i & 1u) == 0) key[i] = -INFINITY;
   }
 
   int sidx[kSlots];
-  uint32_t before = kTaken;   // the key of the slot before
 #pragma unroll
-  for (int q = 0; q < kSlots; ++q) {
-    sidx[q] = 0;
-    for (int rr = 0; rr < G; ++rr) {
-      const int r = q * G + rr;
-      if (r > p.k || (r == p.k && !kKeys)) break;   // (one more than the slots, for the border)
-      uint32_t best = u[0];
+  for (int q = 0; q < kSlots; ++q) sidx[q] = 0;
+  // The bound: the k + 1st of the largest keys of half lanes, less what keys may be off
+  bool rounds = p.k >= G;
+  int count = 0;   // candidates of the token
+  Cand& cand = shared[warp].c[lane / G];
+  if (!rounds) {
+    float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 1; i < NV; ++i) best = max(best, u[i]);
-      const uint32_t v = group_max<G>(best, mask);
-      if (kKeys) {
-        if (r > 0 && v > kMasked) {
-          const float fb = value_of(before);
-          doubt |= fb - value_of(v) <= tol * fmaxf(1.f, fabsf(fb));
-        }
-        before = v;
-        if (r == p.k) break;
-      }
-      const int owner = __ffs(__ballot_sync(mask, best == v) & mine) - 1;
-      int il = 0;
+    for (int i = 0; i < NV; ++i) best[2 * i / NV] = fmaxf(best[2 * i / NV], key[i]);
+    const float sorted = NV > 1 ? sort_pairs<G>(best[0], best[1], li) : sort_lanes<G>(best[0], li);
+    float bound = __shfl_sync(mask, sorted, p.k, G);
+    rounds = !(bound > -INFINITY);
+    if (kKeys) bound -= 2.f * tol * fmaxf(1.f, fabsf(bound));
+    int upto = 0;
 #pragma unroll
-      for (int i = NV - 1; i >= 0; --i)
-        if (u[i] == v) il = i;
+    for (int i = 0; i < NV; ++i) upto += key[i] >= bound;
+    const int own = upto;
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) {
+      const int v = __shfl_up_sync(mask, upto, o, G);
+      if (li >= o) upto += v;
+    }
+    count = __shfl_sync(mask, upto, G - 1, G);
+    rounds = __any_sync(mask, rounds || count > kMaxCand);
+    if (!rounds) {
+      int to = upto - own;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (lane == owner && i == il) u[i] = kTaken;
-      const int e = __shfl_sync(mask, e0 + il, owner);
-      if (rr == li) sidx[q] = e;
+        if (key[i] >= bound) {
+          cand.key[to] = key[i];
+          cand.e[to++] = e0 + i;
+        }
+      __syncwarp();
+      // ranks: candidates lie in the order of the experts, so that among equal ones the earlier comes first
+      float own_key[kSlots];
+      int rank[kSlots];
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        own_key[q] = q * G + li < count ? cand.key[q * G + li] : -INFINITY;
+        rank[q] = 0;
+      }
+      const int most = G == 32 ? count : __reduce_max_sync(mask, count);
+      for (int c = 0; c < most; ++c) {
+        const float v = c < count ? cand.key[c] : -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) rank[q] += c < q * G + li ? v >= own_key[q] : v > own_key[q];
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (q * G + li < count) {
+          cand.top[rank[q]] = own_key[q];
+          cand.who[rank[q]] = cand.e[q * G + li];
+        }
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        const int j = q * G + li;
+        if (j >= p.k) continue;
+        sidx[q] = cand.who[j];
+        // (there are more than k candidates)
+        if (kKeys) doubt |= near_by(cand.top[j], cand.top[j + 1], tol);
+      }
+      if (kKeys) doubt = (__ballot_sync(mask, doubt) & mine) != 0;
     }
   }
-  if (kKeys && p.k == kMaxSlots) {   // the border's key of a full set of slots
-    uint32_t best = u[0];
+  if (rounds) {
+    uint32_t u[NV];
 #pragma unroll
-    for (int i = 1; i < NV; ++i) best = max(best, u[i]);
-    const uint32_t v = group_max<G>(best, mask);
-    const float fb = value_of(before);
-    doubt |= v > kMasked && fb - value_of(v) <= tol * fmaxf(1.f, fabsf(fb));
+    for (int i = 0; i < NV; ++i)
+      u[i] = (allowed >> i & 1u) == 0 ? kTaken : (key[i] > -INFINITY ? order_of(key[i]) : kMasked);
+    uint32_t before = kTaken;   // the key of the slot before
+    doubt = false;
+#pragma unroll
+    for (int q = 0; q <= kSlots; ++q) {
+      for (int rr = 0; rr < G; ++rr) {
+        const int r = q * G + rr;
+        if (r > p.k || (r == p.k && !kKeys)) break;   // (one more than the slots, for the border)
+        uint32_t best = u[0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i) best = max(best, u[i]);
+        const uint32_t v = group_max<G>(best, mask);
+        if (kKeys) {
+          if (r > 0 && v > kMasked) doubt |= near_by(value_of(before), value_of(v), tol);
+          before = v;
+          if (r == p.k) break;
+        }
+        const int owner = __ffs(__ballot_sync(mask, best == v) & mine) - 1;
+        int il = 0;
+#pragma unroll
+        for (int i = NV - 1; i >= 0; --i)
+          if (u[i] == v) il = i;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (lane == owner && i == il) u[i] = kTaken;
+        const int e = __shfl_sync(mask, e0 + il, owner);
+        if (q < kSlots && rr == li) sidx[q] = e;
+      }
+    }
   }
-  if (kKeys && doubt) select64<T, G, NV>(p, t, lane, sidx);
+  if (kKeys) {
+    if (border || (doubt && rounds)) {
+      select64<T, G, NV>(p, t, lane, sidx);
+    } else if (doubt) {
+      // every candidate's key in 64 bits: whoever may be among the k is one
+      const double total = softmax64<T, G, NV>(p, row, e0, m, mine);
+      double wide[kSlots];
+      int rank[kSlots];
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        const int c = q * G + li;
+        rank[q] = kMaxCand;
+        wide[q] = -INFINITY;
+        if (c >= count) continue;
+        wide[q] = key64(p, row, cand.e[c], m, total);
+        cand.wide[c] = wide[q];
+        rank[q] = 0;
+      }
+      __syncwarp(mine);
+      for (int c = 0; c < count; ++c) {
+        const double v = cand.wide[c];
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) rank[q] += c < q * G + li ? v >= wide[q] : v > wide[q];
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (rank[q] < p.k) cand.who[rank[q]] = cand.e[q * G + li];
+      __syncwarp(mine);
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (q * G + li < p.k) sidx[q] = cand.who[q * G + li];
+    }
+  }
   __syncwarp();
 
   // weights, a slot a lane
@@ -451,10 +630,13 @@ __global__ void __launch_bounds__(32 * kWarps) select_kernel(const __grid_consta
 
 // ---- gradient ------------------------------------------------------------------------------------
 
-// d_j, a slot a lane, then each expert's sum over the slots that chose it, in slot order, by the lane that holds it:
+// d_j, a slot a lane:
 //   renormalised      d_j = w_j (c_j - sum_m c_m h_m), sigmoid: times 1 - s_j
-//   not renormalised  d_j = scale c_j s_j (1 - s_j); softmax: d_j = scale c_j p_j, and less
-//                     p_e scale sum_j c_j p_j for every expert
+//   not renormalised  d_j = scale c_j s_j (1 - s_j); softmax: d_j = scale p_j (c_j - sum_m c_m p_m), and
+//                     -scale p_e sum_m c_m p_m for the experts of no slot
+// The row is first written as of a token without slots, in whole vectors, and then at the slots' experts, by the same
+// warp: no lane looks through its experts for every slot (46 us at 65536 tokens of 256 experts).  An expert in several
+// slots gets the sum of their terms, in slot order, from the first of them.
 template <class T, int G, int NV>
 __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_constant__ SelParams p) {
   constexpr int kTok = 32 / G, kSlots = 32 / G;
@@ -463,6 +645,7 @@ __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_co
   const int64_t at = ((int64_t)blockIdx.x * kWarps + warp) * kTok + lane / G;
   const int64_t t = min(at, p.T - 1);
   const T* row = static_cast<const T*>(p.logits) + t * p.E;
+  T* out = static_cast<T*>(p.dl) + t * p.E;
   after_previous_kernel();
 
   int e[kSlots];
@@ -521,24 +704,40 @@ __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_co
   for (int q = 0; q < kSlots; ++q) dot += c[q] * h[q];
   if (p.renorm || dense) dot = group_sum<G>(dot, mask);
   float d[kSlots];
+  bool first[kSlots];
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
     d[q] = h[q] == 0.f ? 0.f : p.scale * h[q] * (p.renorm ? c[q] - dot : c[q]);
     if (p.sigmoid) d[q] *= sigmoid32(-xs[q]);   // (of a slot without an expert 1)
+    first[q] = e[q] >= 0;
+  }
+  const uint32_t same = __match_any_sync(mask, e[0] >= 0 ? e[0] | (lane / G) << 16 : -1 - lane);
+  if (p.k > G || __any_sync(mask, (same & (same - 1)) != 0)) {
+    float total[kSlots] = {};
+#pragma unroll
+    for (int r = 0; r < kSlots; ++r)
+      for (int rr = 0; rr < G; ++rr) {
+        if (r * G + rr >= p.k) break;
+        const int ej = __shfl_sync(mask, e[r], rr, G);
+        const float dj = __shfl_sync(mask, d[r], rr, G);
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q)
+          if (ej == e[q]) {
+            total[q] += dj;
+            if (r * G + rr < q * G + li) first[q] = false;
+          }
+      }
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) d[q] = total[q];
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i] = dense ? -(v[i] * rz) * (p.scale * dot) : 0.f;
+  if (at < p.T) store_row<T, NV>(out, e0, p.E, v);
+  __syncwarp();
+  if (at >= p.T) return;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q)
-    for (int rr = 0; rr < G; ++rr) {
-      if (q * G + rr >= p.k) break;
-      const int at_e = __shfl_sync(mask, e[q], rr, G) - e0;
-      const float add = __shfl_sync(mask, d[q], rr, G);
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (at_e == i) v[i] += add;
-    }
-  if (at < p.T) store_row<T, NV>(static_cast<T*>(p.dl) + t * p.E, e0, p.E, v);
+    if (first[q]) out[e[q]] = narrow1<T>(dense ? d[q] - h[q] * (p.scale * dot) : d[q]);
 }
 
 // ---- host side -----------------------------------------------------------------------------------
@@ -566,7 +765,7 @@ cudaError_t by_experts(int E, F f) {
   if (E <= 32) return f.template call<T, 8, 4>();
   if (E <= 64) return f.template call<T, 16, 4>();
   if (E <= 128) return f.template call<T, 16, 8>();
-  if (E <= 256) return f.template call<T, 32, 8>();
+  if (E <= 256) return f.template call<T, 16, 16>();
   if (E <= 512) return f.template call<T, 32, 16>();
   return f.template call<T, 32, 32>();
 }
