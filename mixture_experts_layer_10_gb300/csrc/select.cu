@@ -122,6 +122,25 @@ __device__ __forceinline__ void load_row(const T* row, int e0, int E, float (&x)
   }
 }
 
+template <int NV>
+__device__ __forceinline__ void load_bias(const float* bias, int e0, int E, float (&b)[NV]) {
+  if (NV % 4 == 0 && E % 4 == 0 && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 4)
+      if (e0 + i < E) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(bias + e0 + i));
+        b[i] = v.x;
+        b[i + 1] = v.y;
+        b[i + 2] = v.z;
+        b[i + 3] = v.w;
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (e0 + i < E) b[i] = __ldg(bias + e0 + i);
+  }
+}
+
 template <class T, int NV>
 __device__ __forceinline__ void store_row(T* row, int e0, int E, const float (&x)[NV]) {
   constexpr int V = vec_of<T, NV>();
@@ -140,8 +159,31 @@ __device__ __forceinline__ void store_row(T* row, int e0, int E, const float (&x
   }
 }
 
+// A warp: n zeros from `at` on, rows of E of them.
+template <class T>
+__device__ __forceinline__ void fill_zero(T* at, int n, int E, int lane) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (E % V == 0) {
+    for (int i = lane * V; i < n; i += 32 * V) *reinterpret_cast<uint4*>(at + i) = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    for (int i = lane; i < n; i += 32) at[i] = narrow1<T>(0.f);
+  }
+}
+
 // (a logit that is -inf masks its expert; NaN too, as far as the selection goes)
 __device__ __forceinline__ bool masked(float x) { return !(x > -INFINITY); }
+
+// e^v for keys: a result below 2^-126 is 0.
+__device__ __forceinline__ float exp_fast(float v) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * 1.4426950408889634f));
+  return e;
+}
+__device__ __forceinline__ float rcp_fast(float v) {   // of 1 and more
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 __device__ __forceinline__ float sigmoid32(float x) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
 
@@ -158,7 +200,7 @@ __device__ __forceinline__ void top2_merge(double& a, double& b, double oa, doub
 
 // An expert's key in 64 bits; top and sum as of softmax64.
 template <class T>
-__device__ __forceinline__ double key64(const SelParams& p, const T* row, int e, double top, double sum) {
+__device__ __noinline__ double key64(const SelParams& p, const T* row, int e, double top, double sum) {
   const double x = fminf(widen1(row[e]), FLT_MAX);
   const double s = p.sigmoid ? 1. / (1. + exp(-x)) : exp(x - top) / sum;
   return p.bias != nullptr ? s + (double)p.bias[e] : s;
@@ -166,7 +208,7 @@ __device__ __forceinline__ double key64(const SelParams& p, const T* row, int e,
 
 // The sum of a token's exponentials, over its lanes (1 with sigmoids).
 template <class T, int G, int NV>
-__device__ __forceinline__ double softmax64(const SelParams& p, const T* row, int e0, double top, uint32_t lanes) {
+__device__ __noinline__ double softmax64(const SelParams& p, const T* row, int e0, double top, uint32_t lanes) {
   if (p.sigmoid) return 1.;
   double sum = 0.;
   for (int i = 0; i < NV && e0 + i < p.E; ++i) {
@@ -263,7 +305,7 @@ constexpr int kMaxCand = 32;       // candidates of a token
 
 // A token's share of shared memory.
 struct Cand {
-  float key[kMaxCand];
+  alignas(16) float key[kMaxCand];   // -inf past the last
   int e[kMaxCand];
   double wide[kMaxCand];
   float top[kMaxCand + 1];         // by rank
@@ -329,26 +371,33 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
     for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
     m = fminf(group_fmax<G>(m, mask), FLT_MAX);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) z += __expf(key[i] - m);
+    for (int i = 0; i < NV; ++i) z += exp_fast(key[i] - m);
     z = group_sum<G>(z, mask);
     broken = !(z <= FLT_MAX);
     if (__any_sync(mask, broken)) {
       z = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) z += masked(key[i]) ? 0.f : __expf(fminf(key[i], FLT_MAX) - m);
+      for (int i = 0; i < NV; ++i) z += masked(key[i]) ? 0.f : exp_fast(fminf(key[i], FLT_MAX) - m);
       z = group_sum<G>(z, mask);
     }
     rz = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
   }
   uint32_t allowed = e0 >= p.E ? 0u : (p.E - e0 >= NV ? kAll : (1u << (p.E - e0)) - 1u);
+  if (kKeys) {
+    float bias[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const float x = key[i];
-    if (kKeys) {
-      key[i] = p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x)) : __expf(fminf(x, FLT_MAX) - m) * rz;
-      if (p.bias != nullptr && e0 + i < p.E) key[i] += __ldg(p.bias + e0 + i);
+    for (int i = 0; i < NV; ++i) bias[i] = 0.f;
+    if (p.bias != nullptr) load_bias<NV>(p.bias, e0, p.E, bias);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float x = key[i];
+      const float k = bias[i] + (p.sigmoid ? rcp_fast(1.f + exp_fast(-x)) : exp_fast(fminf(x, FLT_MAX) - m) * rz);
+      key[i] = masked(x) || masked(k) ? -INFINITY : k;
     }
-    if (masked(x) || (kKeys && masked(key[i]))) key[i] = -INFINITY;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (masked(key[i])) key[i] = -INFINITY;   // (NaN)
   }
 
   bool border = false, doubt = false;   // the same in all lanes of a token
@@ -480,6 +529,9 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
     count = __shfl_sync(mask, upto, G - 1, G);
     rounds = __any_sync(mask, rounds || count > kMaxCand);
     if (!rounds) {
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (q * G + li >= count) cand.key[q * G + li] = -INFINITY;
       int to = upto - own;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -493,14 +545,19 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
       int rank[kSlots];
 #pragma unroll
       for (int q = 0; q < kSlots; ++q) {
-        own_key[q] = q * G + li < count ? cand.key[q * G + li] : -INFINITY;
+        own_key[q] = cand.key[q * G + li];
         rank[q] = 0;
       }
       const int most = G == 32 ? count : __reduce_max_sync(mask, count);
-      for (int c = 0; c < most; ++c) {
-        const float v = c < count ? cand.key[c] : -INFINITY;
+      for (int c = 0; c < most; c += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(cand.key + c);
 #pragma unroll
-        for (int q = 0; q < kSlots; ++q) rank[q] += c < q * G + li ? v >= own_key[q] : v > own_key[q];
+        for (int q = 0; q < kSlots; ++q) {
+          if (q > 0 && most <= q * G) break;
+          const int at = q * G + li - c;
+          rank[q] += (at > 0 ? v.x >= own_key[q] : v.x > own_key[q]) + (at > 1 ? v.y >= own_key[q] : v.y > own_key[q]) +
+                     (at > 2 ? v.z >= own_key[q] : v.z > own_key[q]) + (at > 3 ? v.w >= own_key[q] : v.w > own_key[q]);
+        }
       }
 #pragma unroll
       for (int q = 0; q < kSlots; ++q)
@@ -602,6 +659,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
   if (p.renorm) M = group_fmax<G>(M, mask);
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
+    s[q] = 0.f;
+    if (q * G >= p.k) continue;
     const bool slot = q * G + li < p.k;
     if (!p.renorm) {
       s[q] = p.sigmoid ? sigmoid32(xs[q]) : expf(xs[q] - m) * rz;
@@ -616,7 +675,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
   if (p.renorm) {
     sum = group_sum<G>(sum, mask);
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) s[q] = sum == 0.f ? 0.f : __fdiv_rn(s[q], sum);
+    for (int q = 0; q < kSlots; ++q)
+      if (q * G < p.k) s[q] = sum == 0.f ? 0.f : __fdiv_rn(s[q], sum);
   }
   if (at >= p.T) return;
 #pragma unroll
@@ -638,7 +698,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 // warp: no lane looks through its experts for every slot (46 us at 65536 tokens of 256 experts).  An expert in several
 // slots gets the sum of their terms, in slot order, from the first of them.
 template <class T, int G, int NV>
-__global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_constant__ SelParams p) {
+__global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_kernel(const __grid_constant__ SelParams p) {
   constexpr int kTok = 32 / G, kSlots = 32 / G;
   constexpr uint32_t mask = 0xffffffffu;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & (G - 1), e0 = li * NV;
@@ -646,6 +706,7 @@ __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_co
   const int64_t t = min(at, p.T - 1);
   const T* row = static_cast<const T*>(p.logits) + t * p.E;
   T* out = static_cast<T*>(p.dl) + t * p.E;
+  __shared__ uint8_t marks[kWarps][32 * NV];
   after_previous_kernel();
 
   int e[kSlots];
@@ -662,8 +723,14 @@ __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_co
     }
     if (e[q] < 0 || e[q] >= p.E) e[q] = -1;   // (no expert: a slot without weight)
   }
-  float v[NV];
   const bool dense = !p.sigmoid && !p.renorm;
+  float v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = 0.f;
+  if (!dense) {   // zeros, of all the warp's tokens, which lie on end
+    const int64_t first = at - lane / G;
+    if (first < p.T) fill_zero(static_cast<T*>(p.dl) + first * p.E, (int)min((int64_t)kTok, p.T - first) * p.E, p.E, lane);
+  }
   float m = -FLT_MAX, rz = 0.f;
   if (dense) {
     load_row<T, NV>(row, e0, p.E, v);
@@ -689,6 +756,8 @@ __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_co
   float h[kSlots], sum = 0.f, dot = 0.f;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
+    h[q] = 0.f;
+    if (q * G >= p.k) continue;
     if (!p.renorm) h[q] = p.sigmoid ? sigmoid32(xs[q]) : __expf(xs[q] - m) * rz;
     else if (p.sigmoid && M >= -40.f) h[q] = sigmoid32(xs[q]);
     else h[q] = M == -INFINITY ? 0.f : expf(xs[q] - M);
@@ -698,7 +767,8 @@ __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_co
   if (p.renorm) {
     sum = group_sum<G>(sum, mask);
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) h[q] = sum == 0.f ? 0.f : __fdiv_rn(h[q], sum);
+    for (int q = 0; q < kSlots; ++q)
+      if (q * G < p.k) h[q] = sum == 0.f ? 0.f : __fdiv_rn(h[q], sum);
   }
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) dot += c[q] * h[q];
@@ -707,12 +777,23 @@ __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_co
   bool first[kSlots];
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
+    first[q] = e[q] >= 0;
+    d[q] = 0.f;
+    if (q * G >= p.k) continue;
     d[q] = h[q] == 0.f ? 0.f : p.scale * h[q] * (p.renorm ? c[q] - dot : c[q]);
     if (p.sigmoid) d[q] *= sigmoid32(-xs[q]);   // (of a slot without an expert 1)
-    first[q] = e[q] >= 0;
   }
-  const uint32_t same = __match_any_sync(mask, e[0] >= 0 ? e[0] | (lane / G) << 16 : -1 - lane);
-  if (p.k > G || __any_sync(mask, (same & (same - 1)) != 0)) {
+  // whether an expert comes twice: a slot that does not find its own mark on its expert
+  bool twice = false;
+  uint8_t* tags = marks[warp] + (lane / G) * (G * NV);
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q)
+    if (e[q] >= 0) tags[e[q]] = (uint8_t)(q * G + li);
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q)
+    if (e[q] >= 0) twice |= tags[e[q]] != (uint8_t)(q * G + li);
+  if (__any_sync(mask, twice)) {
     float total[kSlots] = {};
 #pragma unroll
     for (int r = 0; r < kSlots; ++r)
@@ -730,9 +811,11 @@ __global__ void __launch_bounds__(32 * kWarps) select_bwd_kernel(const __grid_co
 #pragma unroll
     for (int q = 0; q < kSlots; ++q) d[q] = total[q];
   }
+  if (dense) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = dense ? -(v[i] * rz) * (p.scale * dot) : 0.f;
-  if (at < p.T) store_row<T, NV>(out, e0, p.E, v);
+    for (int i = 0; i < NV; ++i) v[i] *= -rz * (p.scale * dot);
+    if (at < p.T) store_row<T, NV>(out, e0, p.E, v);
+  }
   __syncwarp();
   if (at >= p.T) return;
 #pragma unroll
