@@ -22,32 +22,52 @@ struct MxParams {
   uint8_t *codes, *scales;
   int64_t vecs;                    // of all rows
   int nvec, blocks, lds;           // of a row: vectors, scales, bytes from one row's scales to the next's
+  uint32_t recip;                  // 2^32 / nvec, rounded up: in / nvec is in * recip / 2^32 as long as in * nvec < 2^32
 };
 
 template <int kType> struct Raw { uint4 v; };
 template <> struct Raw<MOE_FP32> { uint4 v[2]; };
 
-__device__ __forceinline__ void unpack(const Raw<MOE_BF16>& r, float (&f)[8]) {
+// The largest magnitude's bits as of a float; a NaN's are above infinity's.
+__device__ __forceinline__ uint32_t top_of(const Raw<MOE_FP32>& r) {
+  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, w[i] & 0x7fffffffu);
+  return top;
+}
+__device__ __forceinline__ uint32_t top16(const uint4& v) {   // (two 16-bit maxima at a time: the order of magnitudes' bits)
+  constexpr uint32_t k = 0x7fff7fffu;
+  const uint32_t t = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+  return max(t & 0xffffu, t >> 16);
+}
+__device__ __forceinline__ uint32_t top_of(const Raw<MOE_BF16>& r) { return top16(r.v) << 16; }
+__device__ __forceinline__ uint32_t top_of(const Raw<MOE_FP16>& r) {
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top16(r.v))));
+}
+
+// The values times a power of two.
+__device__ __forceinline__ void scaled(const Raw<MOE_BF16>& r, float by, float (&f)[8]) {
   const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
+    f[2 * i] = bf16_lo(w[i]) * by;
+    f[2 * i + 1] = bf16_hi(w[i]) * by;
   }
 }
-__device__ __forceinline__ void unpack(const Raw<MOE_FP16>& r, float (&f)[8]) {
+__device__ __forceinline__ void scaled(const Raw<MOE_FP16>& r, float by, float (&f)[8]) {
   const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
+    f[2 * i] = v.x * by;
+    f[2 * i + 1] = v.y * by;
   }
 }
-__device__ __forceinline__ void unpack(const Raw<MOE_FP32>& r, float (&f)[8]) {
+__device__ __forceinline__ void scaled(const Raw<MOE_FP32>& r, float by, float (&f)[8]) {
   const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]) * by;
 }
 
 // Eight values to eight codes, the first in the lowest bits.
@@ -80,26 +100,20 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_mxf4_kernel(const MxPa
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int v = threadIdx.x + i * kThreads;
-    float f[8];
-    unpack(raw[i], f);
-    uint32_t top = 0;   // of the magnitudes' bits: a NaN's are above infinity's
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+    uint32_t top = top_of(raw[i]);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int field = (int)(top >> 23);
-    const int code = field == 255 ? 255 : max(field - 2, 0);
-    const float inv = field == 255 ? 0.f : __uint_as_float((uint32_t)(254 - code) << 23);
-    float q[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = field == 255 ? 0.f : f[j] * inv;
+    const uint32_t field = top >> 23, code = field == 255 ? 255u : max(field, 2u) - 2u;
+    float f[8];
+    scaled(raw[i], __uint_as_float((254u - min(code, 253u)) << 23), f);
+    const uint32_t w = encode8(f);
     if (v >= left) continue;
-    reinterpret_cast<uint32_t*>(p.codes)[base + v] = encode8(q);
+    reinterpret_cast<uint32_t*>(p.codes)[base + v] = code == 255 ? 0u : w;
     if ((v & 3) == 0) {
-      const int in = at0 + v, dr = in / p.nvec, block = (in - dr * p.nvec) / 4;
+      const uint32_t in = at0 + v, dr = __umulhi(in, p.recip), block = (in - dr * p.nvec) / 4;
       uint8_t* to = p.scales + (row0 + dr) * p.lds + block;
       *to = (uint8_t)code;
-      if (block == p.blocks - 1)
+      if ((int)block == p.blocks - 1)
         for (int b = p.blocks; b < p.lds; ++b) *++to = 0;
     }
   }
@@ -110,7 +124,8 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_mxf4_kernel(const MxPa
 cudaError_t launch_quantize_rows_mxf4(const void* src, int dtype, int64_t rows, int cols, uint8_t* codes,
                                       uint8_t* scales, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
-  MxParams p{src, codes, scales, rows * (cols / 8), cols / 8, cols / 32, mx_scale_stride(cols)};
+  MxParams p{src, codes, scales, rows * (cols / 8), cols / 8, cols / 32, mx_scale_stride(cols), 0};
+  p.recip = (uint32_t)((((uint64_t)1 << 32) + p.nvec - 1) / p.nvec);   // (nvec: 4 .. 8192)
   const int64_t per = kThreads * kVecs, blocks = (p.vecs + per - 1) / per;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   prof_mark(kKQuantMxf4, s, true);
