@@ -402,7 +402,9 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 
   bool border = false, doubt = false;   // the same in all lanes of a token
   const float tol = p.sigmoid ? 0x1p-19f : 0x1p-18f;
-  auto near_by = [](float hi, float lo, float by) { return hi - lo <= by * fmaxf(1.f, fabsf(hi)); };   // (of -inf: no)
+  auto near_by = [](float hi, float lo, float by) {   // (of infinities: no)
+    return hi < INFINITY && hi - lo <= by * fmaxf(1.f, fabsf(hi));
+  };
   if (p.top < p.n) {
     // scores of the groups: of masked experts nothing is added, and a group of none else comes last
     const int lanes = p.per / NV;   // of a group
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
           uint32_t need = 0;
 #pragma unroll
           for (int i = 0; i < NV; ++i)
-            if (key[i] > -INFINITY && (least == -INFINITY || key[i] >= from)) need |= 1u << i;
+            if (key[i] > -INFINITY && (least == -INFINITY || key[i] >= from || key[i] == INFINITY)) need |= 1u << i;
           double da = -INFINITY, db = -INFINITY;
           for (; need != 0; need &= need - 1)
             top2_merge(da, db, key64(p, row, e0 + __ffs(need) - 1, m, total), -INFINITY);
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
     for (int i = 0; i < NV; ++i) best[2 * i / NV] = fmaxf(best[2 * i / NV], key[i]);
     const float sorted = NV > 1 ? sort_pairs<G>(best[0], best[1], li) : sort_lanes<G>(best[0], li);
     float bound = __shfl_sync(mask, sorted, p.k, G);
-    rounds = !(bound > -INFINITY);
+    rounds = !(fabsf(bound) < INFINITY);
     if (kKeys) bound -= 2.f * tol * fmaxf(1.f, fabsf(bound));
     int upto = 0;
 #pragma unroll
@@ -571,8 +573,11 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         const int j = q * G + li;
         if (j >= p.k) continue;
         sidx[q] = cand.who[j];
-        // (there are more than k candidates)
-        if (kKeys) doubt |= near_by(cand.top[j], cand.top[j + 1], tol);
+        // (there are more than k candidates; one key twice by the same logit and bias is no doubt, but a tie)
+        if (kKeys && near_by(cand.top[j], cand.top[j + 1], tol)) {
+          const int e = cand.who[j], f = cand.who[j + 1];
+          doubt |= !(widen1(row[e]) == widen1(row[f]) && (p.bias == nullptr || p.bias[e] == p.bias[f]));
+        }
       }
       if (kKeys) doubt = (__ballot_sync(mask, doubt) & mine) != 0;
     }

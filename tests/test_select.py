@@ -190,6 +190,17 @@ def test_large_biases(moe):
         check(moe, l, b, 8, score, renorm=1)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_infinite_biases(moe, score):
+    """Experts that a bias puts first or last, fewer and more than the slots."""
+    for E, groups in ((64, dict()), (256, dict(groups=8, top=4, group_top=2)), (40, dict(groups=5, top=3, group_top=2))):
+        for n in (1, 3, 8, 20):
+            l, b = rand((60, E), n), rand((E,), n + 1, 0.1)
+            b[torch.randperm(E, device="cuda", generator=torch.Generator("cuda").manual_seed(n))[:n]] = INF
+            b[:3] = -INF
+            check(moe, l, b, 6, score, renorm=1, **groups)
+
+
 def test_far_logits(moe):
     """Scores that underflow in 32 bits: renormalised weights stay those of the scores' ratios."""
     for shift in (-60.0, -200.0, -3000.0, 100.0, 3000.0):
