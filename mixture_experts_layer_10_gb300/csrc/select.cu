@@ -107,7 +107,14 @@ template <class T, int NV> constexpr int vec_of() { return NV * (int)sizeof(T) <
 template <class T, int NV>
 __device__ __forceinline__ void load_row(const T* row, int e0, int E, float (&x)[NV]) {
   constexpr int V = vec_of<T, NV>();
-  if (E % V == 0) {   // rows start on V elements (the array on 16 bytes)
+  if (E % V == 0 && e0 + NV <= E) {   // rows start on V elements (the array on 16 bytes)
+#pragma unroll
+    for (int i = 0; i < NV; i += V) {
+      const Vec<T, V> r = *reinterpret_cast<const Vec<T, V>*>(row + e0 + i);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[i + j] = widen1(r.v[j]);
+    }
+  } else if (E % V == 0) {
 #pragma unroll
     for (int i = 0; i < NV; i += V) {
       Vec<T, V> r;
@@ -219,9 +226,9 @@ __device__ __noinline__ double softmax64(const SelParams& p, const T* row, int e
   return sum;
 }
 
-// One token by its G lanes: slot j to lane j % G, element j / G.
+// One token by its G lanes, the slots' experts to who.
 template <class T, int G, int NV>
-__device__ __noinline__ void select64(const SelParams& p, int64_t t, int lane, int (&sidx)[32 / G]) {
+__device__ __noinline__ void select64(const SelParams& p, int64_t t, int lane, int* who) {
   const uint32_t mask = group_mask<G>(lane);
   const int li = lane & (G - 1), e0 = li * NV;
   const T* row = static_cast<const T*>(p.logits) + t * p.E;
@@ -295,7 +302,7 @@ __device__ __noinline__ void select64(const SelParams& p, int64_t t, int lane, i
       }
     }
     if (e >= e0 && e < e0 + NV) gone |= 1u << (e - e0);
-    if (r % G == li) sidx[r / G] = e;
+    if (li == 0) who[r] = e;
   }
 }
 
@@ -304,13 +311,114 @@ __device__ __noinline__ void select64(const SelParams& p, int64_t t, int lane, i
 constexpr int kMaxCand = 32;       // candidates of a token
 
 // A token's share of shared memory.
-struct Cand {
-  alignas(16) float key[kMaxCand];   // -inf past the last
-  int e[kMaxCand];
-  double wide[kMaxCand];
-  float top[kMaxCand + 1];         // by rank
+template <int G, int NV>
+struct Token {
+  // its keys, -inf for masked experts: a lane's next to each other, lanes four words further apart than that, so that
+  // vectors of eight lanes fall on all banks
+  static constexpr int kPad = NV >= 4 ? 4 : 0;
+  alignas(16) float keys[G * (NV + kPad)];
+  alignas(16) float cand[kMaxCand];   // candidates' keys, -inf past the last
+  int e[kMaxCand];                    // and experts
+  float top[kMaxCand];                // by rank
   int who[kMaxCand];
+  union {
+    double wide[kMaxCand];
+    float scores[kMaxExpertGroups];   // of groups that do not fall on lanes
+  };
+  __device__ __forceinline__ float& key(int e) { return keys[e + e / NV * kPad]; }
 };
+
+// Whether two keys, the larger one first, may stand the other way round.  (Infinities do not.)
+__device__ __forceinline__ bool near_by(float hi, float lo, float by) {
+  return hi < INFINITY && hi - lo <= by * fmaxf(1.f, fabsf(hi));
+}
+
+// How many groups come before this lane's, by scores in 64 bits of the keys that may be among a group's largest.
+// `least`: the smallest key that the group's score counts.
+template <class T, int G, int NV>
+__device__ __noinline__ int groups_above64(const SelParams& p, const T* row, Token<G, NV>& token, int lane, int e0, float m,
+                                           float least, float tol) {
+  const uint32_t mine = group_mask<G>(lane);
+  const int lanes = p.per / NV, g = e0 / p.per;
+  const double total = softmax64<T, G, NV>(p, row, e0, m, mine);
+  const float from = least - 2.f * tol * fmaxf(1.f, fabsf(least));
+  double a = -INFINITY, b = -INFINITY;
+  uint32_t need = 0;   // (collected first: the lanes' few then go side by side)
+  for (int i = 0; i < NV && e0 + i < p.E; ++i) {
+    const float v = token.key(e0 + i);
+    if (v > -INFINITY && (least == -INFINITY || v >= from || v == INFINITY)) need |= 1u << i;
+  }
+  for (; need != 0; need &= need - 1) top2_merge(a, b, key64(p, row, e0 + __ffs(need) - 1, m, total), -INFINITY);
+  __syncwarp(mine);
+  for (int o = lanes / 2; o > 0; o >>= 1) top2_merge(a, b, __shfl_xor_sync(mine, a, o), __shfl_xor_sync(mine, b, o));
+  const double s = p.sum == 2 && b > -INFINITY ? a + b : a;
+  int above = 0;
+  for (int h = 0; h < p.n; ++h) {
+    const double o = __shfl_sync(mine, s, h * lanes, G);
+    above += h < g ? o >= s : o > s;
+  }
+  return above;
+}
+
+// The slots' experts by k rounds of a maximum over the lanes (a whole warp).  Returns whether two keys that follow each
+// other are too near.
+template <int G, int NV, bool kKeys>
+__device__ __noinline__ bool select_rounds(const SelParams& p, Token<G, NV>& token, int lane, uint32_t allowed, float tol) {
+  const int li = lane & (G - 1), e0 = li * NV;
+  const uint32_t mine = group_mask<G>(lane);
+  uint32_t u[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const float v = token.key(e0 + i);
+    u[i] = (allowed >> i & 1u) == 0 ? kTaken : (v > -INFINITY ? order_of(v) : kMasked);
+  }
+  uint32_t before = kTaken;   // the key of the slot before
+  bool doubt = false;
+  for (int r = 0; r < p.k + (int)kKeys; ++r) {   // (one more than the slots, for the border)
+    uint32_t best = u[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) best = max(best, u[i]);
+    const uint32_t v = group_max<G>(best, 0xffffffffu);
+    if (kKeys && r > 0 && v > kMasked) doubt |= near_by(value_of(before), value_of(v), tol);
+    before = v;
+    if (r == p.k) break;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, best == v) & mine) - 1;
+    int il = 0;
+#pragma unroll
+    for (int i = NV - 1; i >= 0; --i)
+      if (u[i] == v) il = i;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane == owner && i == il) u[i] = kTaken;
+    if (lane == owner) token.who[r] = e0 + il;
+  }
+  return doubt;
+}
+
+// The order of a token's candidates by keys in 64 bits: whoever may be among the k is one.
+template <class T, int G, int NV>
+__device__ __noinline__ void rank64(const SelParams& p, const T* row, Token<G, NV>& token, int lane, int e0, float m,
+                                    int count) {
+  constexpr int kSlots = 32 / G;
+  const int li = lane & (G - 1);
+  const uint32_t mine = group_mask<G>(lane);
+  const double total = softmax64<T, G, NV>(p, row, e0, m, mine);
+  for (int c = li; c < count; c += G) token.wide[c] = key64(p, row, token.e[c], m, total);
+  __syncwarp(mine);
+  int rank[kSlots];
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int own = q * G + li;
+    rank[q] = kMaxCand;
+    if (own >= count) continue;
+    rank[q] = 0;
+    const double v = token.wide[own];
+    for (int c = 0; c < count; ++c) rank[q] += c < own ? token.wide[c] >= v : token.wide[c] > v;
+  }
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q)
+    if (rank[q] < p.k) token.who[rank[q]] = token.e[q * G + li];
+}
 
 // Descending over the token's lanes.
 template <int G>
@@ -345,20 +453,14 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
   constexpr int kTok = 32 / G;       // tokens of a warp
   constexpr int kSlots = 32 / G;     // slots of a lane, and candidates
   constexpr uint32_t kAll = NV == 32 ? 0xffffffffu : (1u << (NV & 31)) - 1u;
-  union Shared {
-    struct {
-      float keys[32 * NV];
-      float scores[kTok][kMaxExpertGroups];
-    } g;
-    Cand c[kTok];
-  };
-  __shared__ Shared shared[kWarps];
+  __shared__ Token<G, NV> shared[kWarps][kTok];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & (G - 1), e0 = li * NV;
   constexpr uint32_t mask = 0xffffffffu;       // (all tokens of a warp take the same way)
   const uint32_t mine = group_mask<G>(lane);
   const int64_t at = ((int64_t)blockIdx.x * kWarps + warp) * kTok + lane / G;
   const int64_t t = min(at, p.T - 1);   // (lanes past the last token do its work again and store nothing)
   const T* row = static_cast<const T*>(p.logits) + t * p.E;
+  Token<G, NV>& token = shared[warp][lane / G];
   after_previous_kernel();
 
   float key[NV];   // the logits, then the keys: -inf for masked experts
@@ -402,9 +504,15 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 
   bool border = false, doubt = false;   // the same in all lanes of a token
   const float tol = p.sigmoid ? 0x1p-19f : 0x1p-18f;
-  auto near_by = [](float hi, float lo, float by) {   // (of infinities: no)
-    return hi < INFINITY && hi - lo <= by * fmaxf(1.f, fabsf(hi));
-  };
+  if (NV % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 4)
+      *reinterpret_cast<float4*>(&token.key(e0) + i) = make_float4(key[i], key[i + 1 < NV ? i + 1 : 0], key[i + 2 < NV ? i + 2 : 0],
+                                                                   key[i + 3 < NV ? i + 3 : 0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) token.key(e0 + i) = key[i];
+  }
   if (p.top < p.n) {
     // scores of the groups: of masked experts nothing is added, and a group of none else comes last
     const int lanes = p.per / NV;   // of a group
@@ -431,54 +539,33 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         const uint32_t last = __ballot_sync(mask, e0 < p.E && above == p.top - 1) & mine;
         const uint32_t next = __ballot_sync(mask, e0 < p.E && above == p.top) & mine;
         const float sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
-        // a border in doubt: the scores again, of the keys that may be among a group's largest, in 64 bits
-        if (near_by(sl, sn, 2.f * tol)) {
-          const double total = softmax64<T, G, NV>(p, row, e0, m, mine);
-          const float least = p.sum == 2 ? b : a;
-          const float from = least - 2.f * tol * fmaxf(1.f, fabsf(least));
-          uint32_t need = 0;
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (key[i] > -INFINITY && (least == -INFINITY || key[i] >= from || key[i] == INFINITY)) need |= 1u << i;
-          double da = -INFINITY, db = -INFINITY;
-          for (; need != 0; need &= need - 1)
-            top2_merge(da, db, key64(p, row, e0 + __ffs(need) - 1, m, total), -INFINITY);
-          __syncwarp(mine);
-          for (int o = lanes / 2; o > 0; o >>= 1)
-            top2_merge(da, db, __shfl_xor_sync(mine, da, o), __shfl_xor_sync(mine, db, o));
-          const double ds = p.sum == 2 && db > -INFINITY ? da + db : da;
-          above = 0;
-          for (int h = 0; h < p.n; ++h) {
-            const double o = __shfl_sync(mine, ds, h * lanes, G);
-            above += h < g ? o >= ds : o > ds;
-          }
-        }
+        if (near_by(sl, sn, 2.f * tol)) above = groups_above64<T, G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol);
         __syncwarp();
       }
-      if (above >= p.top) allowed = 0u;
+      if (above >= p.top) {
+        allowed = 0u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = -INFINITY;
+      }
     } else {
       // groups that do not fall on lanes: through shared memory, a group a lane
-      float* kr = shared[warp].g.keys + (lane / G) * (G * NV);
-      float* sr = shared[warp].g.scores[lane / G];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) kr[e0 + i] = key[i];
       __syncwarp();
       for (int g = li; g < p.n; g += G) {
         float a = -INFINITY, b = -INFINITY;
         for (int e = g * p.per; e < (g + 1) * p.per; ++e) {
-          const float v = kr[e];
+          const float v = token.key(e);
           b = fmaxf(b, fminf(a, v));
           a = fmaxf(a, v);
         }
-        sr[g] = p.sum == 2 && b > -INFINITY ? a + b : a;
+        token.scores[g] = p.sum == 2 && b > -INFINITY ? a + b : a;
       }
       __syncwarp();
       float lo = INFINITY, hi = -INFINITY;   // the lowest score kept, the highest dropped
       uint32_t drop[2] = {0u, 0u};
       for (int g = li; g < p.n; g += G) {
-        const float s = sr[g];
+        const float s = token.scores[g];
         int above = 0;
-        for (int h = 0; h < p.n; ++h) above += h < g ? sr[h] >= s : sr[h] > s;
+        for (int h = 0; h < p.n; ++h) above += h < g ? token.scores[h] >= s : token.scores[h] > s;
         if (above < p.top) {
           lo = fminf(lo, s);
         } else {
@@ -495,22 +582,17 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int g = min((e0 + i) / p.per, p.n - 1);
-        if ((drop[g >> 5] >> (g & 31) & 1u) != 0) allowed &= ~(1u << i);
+        if ((drop[g >> 5] >> (g & 31) & 1u) != 0) {
+          allowed &= ~(1u << i);
+          key[i] = -INFINITY;   // (masked ones of the groups that stay: only the rounds below choose them)
+        }
       }
-      __syncwarp();   // (the candidates come where the keys were)
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)   // (masked ones of the groups that stay: only the rounds below choose them)
-      if ((allowed >> i & 1u) == 0) key[i] = -INFINITY;
   }
 
-  int sidx[kSlots];
-#pragma unroll
-  for (int q = 0; q < kSlots; ++q) sidx[q] = 0;
   // The bound: the k + 1st of the largest keys of half lanes, less what keys may be off
   bool rounds = p.k >= G;
   int count = 0;   // candidates of the token
-  Cand& cand = shared[warp].c[lane / G];
   if (!rounds) {
     float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -519,40 +601,37 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
     float bound = __shfl_sync(mask, sorted, p.k, G);
     rounds = !(fabsf(bound) < INFINITY);
     if (kKeys) bound -= 2.f * tol * fmaxf(1.f, fabsf(bound));
-    int upto = 0;
+    uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) upto += key[i] >= bound;
-    const int own = upto;
+    for (int i = 0; i < NV; ++i) bits |= key[i] >= bound ? 1u << i : 0u;
+    int upto = __popc(bits);
+    int to = -upto;
 #pragma unroll
     for (int o = 1; o < G; o <<= 1) {
       const int v = __shfl_up_sync(mask, upto, o, G);
       if (li >= o) upto += v;
     }
+    to += upto;
     count = __shfl_sync(mask, upto, G - 1, G);
     rounds = __any_sync(mask, rounds || count > kMaxCand);
     if (!rounds) {
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q)
-        if (q * G + li >= count) cand.key[q * G + li] = -INFINITY;
-      int to = upto - own;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (key[i] >= bound) {
-          cand.key[to] = key[i];
-          cand.e[to++] = e0 + i;
-        }
+      for (; bits != 0; bits &= bits - 1) token.e[to++] = e0 + __ffs(bits) - 1;
       __syncwarp();
       // ranks: candidates lie in the order of the experts, so that among equal ones the earlier comes first
       float own_key[kSlots];
-      int rank[kSlots];
+      int own_e[kSlots], rank[kSlots];
 #pragma unroll
       for (int q = 0; q < kSlots; ++q) {
-        own_key[q] = cand.key[q * G + li];
+        const bool in = q * G + li < count;
+        own_e[q] = in ? token.e[q * G + li] : 0;
+        own_key[q] = in ? token.key(own_e[q]) : -INFINITY;
+        token.cand[q * G + li] = own_key[q];
         rank[q] = 0;
       }
+      __syncwarp();
       const int most = G == 32 ? count : __reduce_max_sync(mask, count);
       for (int c = 0; c < most; c += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(cand.key + c);
+        const float4 v = *reinterpret_cast<const float4*>(token.cand + c);
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) {
           if (q > 0 && most <= q * G) break;
@@ -564,92 +643,33 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 #pragma unroll
       for (int q = 0; q < kSlots; ++q)
         if (q * G + li < count) {
-          cand.top[rank[q]] = own_key[q];
-          cand.who[rank[q]] = cand.e[q * G + li];
+          token.top[rank[q]] = own_key[q];
+          token.who[rank[q]] = own_e[q];
         }
       __syncwarp();
+      if (kKeys) {
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        const int j = q * G + li;
-        if (j >= p.k) continue;
-        sidx[q] = cand.who[j];
-        // (there are more than k candidates; one key twice by the same logit and bias is no doubt, but a tie)
-        if (kKeys && near_by(cand.top[j], cand.top[j + 1], tol)) {
-          const int e = cand.who[j], f = cand.who[j + 1];
-          doubt |= !(widen1(row[e]) == widen1(row[f]) && (p.bias == nullptr || p.bias[e] == p.bias[f]));
+        for (int q = 0; q < kSlots; ++q) {
+          const int j = q * G + li;
+          // (there are more than k candidates; one key twice by the same logit and bias is no doubt, but a tie)
+          if (j < p.k && near_by(token.top[j], token.top[j + 1], tol)) {
+            const int e = token.who[j], f = token.who[j + 1];
+            doubt |= !(widen1(row[e]) == widen1(row[f]) && (p.bias == nullptr || p.bias[e] == p.bias[f]));
+          }
         }
-      }
-      if (kKeys) doubt = (__ballot_sync(mask, doubt) & mine) != 0;
-    }
-  }
-  if (rounds) {
-    uint32_t u[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      u[i] = (allowed >> i & 1u) == 0 ? kTaken : (key[i] > -INFINITY ? order_of(key[i]) : kMasked);
-    uint32_t before = kTaken;   // the key of the slot before
-    doubt = false;
-#pragma unroll
-    for (int q = 0; q <= kSlots; ++q) {
-      for (int rr = 0; rr < G; ++rr) {
-        const int r = q * G + rr;
-        if (r > p.k || (r == p.k && !kKeys)) break;   // (one more than the slots, for the border)
-        uint32_t best = u[0];
-#pragma unroll
-        for (int i = 1; i < NV; ++i) best = max(best, u[i]);
-        const uint32_t v = group_max<G>(best, mask);
-        if (kKeys) {
-          if (r > 0 && v > kMasked) doubt |= near_by(value_of(before), value_of(v), tol);
-          before = v;
-          if (r == p.k) break;
-        }
-        const int owner = __ffs(__ballot_sync(mask, best == v) & mine) - 1;
-        int il = 0;
-#pragma unroll
-        for (int i = NV - 1; i >= 0; --i)
-          if (u[i] == v) il = i;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (lane == owner && i == il) u[i] = kTaken;
-        const int e = __shfl_sync(mask, e0 + il, owner);
-        if (q < kSlots && rr == li) sidx[q] = e;
+        doubt = (__ballot_sync(mask, doubt) & mine) != 0;
       }
     }
   }
+  if (rounds) doubt = select_rounds<G, NV, kKeys>(p, token, lane, allowed, tol);
   if (kKeys) {
-    if (border || (doubt && rounds)) {
-      select64<T, G, NV>(p, t, lane, sidx);
-    } else if (doubt) {
-      // every candidate's key in 64 bits: whoever may be among the k is one
-      const double total = softmax64<T, G, NV>(p, row, e0, m, mine);
-      double wide[kSlots];
-      int rank[kSlots];
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        const int c = q * G + li;
-        rank[q] = kMaxCand;
-        wide[q] = -INFINITY;
-        if (c >= count) continue;
-        wide[q] = key64(p, row, cand.e[c], m, total);
-        cand.wide[c] = wide[q];
-        rank[q] = 0;
-      }
-      __syncwarp(mine);
-      for (int c = 0; c < count; ++c) {
-        const double v = cand.wide[c];
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q) rank[q] += c < q * G + li ? v >= wide[q] : v > wide[q];
-      }
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q)
-        if (rank[q] < p.k) cand.who[rank[q]] = cand.e[q * G + li];
-      __syncwarp(mine);
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q)
-        if (q * G + li < p.k) sidx[q] = cand.who[q * G + li];
-    }
+    if (border || (doubt && rounds)) select64<T, G, NV>(p, t, lane, token.who);
+    else if (doubt) rank64<T, G, NV>(p, row, token, lane, e0, m, count);
   }
   __syncwarp();
+  int sidx[kSlots];
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) sidx[q] = q * G + li < p.k ? token.who[q * G + li] : 0;
 
   // weights, a slot a lane
   float xs[kSlots], M = -INFINITY;
