@@ -467,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (kOp == kMx ? elect_one() : lane == 0) {
       int slot = 0, uses = 0;
       uint32_t phase = 0;
       int mapped = -1;   // weight gradient: the group whose maps are in use
@@ -911,10 +911,15 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base
 }
 
 // Rows of 4-bit values [rows, bytes] as K-major boxes of 128 bytes x 96, 64 and 32 rows.
+// (Only those that a tile of so many rows may ask for; the others hold the smallest.)
 bool map_mx_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t bytes, uint64_t ld) {
   const cuuint64_t dims[2] = {bytes, rows}, strides[1] = {ld};
-  for (uint32_t i = 0; i < kBoxes; ++i) {
-    const cuuint32_t box[2] = {kMxWide, 96 - 32 * i};
+  for (int i = kBoxes - 1; i >= 0; --i) {
+    if (i < kBoxes - 1 && rows <= 64u * (kBoxes - 1 - i)) {
+      m[i] = m[kBoxes - 1];
+      continue;
+    }
+    const cuuint32_t box[2] = {kMxWide, 96u - 32u * i};
     if (!encode(&m[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
   }
   return true;
