@@ -719,19 +719,20 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 //   renormalised      d_j = w_j (c_j - sum_m c_m h_m), sigmoid: times 1 - s_j
 //   not renormalised  d_j = scale c_j s_j (1 - s_j); softmax: d_j = scale p_j (c_j - sum_m c_m p_m), and
 //                     -scale p_e sum_m c_m p_m for the experts of no slot
-// The row is first written as of a token without slots, in whole vectors, and then at the slots' experts, by the same
-// warp: no lane looks through its experts for every slot (46 us at 65536 tokens of 256 experts).  An expert in several
-// slots gets the sum of their terms, in slot order, from the first of them.
-template <class T, int G, int NV>
+// The rows are first written as of tokens without slots, in whole vectors, and then at the slots' experts, by the same
+// warp: no lane looks through its experts for every slot (46 us at 65536 tokens of 256 experts).  Only a softmax that is not
+// renormalised reads a whole row, and has lanes enough for it; else the slots alone say how many lanes a token
+// has (16 for 8 slots: 22 us).  An expert in several slots gets the sum of their terms, in slot order, from
+// the first of them.
+template <class T, int G, int NV, bool kDense>
 __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_kernel(const __grid_constant__ SelParams p) {
-  constexpr int kTok = 32 / G, kSlots = 32 / G;
+  constexpr int kTok = 32 / G, kSlots = kDense ? 32 / G : 1;   // (sparse: k is at most G)
   constexpr uint32_t mask = 0xffffffffu;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & (G - 1), e0 = li * NV;
   const int64_t at = ((int64_t)blockIdx.x * kWarps + warp) * kTok + lane / G;
   const int64_t t = min(at, p.T - 1);
   const T* row = static_cast<const T*>(p.logits) + t * p.E;
   T* out = static_cast<T*>(p.dl) + t * p.E;
-  __shared__ uint8_t marks[kWarps][32 * NV];
   after_previous_kernel();
 
   int e[kSlots];
@@ -748,16 +749,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
     }
     if (e[q] < 0 || e[q] >= p.E) e[q] = -1;   // (no expert: a slot without weight)
   }
-  const bool dense = !p.sigmoid && !p.renorm;
-  float v[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = 0.f;
-  if (!dense) {   // zeros, of all the warp's tokens, which lie on end
-    const int64_t first = at - lane / G;
-    if (first < p.T) fill_zero(static_cast<T*>(p.dl) + first * p.E, (int)min((int64_t)kTok, p.T - first) * p.E, p.E, lane);
-  }
-  float m = -FLT_MAX, rz = 0.f;
-  if (dense) {
+  float v[NV], m = -FLT_MAX, rz = 0.f;
+  if constexpr (kDense) {
     load_row<T, NV>(row, e0, p.E, v);
 #pragma unroll
     for (int i = 0; i < NV; ++i) m = fmaxf(m, v[i]);
@@ -770,6 +763,9 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
     }
     z = group_sum<G>(z, mask);
     rz = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
+  } else {   // zeros, of all the warp's tokens, which lie on end
+    const int64_t first = at - lane / G;
+    if (first < p.T) fill_zero(static_cast<T*>(p.dl) + first * p.E, (int)min((int64_t)kTok, p.T - first) * p.E, p.E, lane);
   }
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
@@ -783,8 +779,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
   for (int q = 0; q < kSlots; ++q) {
     h[q] = 0.f;
     if (q * G >= p.k) continue;
-    if (!p.renorm) h[q] = p.sigmoid ? sigmoid32(xs[q]) : __expf(xs[q] - m) * rz;
-    else if (p.sigmoid && M >= -40.f) h[q] = sigmoid32(xs[q]);
+    if (kDense) h[q] = __expf(xs[q] - m) * rz;
+    else if (p.sigmoid && !(p.renorm && M < -40.f)) h[q] = sigmoid32(xs[q]);
     else h[q] = M == -INFINITY ? 0.f : expf(xs[q] - M);
     if (e[q] < 0) h[q] = 0.f;
     sum += h[q];
@@ -797,7 +793,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
   }
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) dot += c[q] * h[q];
-  if (p.renorm || dense) dot = group_sum<G>(dot, mask);
+  if (p.renorm || kDense) dot = group_sum<G>(dot, mask);
   float d[kSlots];
   bool first[kSlots];
 #pragma unroll
@@ -806,18 +802,20 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
     d[q] = 0.f;
     if (q * G >= p.k) continue;
     d[q] = h[q] == 0.f ? 0.f : p.scale * h[q] * (p.renorm ? c[q] - dot : c[q]);
-    if (p.sigmoid) d[q] *= sigmoid32(-xs[q]);   // (of a slot without an expert 1)
+    if (!kDense && p.sigmoid) d[q] *= sigmoid32(-xs[q]);   // (of a slot without an expert 1)
   }
-  // whether an expert comes twice: a slot that does not find its own mark on its expert
+  // whether an expert comes twice among a token's slots
   bool twice = false;
-  uint8_t* tags = marks[warp] + (lane / G) * (G * NV);
 #pragma unroll
   for (int q = 0; q < kSlots; ++q)
-    if (e[q] >= 0) tags[e[q]] = (uint8_t)(q * G + li);
-  __syncwarp();
 #pragma unroll
-  for (int q = 0; q < kSlots; ++q)
-    if (e[q] >= 0) twice |= tags[e[q]] != (uint8_t)(q * G + li);
+    for (int r = 0; r <= q; ++r) {
+      if (q * G >= p.k) break;
+      for (int o = r == q ? 1 : 0; o < G; ++o) {
+        const int other = __shfl_xor_sync(mask, e[r], o);
+        twice |= other == e[q] && other >= 0;
+      }
+    }
   if (__any_sync(mask, twice)) {
     float total[kSlots] = {};
 #pragma unroll
@@ -836,7 +834,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
 #pragma unroll
     for (int q = 0; q < kSlots; ++q) d[q] = total[q];
   }
-  if (dense) {
+  if constexpr (kDense) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] *= -rz * (p.scale * dot);
     if (at < p.T) store_row<T, NV>(out, e0, p.E, v);
@@ -845,7 +843,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
   if (at >= p.T) return;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q)
-    if (first[q]) out[e[q]] = narrow1<T>(dense ? d[q] - h[q] * (p.scale * dot) : d[q]);
+    if (first[q]) out[e[q]] = narrow1<T>(kDense ? d[q] - h[q] * (p.scale * dot) : d[q]);
 }
 
 // ---- host side -----------------------------------------------------------------------------------
@@ -904,7 +902,12 @@ struct Backward {
   cudaStream_t s;
   template <class T, int G, int NV>
   cudaError_t call() const {
-    return launch_after(select_bwd_kernel<T, G, NV>, blocks_of(p.T, 32 / G), 32 * kWarps, 0, 1, s, p);
+    if (!p.sigmoid && !p.renorm) return launch<T, G, NV, true>();
+    return p.k <= 8 ? launch<T, 8, 1, false>() : p.k <= 16 ? launch<T, 16, 1, false>() : launch<T, 32, 1, false>();
+  }
+  template <class T, int G, int NV, bool kDense>
+  cudaError_t launch() const {
+    return launch_after(select_bwd_kernel<T, G, NV, kDense>, blocks_of(p.T, 32 / G), 32 * kWarps, 0, 1, s, p);
   }
 };
 
