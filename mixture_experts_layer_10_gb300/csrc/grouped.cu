@@ -1,6 +1,6 @@
 // Grouped products: rows of every group times the group's own weight (y = x W[g]^T, dx = dy W[g]), the
 // gradient of the weight (dW[g] = dy^T x over the group's rows), and the first of them with 8-bit
-// integers.  Groups are given on the device as first and past-the-end rows, of any length and start;
+// integers and with microscaled 4-bit values.  Groups are given on the device as first and past-the-end rows, of any length and start;
 // nothing is padded or copied.
 //
 // All of them run on the 5th-generation tensor cores in one persistent kernel per product, on CTA pairs
@@ -11,6 +11,7 @@
 //   warp 1      MMA issuer (the even CTA's one thread)
 //   warps 2-5   epilogue: tcgen05.ld of the accumulator, scales, rounding, stores
 //   warps 6-21  8-bit integers: widen the codes to fp16 (below)
+//   warps 6-13  4-bit values: bring their scales to TMEM (below)
 //
 // Rows times a weight.  The weight's 256 features are the M side of the tile and up to 256 rows of one
 // group its N side, so a group's ragged end costs a narrower product (N in steps of 32) rather than
@@ -35,6 +36,16 @@
 // fp16 and a product of two in fp32, so fp16 tensor products of widened codes are the integer products,
 // and their fp32 sums are exact up to 2^24.  TMA brings the codes as bytes to a ring of raw stages, and
 // sixteen warps widen them into the ring that the tensor cores read.
+//
+// Microscaled 4-bit values.  kind::mxf4 multiplies them and their scales as they are: a stage is the same 128 bytes of a
+// row, 256 values deep, and the tile 256 features x 192 rows, which leaves the scales 128 columns of TMEM beside two
+// accumulators.  Five stages, each with columns for its scales.  What bounds it (16384 rows, 8 groups, 4096 x
+// 14336, 365 us, 5.3 PFLOP/s): the copies alone take 295 us (15 TB/s from L2), the products alone about 265, both
+// without scales 304; the scales are 9% more traffic and one more arrival a stage to wait for.  Few rows read the
+// weights at 5.1 TB/s.  Steps on the way, same size: scales copied by tcgen05.cp 644 us; written to TMEM from registers
+// 525; by two teams in turn 474; one barrier a stage for operands and scales 434; one elected thread issuing 374; scales
+// a sector at a time 368.  (Tried and not kept: four stages, tiles of equal height, weights fetched to L2 ahead,
+// eight epilogue warps: 362, 367, 382, 382 us, the smaller sizes slower or the same.)
 //
 // Measured (graph replays on inputs larger than L2; 36 launches / after three seconds of them, when the power
 // cap has lowered the clock): y of 16384 rows, 8 groups, 4096 x 14336, bf16: 1.14 / 1.19 ms, 1.69 / 1.62
@@ -78,6 +89,7 @@ constexpr int kMxTurn = 4;                   // stages whose scales are brought 
 constexpr int kMxPieces = (2 * kMxHand + 128 * kMxTeams - 1) / (128 * kMxTeams);   // of 16 bytes, a thread's share of them
 constexpr uint32_t kMxScales = 2 * 32 * kMxHand;   // two hand-overs
 constexpr int kAheadMx = 2;                  // 4-bit: such times that are on their way
+constexpr int kMxSplit = 16;                 // K blocks of a tile from which two or four pairs share them
 constexpr int kMxCols = 24;                  // their TMEM columns: 2 words x (4 + 8)
 
 template <int kOp>
@@ -119,7 +131,7 @@ struct Params {
 struct Job {
   int g, row, n, f0;   // rows times a weight: first row, rows, first feature
   int kits;            // K blocks
-  int k0, k;           // weight gradient (row, n, f0: rows and columns of dW): rows of the run,
+  int k0, k;           // weight gradient (row, n, f0: rows and columns of dW): rows of the run; 4-bit: the first K block
   int run, runs;       // its number, of how many
 };
 
@@ -178,19 +190,24 @@ __device__ __forceinline__ int box_of(int half) { return half > 64 ? 0 : (half >
 
 // One pair's walk over its tiles, the same in every role of both CTAs: rows times a weight has one job a
 // tile, the weight gradient one a run of rows.
-template <int kOp>
+template <int kOp, int kSplit = 1>
 struct Walk {
   const Params& p;
   const GroupTab& s;
-  int t, step, ntiles, run = 0;
-  __device__ Walk(const Params& p_, const GroupTab& s_, int first, int step_, int ntiles_)
-      : p(p_), s(s_), t(first), step(step_), ntiles(ntiles_) {}
+  int t, step, ntiles, part, run = 0;
+  __device__ Walk(const Params& p_, const GroupTab& s_, int first, int step_, int ntiles_, int part_)
+      : p(p_), s(s_), t(first), step(step_), ntiles(ntiles_), part(part_) {}
   __device__ bool next(Job& j) {
     if (kOp != kDw) {
       if (t >= ntiles) return false;
       constexpr int kDeep = kOp == kMx ? kMxWide : kBK;
       j = row_job<Shape<kOp>::kRows>(p, s, t);
       j.kits = (p.depth + kDeep - 1) / kDeep;
+      if (kSplit > 1) {   // this pair's share of them, from an even one on (scales come 16 bytes, two blocks, at a time)
+        const int twos = (j.kits + 1) / 2;
+        j.k0 = twos * part / kSplit * 2;
+        j.kits = min(j.kits, twos * (part + 1) / kSplit * 2) - j.k0;
+      }
       t += step;
       return true;
     }
@@ -380,13 +397,13 @@ __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int32_t c0, 
                : "memory");
 }
 
-// Arrive once on the mbarrier at this shared-memory offset in both CTAs when every pair MMA this thread
+// Arrive once on the mbarrier at this shared-memory offset in both CTAs (`lead`: the even one's rank) when every pair MMA this thread
 // issued so far has completed.
-__device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
+__device__ __forceinline__ void umma_commit_both(uint64_t* bar, int lead) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)(3 << lead))
       : "memory");
 }
 
@@ -401,8 +418,12 @@ __device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
 //   rempty[s]   8-bit integers, own CTA: every widening warp has passed it
 // Every wait is bounded; whatever happens, both CTAs meet at the last cluster barrier before TMEM is
 // freed, with their own copies landed.
-template <int kOp>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads, 1)
+//
+// kSplit pairs of a cluster share the contraction of a tile (4-bit, few tiles): each sums its K blocks, leaves the sums in
+// its stages, which are free then, and stores a share of the rows, adding all pairs' sums in their order.  A cluster
+// has one tile.
+template <int kOp, int kSplit = 1>
+__global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(Shape<kOp>::kThreads, 1)
     grouped_kernel(const __grid_constant__ Params p) {
   using S = Shape<kOp>;
   constexpr int kStages = S::kStages;
@@ -424,8 +445,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   GroupTab& tab = *reinterpret_cast<GroupTab*>(scales + S::kScales + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank();
-  const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
+  const int crank = (int)cluster_rank(), rank = kSplit == 1 ? crank : crank & 1;
+  const int lead = kSplit == 1 ? 0 : crank & ~1, part = kSplit == 1 ? 0 : crank >> 1;
+  const int pair = (int)blockIdx.x / (2 * kSplit), npairs = (int)gridDim.x / (2 * kSplit);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
       mbar_init(&full[s], kOp == kI8 ? 2 * S::kTeam : (kOp == kMx ? 1 + 2 * 4 : 1));
@@ -458,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t limit = wait_limit_ns(p.hdr);
   const int ntiles = rtiles < 0 ? 0 : (kOp == kDw ? p.G * p.mf * p.nf : rtiles * (p.nf + (int)p.narrow));
-  Walk<kOp> walk(p, tab, pair, npairs, ntiles);
+  Walk<kOp, kSplit> walk(p, tab, pair, npairs, ntiles, part);
   Job j;
 
   auto fail = [&](int site) {
@@ -524,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
             if (uses != skip) {
               uint8_t* st = stages + (size_t)slot * kStage;
               if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * bytes);
-              const uint32_t bar = cluster_addr(&full[slot], 0);
+              const uint32_t bar = cluster_addr(&full[slot], lead);
               if constexpr (kOp == kDw) {
                 const int row = j.k0 + kit * kBK, ca = j.f0 + kBM * rank, cb = j.row + kBM * rank;
                 if (p.wide_a) {
@@ -542,12 +564,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
               } else {
                 const int f = j.f0 + kBM * rank;
                 if (kOp == kMm || kOp == kMx) {
-                  tma_load_3d_pair(st, ma, bar, kit * (kOp == kMx ? kMxWide : kBK), f, j.g);
+                  tma_load_3d_pair(st, ma, bar, kOp == kMx ? (j.k0 + kit) * kMxWide : kit * kBK, f, j.g);
                 } else {
                   tma_load_3d_pair(st, ma, bar, f, kit * kBK, j.g);
                   tma_load_3d_pair(st + kBox, ma, bar, f + 64, kit * kBK, j.g);
                 }
-                tma_load_2d_pair(st + kHalf, mb, bar, kit * (kOp == kMx ? kMxWide : kBK), j.row + half * rank);
+                tma_load_2d_pair(st + kHalf, mb, bar, kOp == kMx ? (j.k0 + kit) * kMxWide : kit * kBK, j.row + half * rank);
               }
             }
             if (kOp != kMx && rank == 0 && uses >= kStages) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 1));
@@ -604,7 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
             const uint64_t db = kOp == kDw ? sdesc_mnmajor(sa + kHalf + kk * 2048, kBox) : sdesc_kmajor(sa + kHalf + kk * 32);
             umma_bf16_pair(dt, da, db, idesc, (kit | kk) != 0);
           }
-          if (kOp == kI8 || kOp == kMx) umma_commit_both(&empty[slot]);
+          if (kOp == kI8 || kOp == kMx) umma_commit_both(&empty[slot], lead);
           else umma_commit_pair(smem_u32(&empty[slot]));
           if (++slot == kStages) {
             slot = 0;
@@ -612,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
           }
         }
         if (!ok) break;
-        umma_commit_both(&tfull[acc]);
+        umma_commit_both(&tfull[acc], lead);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1;
@@ -620,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       }
       // every pair MMA issued has completed, and every arrival on either CTA's barriers, before the
       // TMEM is freed and the CTAs exit (bounded)
-      umma_commit_both(drain);
+      umma_commit_both(drain, lead);
     }
     if (lane == 0) mbar_wait_drain(drain, 0, limit);
   } else if (warp < 2 + S::kEpiWarps) {
@@ -641,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       tc_fence_before();
       __syncwarp();
       // (relaxed: the reads of the accumulator have completed, and a release would wait for the tile's stores)
-      if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[acc], 0));
+      if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[acc], lead));
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
@@ -675,6 +697,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
         continue;
       }
       if (!wait_acc()) break;
+      if constexpr (kSplit > 1) {
+        float* red = reinterpret_cast<float*>(stages) + 32 * q + lane;   // [row][the CTA's 128 features]
+        for (int c = 0; c < j.n; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(acc_addr() + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) red[(c + i) * kBM] = __uint_as_float(v[i]);
+        }
+        break;
+      }
       store_tile<kOp>(p, j, rank, q, lane, acc_addr(), share);
       release_acc();
     }
@@ -734,7 +767,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
         __syncwarp();
         if (lane == 0) {
           fence_release_smem();
-          mbar_arrive_cluster_relaxed(cluster_addr(&full[team], 0));
+          mbar_arrive_cluster_relaxed(cluster_addr(&full[team], lead));
         }
       }
       block += kits;
@@ -796,7 +829,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
       t.stages = min(kMxTurn, kits - kit);
       if (t.stages <= 0) return;
 #pragma unroll
-      for (int i = 0; i < kMxPieces; ++i) t.v[i] = fetch(from[i], kit * kMxBlocks + (r & 1) * 16);
+      for (int i = 0; i < kMxPieces; ++i) t.v[i] = fetch(from[i], (j.k0 + kit) * kMxBlocks + (r & 1) * 16);
       kit += kMxTurn;
     };
 #pragma unroll
@@ -848,7 +881,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
               tmem_st_wait();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&full[slot], 0));   // (the writes have completed)
+              if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&full[slot], lead));   // (the writes have completed)
             }
           }
           if (++slot == kStages) {
@@ -862,6 +895,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kOp>::kThreads
   tc_fence_before();
   __syncthreads();
   cluster_sync();
+  if constexpr (kSplit > 1) {
+    Walk<kOp, kSplit> again(p, tab, pair, npairs, ntiles, part);
+    if (again.next(j)) {   // this pair's rows of the tile, two features a lane and turn
+      static_assert(kMxRows * kBM * 4 <= kStages * (int)kStage, "room for the sums");
+      const float* red = reinterpret_cast<const float*>(stages);
+      const int from = j.n * part / kSplit, to = j.n * (part + 1) / kSplit;
+      for (int i = 2 * from + warp; i < 2 * to; i += S::kThreads / 32) {
+        const int row = i / 2, fl = (i & 1) * 64 + 2 * lane, f = j.f0 + kBM * rank + fl;
+        if (f >= p.width) continue;   // (a multiple of 8)
+        float2 v = load_peer(red + row * kBM + fl, rank);
+#pragma unroll
+        for (int o = 1; o < kSplit; ++o) {
+          const float2 w = load_peer(red + row * kBM + fl, 2 * o + rank);
+          v = make_float2(v.x + w.x, v.y + w.y);
+        }
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + ((int64_t)j.row + row) * p.ldy + f) =
+            pack16(v.x, v.y, p.fp16);
+      }
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA ends while another may read its sums
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
@@ -985,30 +1040,38 @@ Params params_of(const Grouped& c, const int32_t* begin, const int32_t* end, Hdr
   return p;
 }
 
-template <int kOp>
-cudaError_t launch(const Params& p, int64_t most_tiles, int id, cudaStream_t s) {
+// How many clusters run at once.
+template <int kOp, int kSplit = 1>
+cudaError_t clusters_at_once(int* fit) {
   using S = Shape<kOp>;
   static SmemOnce once;
-  static IntOnce most;   // pairs that run at once
-  cudaError_t e = once.set(reinterpret_cast<const void*>(grouped_kernel<kOp>), S::kSmem);
+  static IntOnce most;
+  cudaError_t e = once.set(reinterpret_cast<const void*>(grouped_kernel<kOp, kSplit>), S::kSmem);
   if (e != cudaSuccess) return e;
-  int fit = 0;
-  e = most.get(&fit, [] {
+  return most.get(fit, [] {
+    constexpr int kSize = 2 * kSplit;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
+    cfg.gridDim = dim3(kSize * (num_sms() / kSize), 1, 1);
     cfg.blockDim = dim3(S::kThreads, 1, 1);
     cfg.dynamicSmemBytes = S::kSmem;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, grouped_kernel<kOp>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, grouped_kernel<kOp, kSplit>, &cfg) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
-      n = num_sms() / 2;
+      n = num_sms() / kSize;
     }
-    return std::min(n, num_sms() / 2);
+    return std::min(n, num_sms() / kSize);
   });
+}
+
+template <int kOp, int kSplit = 1>
+cudaError_t launch(const Params& p, int64_t most_tiles, int id, cudaStream_t s) {
+  using S = Shape<kOp>;
+  int fit = 0;
+  cudaError_t e = clusters_at_once<kOp, kSplit>(&fit);
   if (e != cudaSuccess) return e;
-  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(fit, most_tiles));
+  const int64_t clusters = kSplit > 1 ? most_tiles : std::max<int64_t>(1, std::min<int64_t>(fit, most_tiles));
   prof_mark(id, s, true);
-  e = launch_after(grouped_kernel<kOp>, 2 * pairs, S::kThreads, S::kSmem, 1, s, p);   // (clusters of two: by its attribute)
+  e = launch_after(grouped_kernel<kOp, kSplit>, 2 * kSplit * clusters, S::kThreads, S::kSmem, 1, s, p);   // (clusters: by its attribute)
   prof_mark(id, s, false);
   return e;
 }
@@ -1114,7 +1177,21 @@ cudaError_t launch_grouped_mxf4(const Grouped& c, const int32_t* begin, const in
   p.nf = c.N / kTile;
   p.narrow = c.N % kTile != 0;
   p.idesc = idesc_mxf4(kTile, kMxRows);
-  return launch<kMx>(p, most_row_tiles(c, kMxRows) * (p.nf + p.narrow), kKGroupedMxf4, s);
+  // Few tiles of a long contraction: clusters of four or two pairs split it, as long as all tiles that the rows may make
+  // run at once.  (us, split : one pair a tile)  1 row 4096 x 4096 8.1 : 8.9; 64 rows 14336 x 4096 13.6 : 18.2; 2 rows
+  // of 8 groups, 14336 x 4096 13.8 : 18.0; 300 rows 14336 x 512 13.4 (two pairs 16.9) : 20.8; 16 rows 65536 x 256 20.3
+  // (34.4) : 61.5.  At 8 blocks the sums' way costs more than the blocks: 8 rows of 8 of 128 groups, 2048 x 768,
+  // 8.0 : 7.4.
+  const int64_t tiles = most_row_tiles(c, kMxRows) * (p.nf + p.narrow);
+  if ((p.depth + kMxWide - 1) / kMxWide >= kMxSplit) {
+    int fit = 0;
+    cudaError_t e = clusters_at_once<kMx, 4>(&fit);
+    if (e == cudaSuccess && tiles <= fit) return launch<kMx, 4>(p, tiles, kKGroupedMxf4, s);
+    if (e == cudaSuccess) e = clusters_at_once<kMx, 2>(&fit);
+    if (e == cudaSuccess && tiles <= fit) return launch<kMx, 2>(p, tiles, kKGroupedMxf4, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch<kMx>(p, tiles, kKGroupedMxf4, s);
 }
 
 cudaError_t launch_segments(const Tables* tabs, int G, int32_t* begin, int32_t* end, cudaStream_t s) {

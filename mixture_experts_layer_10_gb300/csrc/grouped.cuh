@@ -158,6 +158,16 @@ __device__ __forceinline__ void fence_release_smem() {
   asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
 
+// Two floats of the shared memory of CTA `rank` of the cluster, at the place of p in this one.
+__device__ __forceinline__ float2 load_peer(const float* p, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(cluster_addr(p, rank))
+               : "memory");
+  return v;
+}
+
 // Bounded wait with naps of kNap ns between polls.  kCluster acquires at cluster scope: for barriers on
 // which the peer CTA's threads arrive after writing shared memory.
 template <bool kCluster>

@@ -68,15 +68,6 @@ __device__ __forceinline__ void step(float (&d)[4], const uint4& lo, const uint4
   mma<kType>(d, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
 }
 
-__device__ __forceinline__ float2 load_peer(const float* p, uint32_t rank) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-               : "=f"(v.x), "=f"(v.y)
-               : "r"(cluster_addr(p, rank))
-               : "memory");
-  return v;
-}
-
 // NT: 8-row tiles.
 template <int kType, int NT, int kDepth, int kBlocks>
 __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) stream_kernel(const __grid_constant__ StreamParams p) {

@@ -4,7 +4,10 @@
 //
 // X is the largest value's exponent field less two, and v / X a product with a power of two, exact but where it is
 // below 2^-126 and rounds to 0 anyway; so nothing here rounds but the conversion.  Four lanes share a block, eight
-// values each; one pass over the rows, bound by HBM.
+// values each; one pass over the rows, 32 values a thread, all its loads before the first of them is used.
+//
+// Measured: 16381 rows of 2880, fp16, 18.8 us, 6.4 TB/s of reads and writes (0.95 of a copy's); 24576 rows of 2048 20.2;
+// one token's 8 rows 1.7.  (With maxima of single values and a division a vector it was bound by issue: 25.5.)
 #include <algorithm>
 
 #include "common.cuh"

@@ -164,6 +164,46 @@ def test_wide_and_long(moe, rows, K, N, G):
     run(moe, cut[:-1], cut[1:], rows, K, N, torch.bfloat16)
 
 
+@pytest.mark.parametrize("K", [512, 544, 1024, 1056, 1280, 1824, 2048, 2080, 2336, 4096, 4128, 14336])
+def test_split_contractions(moe, K):
+    """Few tiles of a contraction that pairs share: whole and broken blocks, one group, groups without rows, every
+    length of a tile's rows."""
+    run(moe, [0], [1], 1, K, 264, torch.bfloat16)
+    run(moe, [2, 9, 9, 40], [7, 9, 33, 232], 240, K, 136, torch.float16)
+    run(moe, [0, 40], [33, 500], 520, K, 520, torch.bfloat16, pad=32)
+
+
+def test_split_sums_are_the_same_every_time(moe):
+    rows, K, N = 24, 14336, 520
+    q, s, Wq, Ws = operands(moe, rows, 1, K, N)
+    cfg = moe.grouped_config(rows, K, N, 1)
+    ws = moe.grouped_workspace(cfg)
+    out = []
+    for _ in range(20):
+        y = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+        moe.moe_grouped_mm_mxf4(cfg, dev_i32([0]), dev_i32([rows]), q, s, Wq, Ws, y, ws)
+        out.append(y)
+    assert all(torch.equal(out[0], y) for y in out)
+
+
+def test_long_sums_of_one_sign(moe):
+    """Rows of one sign, 65536 columns: what the accumulator drops, at most a unit of 2^-23 of the sum at every 16
+    products and always towards zero, shows in the mean over many outputs, where the roundings to fp16
+    (half a step, 2^-11, either way) mostly cancel: 24576 of them leave at most 5 standard deviations of
+    2^-11 / sqrt(3) / sqrt(24576).  A split of the contraction drops less."""
+    for rows, N in ((192, 128), (192, 4096)):
+        K = 65536
+        x, W = (torch.rand(shape, device="cuda") + 0.25 for shape in ((rows, K), (1, N, K)))
+        (q, s), (Wq, Ws) = quantise(moe, x), quantise(moe, W / K)
+        cfg = moe.grouped_config(rows, K, N, 1, dtype=torch.float16)
+        ws = moe.grouped_workspace(cfg)
+        y = torch.empty(rows, N, dtype=torch.float16, device="cuda")
+        moe.moe_grouped_mm_mxf4(cfg, dev_i32([0]), dev_i32([rows]), q, s, Wq, Ws, y, ws)
+        vx, vw = values(q, s), values(Wq, Ws)[0]
+        off = (y.double() - vx @ vw.T) / (vx @ vw.T)
+        assert -K / 16 * 2.0 ** -23 - 9e-6 <= off.mean().item() <= 9e-6, off.mean().item()
+
+
 def test_many_groups(moe):
     n = [(i * 7) % 11 for i in range(1024)]
     begin, end, rows = layout(n)
@@ -221,7 +261,7 @@ def test_bad_groups(moe, rows):
     assert moe.moe_check_error(ws) == 0 and not bool((y == 7).all(1).any())
 
 
-@pytest.mark.parametrize("rows", [20, 600])
+@pytest.mark.parametrize("rows", [20, 600, 9000])
 def test_a_wait_that_runs_out(moe, rows):
     """One stage is never filled: the call reports it, and the next one is right."""
     K, N = 2048, 264
