@@ -40,12 +40,12 @@
 // Microscaled 4-bit values.  kind::mxf4 multiplies them and their scales as they are: a stage is the same 128 bytes of a
 // row, 256 values deep, and the tile 256 features x 192 rows, which leaves the scales 128 columns of TMEM beside two
 // accumulators.  Five stages, each with columns for its scales.  What bounds it (16384 rows, 8 groups, 4096 x
-// 14336, 365 us, 5.3 PFLOP/s): the copies alone take 295 us (15 TB/s from L2), the products alone about 265, both
-// without scales 304; the scales are 9% more traffic and one more arrival a stage to wait for.  Few rows read the
-// weights at 5.1 TB/s.  Steps on the way, same size: scales copied by tcgen05.cp 644 us; written to TMEM from registers
+// 14336, 332 us, 5.8 PFLOP/s): the copies alone take 295 us (15 TB/s from L2), the products alone about 265, both
+// without scales 304; the scales are 9% more traffic, and their way through shared memory.  Few rows read the weights at
+// 5.1 TB/s.  Steps on the way, same size: scales copied by tcgen05.cp 644 us; written to TMEM from registers
 // 525; by two teams in turn 474; one barrier a stage for operands and scales 434; one elected thread issuing 374; scales
-// a sector at a time 368.  (Tried and not kept: four stages, tiles of equal height, weights fetched to L2 ahead,
-// eight epilogue warps: 362, 367, 382, 382 us, the smaller sizes slower or the same.)
+// a sector at a time 365; no bank conflicts on their way, and two sectors at a time 332.  (Tried and not kept: four
+// stages, tiles of equal height, weights fetched to L2 ahead, eight epilogue warps, naps of 100 ns: the same or slower.)
 //
 // Measured (graph replays on inputs larger than L2; 36 launches / after three seconds of them, when the power
 // cap has lowered the clock): y of 16384 rows, 8 groups, 4096 x 14336, bf16: 1.14 / 1.19 ms, 1.69 / 1.62
@@ -85,9 +85,12 @@ constexpr int kMxWide = 128;                 // 4-bit: bytes of a row in a stage
 constexpr int kMxBlocks = 8;                 // and their scales
 constexpr int kMxHand = 128 + kMxRows;       // rows whose scales a CTA needs: its rows of the weight, the tile's
 constexpr int kMxTeams = 2;                  // of four warps, which take turns at the stages
-constexpr int kMxTurn = 4;                   // stages whose scales are brought at once (32 of a row: a sector)
-constexpr int kMxPieces = (2 * kMxHand + 128 * kMxTeams - 1) / (128 * kMxTeams);   // of 16 bytes, a thread's share of them
-constexpr uint32_t kMxScales = 2 * 32 * kMxHand;   // two hand-overs
+// Scales are brought for kTurn stages at once, 4 or 8, by half as many lanes a row, 16 bytes a lane.
+// In shared memory a stage's are 8 bytes a row, and the next stage's so much further apart that the pieces of neighbouring
+// lanes fall on all banks.
+constexpr int mx_pieces(int turn) { return (turn / 2 * kMxHand + 128 * kMxTeams - 1) / (128 * kMxTeams); }   // a thread's
+constexpr int mx_stage(int turn) { return 8 * kMxHand + 128 / turn; }
+constexpr uint32_t kMxScales = 2 * 8 * mx_stage(8);   // two hand-overs
 constexpr int kAheadMx = 2;                  // 4-bit: such times that are on their way
 constexpr int kMxSplit = 16;                 // K blocks of a tile from which two or four pairs share them
 constexpr int kMxCols = 24;                  // their TMEM columns: 2 words x (4 + 8)
@@ -422,7 +425,7 @@ __device__ __forceinline__ void umma_commit_both(uint64_t* bar, int lead) {
 // kSplit pairs of a cluster share the contraction of a tile (4-bit, few tiles): each sums its K blocks, leaves the sums in
 // its stages, which are free then, and stores a share of the rows, adding all pairs' sums in their order.  A cluster
 // has one tile.
-template <int kOp, int kSplit = 1>
+template <int kOp, int kSplit = 1, int kTurn = 4>
 __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(Shape<kOp>::kThreads, 1)
     grouped_kernel(const __grid_constant__ Params p) {
   using S = Shape<kOp>;
@@ -777,9 +780,10 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(Shape<kOp>:
     // Scales go to TMEM from registers, while the tensor cores work.  (Their copies from shared memory, tcgen05.cp, take
     // turns with the products: 56 cycles each, six a stage of 384.)  They lie there as row r in lane r % 32 of all four
     // lane quarters, column r / 32, a word for 128 values; so each of the four warps, which may write one
-    // quarter, needs every row's.  A turn is four stages: two lanes bring the 32 bytes of a row (a sector of L2: 16 at a
-    // time came twice, for 18% more traffic where the copies' traffic is the bound), and the warps hand them to each
-    // other through shared memory.
+    // quarter, needs every row's.  A turn is four or eight stages: two or four lanes bring the 32 or 64 bytes of a row
+    // (16 at a time came twice from L2, and each load of so many lines takes as many turns of the load/store unit,
+    // whose way to shared memory the copies and the products need), and the warps hand them to each other through shared
+    // memory.
     //
     // Two teams of four warps take every other stage of a turn, so that one's way through the barriers runs beside the
     // other's.  A barrier's phase must not pass a waiter by, so a team's wait for a stage's last use has to follow one
@@ -807,30 +811,32 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(Shape<kOp>:
       }
       return v;
     };
+    constexpr int kPieces = mx_pieces(kTurn), kLanes = kTurn / 2, kRowsAt = 128 * kMxTeams / kLanes, kNext = mx_stage(kTurn);
     struct Turn {
-      uint4 v[kMxPieces];
+      uint4 v[kPieces];
       int stages;
     } ring[kAheadMx];
     int kit = 0, kits = 0;
-    const uint8_t* from[kMxPieces] = {};
+    const uint8_t* from[kPieces] = {};
     auto next_turn = [&](Turn& t) {
       if (kit >= kits) {
         kit = kits = 0;
         if (walk.next(j)) {
 #pragma unroll
-          for (int i = 0; i < kMxPieces; ++i) {
-            const int row = 64 * kMxTeams * i + (r >> 1), f = j.f0 + kBM * rank + row, n = row - 128;   // (of the weight, of the tile)
-            if (row < 128) from[i] = f < p.width ? p.wx + ((int64_t)j.g * p.width + f) * p.ldx : nullptr;
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = kRowsAt * i + r / kLanes, f = j.f0 + kBM * rank + row, n = row - 128;   // (of the weight, of the tile)
+            if (row >= kMxHand) from[i] = nullptr;
+            else if (row < 128) from[i] = f < p.width ? p.wx + ((int64_t)j.g * p.width + f) * p.ldx : nullptr;
             else from[i] = n < j.n ? p.qx + ((int64_t)j.row + n) * p.ldx : nullptr;
           }
           kits = j.kits;
         }
       }
-      t.stages = min(kMxTurn, kits - kit);
+      t.stages = min(kTurn, kits - kit);
       if (t.stages <= 0) return;
 #pragma unroll
-      for (int i = 0; i < kMxPieces; ++i) t.v[i] = fetch(from[i], (j.k0 + kit) * kMxBlocks + (r & 1) * 16);
-      kit += kMxTurn;
+      for (int i = 0; i < kPieces; ++i) t.v[i] = fetch(from[i], (j.k0 + kit) * kMxBlocks + r % kLanes * 16);
+      kit += kTurn;
     };
 #pragma unroll
     for (int d = 0; d < kAheadMx; ++d) next_turn(ring[d]);
@@ -840,32 +846,34 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(Shape<kOp>:
         Turn& t = ring[d];
         if (t.stages <= 0) more = false;
         if (!more) break;
-        uint4* hand = reinterpret_cast<uint4*>(scales) + turn * (2 * kMxHand);   // [half][row]
+        uint8_t* hand = scales + turn * (kTurn * kNext);
         turn ^= 1;
 #pragma unroll
-        for (int i = 0; i < kMxPieces; ++i) {
-          const int row = 64 * kMxTeams * i + (r >> 1);
-          if (row < kMxHand) hand[(r & 1) * kMxHand + row] = t.v[i];
+        for (int i = 0; i < kPieces; ++i) {   // (two stages' 8 bytes)
+          const int row = kRowsAt * i + r / kLanes;
+          if (row >= kMxHand) continue;
+          uint8_t* to = hand + r % kLanes * 2 * kNext + row * 8;
+          *reinterpret_cast<uint2*>(to) = make_uint2(t.v[i].x, t.v[i].y);
+          *reinterpret_cast<uint2*>(to + kNext) = make_uint2(t.v[i].z, t.v[i].w);
         }
         asm volatile("bar.sync 1, %0;" ::"n"(128 * kMxTeams) : "memory");
         const int stages = t.stages;
         next_turn(t);
 #pragma unroll
-        for (int h = 0; h < kMxTurn; ++h) {
+        for (int h = 0; h < kTurn; ++h) {
           if (h >= stages) break;
           if (h % kMxTeams == team) {
-            // words of the stage: 2 (h & 1) and the next of half h / 2
-            const uint2* words = reinterpret_cast<const uint2*>(hand + (h >> 1) * kMxHand) + (h & 1);
+            const uint2* words = reinterpret_cast<const uint2*>(hand + h * kNext) + lane;
             uint32_t wa[8], wb[16] = {};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint2 v = words[2 * (32 * c + lane)];
+              const uint2 v = words[32 * c];
               wa[c] = v.x;
               wa[4 + c] = v.y;
             }
 #pragma unroll
             for (int c = 0; c < kMxRows / 32; ++c) {
-              const uint2 v = words[2 * (128 + 32 * c + lane)];
+              const uint2 v = words[128 + 32 * c];
               wb[c] = v.x;
               wb[8 + c] = v.y;
             }
@@ -1041,12 +1049,12 @@ Params params_of(const Grouped& c, const int32_t* begin, const int32_t* end, Hdr
 }
 
 // How many clusters run at once.
-template <int kOp, int kSplit = 1>
+template <int kOp, int kSplit = 1, int kTurn = 4>
 cudaError_t clusters_at_once(int* fit) {
   using S = Shape<kOp>;
   static SmemOnce once;
   static IntOnce most;
-  cudaError_t e = once.set(reinterpret_cast<const void*>(grouped_kernel<kOp, kSplit>), S::kSmem);
+  cudaError_t e = once.set(reinterpret_cast<const void*>(grouped_kernel<kOp, kSplit, kTurn>), S::kSmem);
   if (e != cudaSuccess) return e;
   return most.get(fit, [] {
     constexpr int kSize = 2 * kSplit;
@@ -1055,7 +1063,7 @@ cudaError_t clusters_at_once(int* fit) {
     cfg.blockDim = dim3(S::kThreads, 1, 1);
     cfg.dynamicSmemBytes = S::kSmem;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, grouped_kernel<kOp, kSplit>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, grouped_kernel<kOp, kSplit, kTurn>, &cfg) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
       n = num_sms() / kSize;
     }
@@ -1063,15 +1071,15 @@ cudaError_t clusters_at_once(int* fit) {
   });
 }
 
-template <int kOp, int kSplit = 1>
+template <int kOp, int kSplit = 1, int kTurn = 4>
 cudaError_t launch(const Params& p, int64_t most_tiles, int id, cudaStream_t s) {
   using S = Shape<kOp>;
   int fit = 0;
-  cudaError_t e = clusters_at_once<kOp, kSplit>(&fit);
+  cudaError_t e = clusters_at_once<kOp, kSplit, kTurn>(&fit);
   if (e != cudaSuccess) return e;
   const int64_t clusters = kSplit > 1 ? most_tiles : std::max<int64_t>(1, std::min<int64_t>(fit, most_tiles));
   prof_mark(id, s, true);
-  e = launch_after(grouped_kernel<kOp, kSplit>, 2 * kSplit * clusters, S::kThreads, S::kSmem, 1, s, p);   // (clusters: by its attribute)
+  e = launch_after(grouped_kernel<kOp, kSplit, kTurn>, 2 * kSplit * clusters, S::kThreads, S::kSmem, 1, s, p);   // (clusters: by its attribute)
   prof_mark(id, s, false);
   return e;
 }
@@ -1182,14 +1190,17 @@ cudaError_t launch_grouped_mxf4(const Grouped& c, const int32_t* begin, const in
   // of 8 groups, 14336 x 4096 13.8 : 18.0; 300 rows 14336 x 512 13.4 (two pairs 16.9) : 20.8; 16 rows 65536 x 256 20.3
   // (34.4) : 61.5.  At 8 blocks the sums' way costs more than the blocks: 8 rows of 8 of 128 groups, 2048 x 768,
   // 8.0 : 7.4.
+  // From there on scales come eight stages at a time, else four: 332 : 355 us at 16384 rows of 8 groups, 4096 x 14336, 40 :
+  // 42 at 384 rows of 64, 4096 x 1408; 23.8 : 22.2 at 384 rows of 64, 2048 x 1408.
   const int64_t tiles = most_row_tiles(c, kMxRows) * (p.nf + p.narrow);
   if ((p.depth + kMxWide - 1) / kMxWide >= kMxSplit) {
     int fit = 0;
-    cudaError_t e = clusters_at_once<kMx, 4>(&fit);
-    if (e == cudaSuccess && tiles <= fit) return launch<kMx, 4>(p, tiles, kKGroupedMxf4, s);
-    if (e == cudaSuccess) e = clusters_at_once<kMx, 2>(&fit);
-    if (e == cudaSuccess && tiles <= fit) return launch<kMx, 2>(p, tiles, kKGroupedMxf4, s);
+    cudaError_t e = clusters_at_once<kMx, 4, 8>(&fit);
+    if (e == cudaSuccess && tiles <= fit) return launch<kMx, 4, 8>(p, tiles, kKGroupedMxf4, s);
+    if (e == cudaSuccess) e = clusters_at_once<kMx, 2, 8>(&fit);
+    if (e == cudaSuccess && tiles <= fit) return launch<kMx, 2, 8>(p, tiles, kKGroupedMxf4, s);
     if (e != cudaSuccess) return e;
+    return launch<kMx, 1, 8>(p, tiles, kKGroupedMxf4, s);
   }
   return launch<kMx>(p, tiles, kKGroupedMxf4, s);
 }
