@@ -368,7 +368,7 @@ cudaError_t launch_quantize_rows_mxf4(const void* src, int dtype, int64_t rows, 
 cudaError_t launch_grouped_mxf4(const Grouped& c, const int32_t* begin, const int32_t* end, const uint8_t* q,
                                 const uint8_t* qx, const uint8_t* Wq, const uint8_t* Wx, uint16_t* y, Hdr* hdr,
                                 cudaStream_t s);
-// Expert selection from logits (select.cu)
+// Expert selection from logits (select.cuh; select_fp32.cu, and _16 for 16-bit logits select_16.cu)
 struct Select {            // validated description
   int T, E, k, n, top, sum;   // n groups of experts, of which `top` stay, scored by their `sum` largest keys
   bool sigmoid, renorm;
@@ -378,6 +378,10 @@ struct Select {            // validated description
 cudaError_t launch_select(const Select& c, const void* logits, const float* bias, int32_t* idx, float* w, cudaStream_t s);
 cudaError_t launch_select_bwd(const Select& c, const void* logits, const int32_t* idx, const float* dw, void* dl,
                               cudaStream_t s);
+cudaError_t launch_select_16(const Select& c, const void* logits, const float* bias, int32_t* idx, float* w,
+                             cudaStream_t s);
+cudaError_t launch_select_bwd_16(const Select& c, const void* logits, const int32_t* idx, const float* dw, void* dl,
+                                 cudaStream_t s);
 cudaError_t launch_segments(const Tables* tabs, int G, int32_t* begin, int32_t* end, cudaStream_t s);
 // 8-bit integer rows: codes [rows, cols] and one fp32 scale per row (amax / 127)
 cudaError_t launch_quantize_rows_i8(const uint16_t* src, bool fp16, int64_t rows, int cols, int8_t* codes,

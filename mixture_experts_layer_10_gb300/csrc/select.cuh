@@ -9,10 +9,11 @@
 // fewer experts left than that, more than 32 candidates.  The slots' weights are then formed one slot a lane, from
 // the logits themselves.
 //
-// Measured: 65536 tokens of 256 experts, k = 8, 4 of 8 groups, sigmoid, bias 51 us, 10.6 of them to read and write (91
-// with rounds, and 136 with every doubt settled for the whole token): issue of ~650 instructions a token, two thirds
-// on the ALU; 8192 of 8, k = 2, 2.4 us.  16 lanes a token of 256 experts rather than 32: 56 and 71 us when that was
-// tried.  The gradient of the first 13.4 us, 5.5 TB/s, 10.9 to read and write.
+// Measured: 65536 tokens of 256 experts, k = 8, 4 of 8 groups, sigmoid, bias, fp32 54 us, 10.6 of them to read and write
+// (91 with rounds, and 136 with every doubt settled for the whole token): issue of ~650 instructions a token, two
+// thirds on the ALU; 8192 of 8, k = 2, 2.4 us; 65536 of 256 in bf16 without groups 42 us, and with biases of 0, where
+// many keys are equal, 41.  16 lanes a token of 256 experts rather than 32: 56 and 71 us when that was tried.  The
+// gradient of the first 13.3 us, 5.5 TB/s, 10.9 to read and write.
 //
 // Which expert wins must not hang on the rounding of a score, so the order is that of the keys in 64 bits:
 //   - without a bias and without sums of keys (groups scored by two) the order of the keys is the order of the
@@ -27,6 +28,11 @@
 // with the bias by 2^-24 of itself: two keys differ wrongly by less than 2^-20.5 + 2^-23 |key|, and
 // 2^-19 max(1, |key|) is what is asked for.  A softmax's sum of at most 32 + 5 rounded additions is
 // 2^-18.7 off in one direction for all experts, so twice as much is asked for there, and for sums of two keys.
+// The kernels are built once for fp32 logits (select_fp32.cu) and once for 16-bit ones (select_16.cu), which look up which
+// of the two types they have: types looked up in one build cost 10% (51 : 57 us, gradient 4.1 : 4.6), a build
+// for each of three types most of the time to compile.
+#pragma once
+
 #include <algorithm>
 #include <cfloat>
 
@@ -37,8 +43,8 @@ namespace moe {
 
 namespace {
 
+constexpr bool kFp32 = MOE_SELECT_FP32;   // set before this file is included
 constexpr int kWarps = 4;          // of a block
-constexpr int kMaxSlots = 32;
 constexpr int kMaxExpertGroups = 64;
 
 struct SelParams {
@@ -53,6 +59,7 @@ struct SelParams {
   int n, per, top, sum;            // expert groups, experts of one, groups kept, keys summed (1 or 2)
   bool sigmoid, renorm;
   float scale;
+  int dtype;                       // of logits and dl
 };
 
 // ---- lanes of a token ----------------------------------------------------------------------------
@@ -64,10 +71,13 @@ __device__ __forceinline__ uint32_t group_mask(int lane) {
 
 template <int G>
 __device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t mask) {
-  if (G == 32) return __reduce_max_sync(0xffffffffu, v);
+  if constexpr (G == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(mask, v, o));
-  return v;
+    for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(mask, v, o));
+    return v;
+  }
 }
 
 template <int G>
@@ -96,42 +106,75 @@ __device__ __forceinline__ float value_of(uint32_t u) {
 
 // ---- logits --------------------------------------------------------------------------------------
 
-template <class T> __device__ __forceinline__ float widen1(T v);
-template <> __device__ __forceinline__ float widen1(float v) { return v; }
-template <> __device__ __forceinline__ float widen1(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> __device__ __forceinline__ float widen1(__half v) { return __half2float(v); }
-template <class T> __device__ __forceinline__ T narrow1(float v);
-template <> __device__ __forceinline__ float narrow1(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 narrow1(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half narrow1(float v) { return __float2half_rn(v); }
+__device__ __forceinline__ float logit(const SelParams& p, int64_t at) {
+  if (kFp32) return static_cast<const float*>(p.logits)[at];
+  const uint16_t v = static_cast<const uint16_t*>(p.logits)[at];
+  return p.dtype == MOE_BF16 ? bf16_lo(v) : __half2float(__ushort_as_half(v));
+}
+
+__device__ __forceinline__ uint16_t narrow16(const SelParams& p, float v) {
+  return p.dtype == MOE_BF16 ? (uint16_t)pack_bf16(v, 0.f) : __half_as_ushort(__float2half_rn(v));
+}
+
+__device__ __forceinline__ void put(const SelParams& p, int64_t at, float v) {
+  if (kFp32) static_cast<float*>(p.dl)[at] = v;
+  else static_cast<uint16_t*>(p.dl)[at] = narrow16(p, v);
+}
 
 template <class T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
 template <class T, int NV> constexpr int vec_of() { return NV * (int)sizeof(T) <= 16 ? NV : 16 / (int)sizeof(T); }
 
-// This lane's experts e0 .. e0 + NV - 1 of a row; -inf past the last.
-template <class T, int NV>
-__device__ __forceinline__ void load_row(const T* row, int e0, int E, float (&x)[NV]) {
+// This lane's experts e0 .. e0 + NV - 1 of the row at `row`; -inf past the last.  Rows start on V elements where E is
+// a multiple of V (the array on 16 bytes).
+template <class T, int NV, class F>
+__device__ __forceinline__ void load_as(const T* row, int e0, int E, float (&x)[NV], F widen) {
   constexpr int V = vec_of<T, NV>();
-  if (E % V == 0 && e0 + NV <= E) {   // rows start on V elements (the array on 16 bytes)
+  if (E % V == 0 && e0 + NV <= E) {
 #pragma unroll
     for (int i = 0; i < NV; i += V) {
       const Vec<T, V> r = *reinterpret_cast<const Vec<T, V>*>(row + e0 + i);
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[i + j] = widen1(r.v[j]);
-    }
-  } else if (E % V == 0) {
-#pragma unroll
-    for (int i = 0; i < NV; i += V) {
-      Vec<T, V> r;
-      const bool in = e0 + i < E;
-      if (in) r = *reinterpret_cast<const Vec<T, V>*>(row + e0 + i);
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[i + j] = in ? widen1(r.v[j]) : -INFINITY;
+      for (int j = 0; j < V; ++j) x[i + j] = widen(r.v[j]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = e0 + i < E ? widen1(row[e0 + i]) : -INFINITY;
+    for (int i = 0; i < NV; ++i) x[i] = e0 + i < E ? widen(row[e0 + i]) : -INFINITY;
   }
+}
+
+template <int NV>
+__device__ __forceinline__ void load_row(const SelParams& p, int64_t row, int e0, float (&x)[NV]) {
+  if constexpr (kFp32) {
+    load_as(static_cast<const float*>(p.logits) + row, e0, p.E, x, [](float v) { return v; });
+  } else {
+    uint16_t const* at = static_cast<const uint16_t*>(p.logits) + row;
+    const bool bf16 = p.dtype == MOE_BF16;
+    load_as(at, e0, p.E, x, [bf16](uint16_t v) { return bf16 ? bf16_lo(v) : __half2float(__ushort_as_half(v)); });
+  }
+}
+
+template <class T, int NV, class F>
+__device__ __forceinline__ void store_as(T* row, int e0, int E, const float (&x)[NV], F narrow) {
+  constexpr int V = vec_of<T, NV>();
+  if (E % V == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; i += V) {
+      Vec<T, V> r;
+#pragma unroll
+      for (int j = 0; j < V; ++j) r.v[j] = narrow(x[i + j]);
+      if (e0 + i < E) *reinterpret_cast<Vec<T, V>*>(row + e0 + i) = r;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (e0 + i < E) row[e0 + i] = narrow(x[i]);
+  }
+}
+
+template <int NV>
+__device__ __forceinline__ void store_row(const SelParams& p, int64_t row, int e0, const float (&x)[NV]) {
+  if constexpr (kFp32) store_as(static_cast<float*>(p.dl) + row, e0, p.E, x, [](float v) { return v; });
+  else store_as(static_cast<uint16_t*>(p.dl) + row, e0, p.E, x, [&p](float v) { return narrow16(p, v); });
 }
 
 template <int NV>
@@ -153,32 +196,14 @@ __device__ __forceinline__ void load_bias(const float* bias, int e0, int E, floa
   }
 }
 
-template <class T, int NV>
-__device__ __forceinline__ void store_row(T* row, int e0, int E, const float (&x)[NV]) {
-  constexpr int V = vec_of<T, NV>();
-  if (E % V == 0) {
-#pragma unroll
-    for (int i = 0; i < NV; i += V) {
-      Vec<T, V> r;
-#pragma unroll
-      for (int j = 0; j < V; ++j) r.v[j] = narrow1<T>(x[i + j]);
-      if (e0 + i < E) *reinterpret_cast<Vec<T, V>*>(row + e0 + i) = r;
-    }
+// A warp: n zeros of dl from `at` on, whole rows.
+__device__ __forceinline__ void fill_zero(const SelParams& p, int64_t at, int n, int lane) {
+  constexpr int size = kFp32 ? 4 : 2;
+  uint8_t* to = static_cast<uint8_t*>(p.dl) + at * size;
+  if (p.E * size % 16 == 0) {
+    for (int i = lane * 16; i < n * size; i += 512) *reinterpret_cast<uint4*>(to + i) = make_uint4(0u, 0u, 0u, 0u);
   } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (e0 + i < E) row[e0 + i] = narrow1<T>(x[i]);
-  }
-}
-
-// A warp: n zeros from `at` on, rows of E of them.
-template <class T>
-__device__ __forceinline__ void fill_zero(T* at, int n, int E, int lane) {
-  constexpr int V = 16 / (int)sizeof(T);
-  if (E % V == 0) {
-    for (int i = lane * V; i < n; i += 32 * V) *reinterpret_cast<uint4*>(at + i) = make_uint4(0u, 0u, 0u, 0u);
-  } else {
-    for (int i = lane; i < n; i += 32) at[i] = narrow1<T>(0.f);
+    for (int i = lane; i < n; i += 32) put(p, at + i, 0.f);
   }
 }
 
@@ -211,20 +236,19 @@ __device__ __forceinline__ void top2_merge(double& a, double& b, double oa, doub
 }
 
 // An expert's key in 64 bits; top and sum as of softmax64.
-template <class T>
-__device__ __noinline__ double key64(const SelParams& p, const T* row, int e, double top, double sum) {
-  const double x = fminf(widen1(row[e]), FLT_MAX);
+__device__ __noinline__ double key64(const SelParams& p, int64_t row, int e, double top, double sum) {
+  const double x = fminf(logit(p, row + e), FLT_MAX);
   const double s = p.sigmoid ? 1. / (1. + exp(-x)) : exp(x - top) / sum;
   return p.bias != nullptr ? s + (double)p.bias[e] : s;
 }
 
 // The sum of a token's exponentials, over its lanes (1 with sigmoids).
-template <class T, int G, int NV>
-__device__ __noinline__ double softmax64(const SelParams& p, const T* row, int e0, double top, uint32_t lanes) {
+template <int G, int NV>
+__device__ __noinline__ double softmax64(const SelParams& p, int64_t row, int e0, double top, uint32_t lanes) {
   if (p.sigmoid) return 1.;
   double sum = 0.;
   for (int i = 0; i < NV && e0 + i < p.E; ++i) {
-    const float x = widen1(row[e0 + i]);
+    const float x = logit(p, row + e0 + i);
     if (!masked(x)) sum += exp((double)fminf(x, FLT_MAX) - top);
   }
   for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
@@ -232,17 +256,17 @@ __device__ __noinline__ double softmax64(const SelParams& p, const T* row, int e
 }
 
 // One token by its G lanes, the slots' experts to who.
-template <class T, int G, int NV>
+template <int G, int NV>
 __device__ __noinline__ void select64(const SelParams& p, int64_t t, int lane, int* who) {
   const uint32_t mask = group_mask<G>(lane);
   const int li = lane & (G - 1), e0 = li * NV;
-  const T* row = static_cast<const T*>(p.logits) + t * p.E;
+  const int64_t row = t * p.E;
   double key[NV];
   uint32_t out = 0;   // masked experts of this lane, and taken or absent ones
   uint32_t gone = 0;
   double m = -INFINITY, z = 0.;
   for (int i = 0; i < NV; ++i) {
-    const float x = e0 + i < p.E ? widen1(row[e0 + i]) : -INFINITY;
+    const float x = e0 + i < p.E ? logit(p, row + e0 + i) : -INFINITY;
     if (e0 + i >= p.E) gone |= 1u << i;
     if (masked(x)) out |= 1u << i;
     key[i] = masked(x) ? -INFINITY : (double)fminf(x, FLT_MAX);
@@ -327,7 +351,7 @@ struct Token {
   float top[kMaxCand];                // by rank
   int who[kMaxCand];
   union {
-    double wide[kMaxCand];
+    double wide[kMaxExpertGroups];    // in 64 bits: candidates' keys, or scores
     float scores[kMaxExpertGroups];   // of groups that do not fall on lanes
   };
   __device__ __forceinline__ float& key(int e) { return keys[e + e / NV * kPad]; }
@@ -340,12 +364,12 @@ __device__ __forceinline__ bool near_by(float hi, float lo, float by) {
 
 // How many groups come before this lane's, by scores in 64 bits of the keys that may be among a group's largest.
 // `least`: the smallest key that the group's score counts.
-template <class T, int G, int NV>
-__device__ __noinline__ int groups_above64(const SelParams& p, const T* row, Token<G, NV>& token, int lane, int e0, float m,
+template <int G, int NV>
+__device__ __noinline__ int groups_above64(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, float m,
                                            float least, float tol) {
   const uint32_t mine = group_mask<G>(lane);
   const int lanes = p.per / NV, g = e0 / p.per;
-  const double total = softmax64<T, G, NV>(p, row, e0, m, mine);
+  const double total = softmax64<G, NV>(p, row, e0, m, mine);
   const float from = least - 2.f * tol * fmaxf(1.f, fabsf(least));
   double a = -INFINITY, b = -INFINITY;
   uint32_t need = 0;   // (collected first: the lanes' few then go side by side)
@@ -365,10 +389,52 @@ __device__ __noinline__ int groups_above64(const SelParams& p, const T* row, Tok
   return above;
 }
 
+// The same for groups that do not fall on lanes, a group a lane: the groups that go, a bit each, those of this lane's.
+template <int G, int NV>
+__device__ __noinline__ uint64_t groups_dropped64(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, float m,
+                                                  float tol) {
+  const uint32_t mine = group_mask<G>(lane);
+  const int li = lane & (G - 1);
+  const double total = softmax64<G, NV>(p, row, e0, m, mine);
+  __syncwarp(mine);   // (the scores in 32 bits have been read)
+  for (int g = li; g < p.n; g += G) {
+    float top = -INFINITY, least = -INFINITY;
+    for (int e = g * p.per; e < (g + 1) * p.per; ++e) {
+      const float v = token.key(e);
+      least = fmaxf(least, fminf(top, v));
+      top = fmaxf(top, v);
+    }
+    if (p.sum == 1) least = top;
+    const float from = least - 2.f * tol * fmaxf(1.f, fabsf(least));
+    double a = -INFINITY, b = -INFINITY;
+    for (int e = g * p.per; e < (g + 1) * p.per; ++e) {
+      const float v = token.key(e);
+      if (v > -INFINITY && (least == -INFINITY || v >= from || v == INFINITY))
+        top2_merge(a, b, key64(p, row, e, m, total), -INFINITY);
+    }
+    token.wide[g] = p.sum == 2 && b > -INFINITY ? a + b : a;
+  }
+  __syncwarp(mine);
+  uint64_t drop = 0;
+  for (int g = li; g < p.n; g += G) {
+    const double s = token.wide[g];
+    int above = 0;
+    for (int h = 0; h < p.n; ++h) above += h < g ? token.wide[h] >= s : token.wide[h] > s;
+    if (above >= p.top) drop |= (uint64_t)1 << g;
+  }
+  return drop;
+}
+
+// One key twice by the same logit and bias is no doubt, but a tie.
+__device__ __forceinline__ bool same_key(const SelParams& p, int64_t row, int e, int f) {
+  return logit(p, row + e) == logit(p, row + f) && (p.bias == nullptr || p.bias[e] == p.bias[f]);
+}
+
 // The slots' experts by k rounds of a maximum over the lanes (a whole warp).  Returns whether two keys that follow each
 // other are too near.
 template <int G, int NV, bool kKeys>
-__device__ __noinline__ bool select_rounds(const SelParams& p, Token<G, NV>& token, int lane, uint32_t allowed, float tol) {
+__device__ __noinline__ bool select_rounds(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, uint32_t allowed,
+                                           float tol) {
   const int li = lane & (G - 1), e0 = li * NV;
   const uint32_t mine = group_mask<G>(lane);
   uint32_t u[NV];
@@ -377,37 +443,40 @@ __device__ __noinline__ bool select_rounds(const SelParams& p, Token<G, NV>& tok
     const float v = token.key(e0 + i);
     u[i] = (allowed >> i & 1u) == 0 ? kTaken : (v > -INFINITY ? order_of(v) : kMasked);
   }
-  uint32_t before = kTaken;   // the key of the slot before
+  uint32_t before = kTaken;   // the key and the expert of the slot before
+  int expert = 0;
   bool doubt = false;
   for (int r = 0; r < p.k + (int)kKeys; ++r) {   // (one more than the slots, for the border)
     uint32_t best = u[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) best = max(best, u[i]);
     const uint32_t v = group_max<G>(best, 0xffffffffu);
-    if (kKeys && r > 0 && v > kMasked) doubt |= near_by(value_of(before), value_of(v), tol);
-    before = v;
-    if (r == p.k) break;
     const int owner = __ffs(__ballot_sync(0xffffffffu, best == v) & mine) - 1;
     int il = 0;
 #pragma unroll
     for (int i = NV - 1; i >= 0; --i)
       if (u[i] == v) il = i;
+    const int e = __shfl_sync(0xffffffffu, e0 + il, owner);
+    if (kKeys && r > 0 && v > kMasked && near_by(value_of(before), value_of(v), tol)) doubt |= !same_key(p, row, expert, e);
+    before = v;
+    expert = e;
+    if (r == p.k) break;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (lane == owner && i == il) u[i] = kTaken;
-    if (lane == owner) token.who[r] = e0 + il;
+    if (lane == owner) token.who[r] = e;
   }
   return doubt;
 }
 
 // The order of a token's candidates by keys in 64 bits: whoever may be among the k is one.
-template <class T, int G, int NV>
-__device__ __noinline__ void rank64(const SelParams& p, const T* row, Token<G, NV>& token, int lane, int e0, float m,
+template <int G, int NV>
+__device__ __noinline__ void rank64(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, float m,
                                     int count) {
   constexpr int kSlots = 32 / G;
   const int li = lane & (G - 1);
   const uint32_t mine = group_mask<G>(lane);
-  const double total = softmax64<T, G, NV>(p, row, e0, m, mine);
+  const double total = softmax64<G, NV>(p, row, e0, m, mine);
   for (int c = li; c < count; c += G) token.wide[c] = key64(p, row, token.e[c], m, total);
   __syncwarp(mine);
   int rank[kSlots];
@@ -453,7 +522,7 @@ __device__ __forceinline__ float sort_pairs(float a, float b, int li) {
 }
 
 // kKeys: keys are scores (with a bias, or summed), else logits.
-template <class T, int G, int NV, bool kKeys>
+template <int G, int NV, bool kKeys>
 __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(const __grid_constant__ SelParams p) {
   constexpr int kTok = 32 / G;       // tokens of a warp
   constexpr int kSlots = 32 / G;     // slots of a lane, and candidates
@@ -464,12 +533,12 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
   const uint32_t mine = group_mask<G>(lane);
   const int64_t at = ((int64_t)blockIdx.x * kWarps + warp) * kTok + lane / G;
   const int64_t t = min(at, p.T - 1);   // (lanes past the last token do its work again and store nothing)
-  const T* row = static_cast<const T*>(p.logits) + t * p.E;
+  const int64_t row = t * p.E;
   Token<G, NV>& token = shared[warp][lane / G];
   after_previous_kernel();
 
   float key[NV];   // the logits, then the keys: -inf for masked experts
-  load_row<T, NV>(row, e0, p.E, key);
+  load_row<NV>(p, row, e0, key);
   const bool softmax_all = !p.sigmoid && (kKeys || !p.renorm);
   float m = -FLT_MAX, z = 0.f, rz = 0.f;
   bool broken = false;   // a NaN or +inf: the selection goes by the rest, or as if it were the largest number
@@ -507,7 +576,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
       if (masked(key[i])) key[i] = -INFINITY;   // (NaN)
   }
 
-  bool border = false, doubt = false;   // the same in all lanes of a token
+  bool doubt = false;   // the same in all lanes of a token
   const float tol = p.sigmoid ? 0x1p-19f : 0x1p-18f;
   if (NV % 4 == 0) {
 #pragma unroll
@@ -544,7 +613,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         const uint32_t last = __ballot_sync(mask, e0 < p.E && above == p.top - 1) & mine;
         const uint32_t next = __ballot_sync(mask, e0 < p.E && above == p.top) & mine;
         const float sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
-        if (near_by(sl, sn, 2.f * tol)) above = groups_above64<T, G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol);
+        if (near_by(sl, sn, 2.f * tol)) above = groups_above64<G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol);
         __syncwarp();
       }
       if (above >= p.top) {
@@ -566,7 +635,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
       }
       __syncwarp();
       float lo = INFINITY, hi = -INFINITY;   // the lowest score kept, the highest dropped
-      uint32_t drop[2] = {0u, 0u};
+      uint64_t drop = 0;
       for (int g = li; g < p.n; g += G) {
         const float s = token.scores[g];
         int above = 0;
@@ -575,19 +644,21 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
           lo = fminf(lo, s);
         } else {
           hi = fmaxf(hi, s);
-          drop[g >> 5] |= 1u << (g & 31);
+          drop |= (uint64_t)1 << g;
         }
       }
-#pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) {
-        drop[0] |= __shfl_xor_sync(mask, drop[0], o);
-        drop[1] |= __shfl_xor_sync(mask, drop[1], o);
+      if (kKeys) {
+        lo = -group_fmax<G>(-lo, mask);
+        hi = group_fmax<G>(hi, mask);
+        if (near_by(lo, hi, 2.f * tol)) drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol);
+        __syncwarp();
       }
-      if (kKeys) border = near_by(-group_fmax<G>(-lo, mask), group_fmax<G>(hi, mask), 2.f * tol);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) drop |= __shfl_xor_sync(mask, drop, o);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int g = min((e0 + i) / p.per, p.n - 1);
-        if ((drop[g >> 5] >> (g & 31) & 1u) != 0) {
+        if ((drop >> g & 1u) != 0) {
           allowed &= ~(1u << i);
           key[i] = -INFINITY;   // (masked ones of the groups that stay: only the rounds below choose them)
         }
@@ -656,20 +727,37 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) {
           const int j = q * G + li;
-          // (there are more than k candidates; one key twice by the same logit and bias is no doubt, but a tie)
-          if (j < p.k && near_by(token.top[j], token.top[j + 1], tol)) {
-            const int e = token.who[j], f = token.who[j + 1];
-            doubt |= !(widen1(row[e]) == widen1(row[f]) && (p.bias == nullptr || p.bias[e] == p.bias[f]));
-          }
+          // (there are more than k candidates)
+          if (j < p.k && near_by(token.top[j], token.top[j + 1], tol))
+            doubt |= !same_key(p, row, token.who[j], token.who[j + 1]);
         }
         doubt = (__ballot_sync(mask, doubt) & mine) != 0;
       }
     }
   }
-  if (rounds) doubt = select_rounds<G, NV, kKeys>(p, token, lane, allowed, tol);
-  if (kKeys) {
-    if (border || (doubt && rounds)) select64<T, G, NV>(p, t, lane, token.who);
-    else if (doubt) rank64<T, G, NV>(p, row, token, lane, e0, m, count);
+  if (rounds) {
+    doubt = select_rounds<G, NV, kKeys>(p, row, token, lane, allowed, tol);
+    if (kKeys) {   // its candidates are all experts that are left, if these are not too many
+      uint32_t bits = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) bits |= key[i] > -INFINITY ? 1u << i : 0u;
+      int upto = __popc(bits);
+      int to = -upto;
+#pragma unroll
+      for (int o = 1; o < G; o <<= 1) {
+        const int v = __shfl_up_sync(mask, upto, o, G);
+        if (li >= o) upto += v;
+      }
+      to += upto;
+      count = __shfl_sync(mask, upto, G - 1, G);
+      if (doubt && count <= kMaxCand)
+        for (; bits != 0; bits &= bits - 1) token.e[to++] = e0 + __ffs(bits) - 1;
+      __syncwarp();
+    }
+  }
+  if (kKeys && doubt) {
+    if (count > kMaxCand) select64<G, NV>(p, t, lane, token.who);
+    else rank64<G, NV>(p, row, token, lane, e0, m, count);
   }
   __syncwarp();
   int sidx[kSlots];
@@ -681,7 +769,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
     const bool slot = q * G + li < p.k;
-    xs[q] = slot ? widen1(row[sidx[q]]) : -INFINITY;
+    xs[q] = slot ? logit(p, row + sidx[q]) : -INFINITY;
     M = fmaxf(M, xs[q]);
   }
   if (broken) rz = __int_as_float(0x7fffffff);
@@ -729,15 +817,14 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
 // renormalised reads a whole row, and has lanes enough for it; else the slots alone say how many lanes a token
 // has (16 for 8 slots: 22 us).  An expert in several slots gets the sum of their terms, in slot order, from
 // the first of them.
-template <class T, int G, int NV, bool kDense>
+template <int G, int NV, bool kDense>
 __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_kernel(const __grid_constant__ SelParams p) {
   constexpr int kTok = 32 / G, kSlots = kDense ? 32 / G : 1;   // (sparse: k is at most G)
   constexpr uint32_t mask = 0xffffffffu;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & (G - 1), e0 = li * NV;
   const int64_t at = ((int64_t)blockIdx.x * kWarps + warp) * kTok + lane / G;
   const int64_t t = min(at, p.T - 1);
-  const T* row = static_cast<const T*>(p.logits) + t * p.E;
-  T* out = static_cast<T*>(p.dl) + t * p.E;
+  const int64_t row = t * p.E;
   after_previous_kernel();
 
   int e[kSlots];
@@ -756,7 +843,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
   }
   float v[NV], m = -FLT_MAX, rz = 0.f;
   if constexpr (kDense) {
-    load_row<T, NV>(row, e0, p.E, v);
+    load_row<NV>(p, row, e0, v);
 #pragma unroll
     for (int i = 0; i < NV; ++i) m = fmaxf(m, v[i]);
     m = group_fmax<G>(m, mask);
@@ -770,11 +857,11 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
     rz = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
   } else {   // zeros, of all the warp's tokens, which lie on end
     const int64_t first = at - lane / G;
-    if (first < p.T) fill_zero(static_cast<T*>(p.dl) + first * p.E, (int)min((int64_t)kTok, p.T - first) * p.E, p.E, lane);
+    if (first < p.T) fill_zero(p, first * p.E, (int)min((int64_t)kTok, p.T - first) * p.E, lane);
   }
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
-    xs[q] = e[q] >= 0 ? widen1(row[e[q]]) : -INFINITY;
+    xs[q] = e[q] >= 0 ? logit(p, row + e[q]) : -INFINITY;
     if (xs[q] == -INFINITY) c[q] = 0.f;   // (whatever the gradient of a weight that is nothing)
     M = fmaxf(M, xs[q]);
   }
@@ -842,13 +929,13 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
   if constexpr (kDense) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] *= -rz * (p.scale * dot);
-    if (at < p.T) store_row<T, NV>(out, e0, p.E, v);
+    if (at < p.T) store_row<NV>(p, row, e0, v);
   }
   __syncwarp();
   if (at >= p.T) return;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q)
-    if (first[q]) out[e[q]] = narrow1<T>(kDense ? d[q] - h[q] * (p.scale * dot) : d[q]);
+    if (first[q]) put(p, row + e[q], kDense ? d[q] - h[q] * (p.scale * dot) : d[q]);
 }
 
 // ---- host side -----------------------------------------------------------------------------------
@@ -865,27 +952,31 @@ SelParams params_of(const Select& c) {
   p.sigmoid = c.sigmoid;
   p.renorm = c.renorm;
   p.scale = c.scale;
+  p.dtype = c.dtype;
   return p;
 }
 
-// A functor's call<T, G, NV>() for the type of the logits and the number of experts.
-template <class T, class F>
-cudaError_t by_experts(int E, F f) {
-  if (E <= 8) return f.template call<T, 8, 1>();
-  if (E <= 16) return f.template call<T, 8, 2>();
-  if (E <= 32) return f.template call<T, 8, 4>();
-  if (E <= 64) return f.template call<T, 16, 4>();
-  if (E <= 128) return f.template call<T, 16, 8>();
-  if (E <= 256) return f.template call<T, 16, 16>();
-  if (E <= 512) return f.template call<T, 32, 16>();
-  return f.template call<T, 32, 32>();
-}
-
+// A functor's call<G, NV>() for the number of experts, and lanes enough for more than `k` candidates' bounds.
 template <class F>
-cudaError_t by_type(const Select& c, F f) {
-  if (c.dtype == MOE_BF16) return by_experts<__nv_bfloat16>(c.E, f);
-  if (c.dtype == MOE_FP16) return by_experts<__half>(c.E, f);
-  return by_experts<float>(c.E, f);
+cudaError_t by_experts(int E, int k, F f) {
+  if (k < 8) {
+    if (E <= 8) return f.template call<8, 1>();
+    if (E <= 16) return f.template call<8, 2>();
+    if (E <= 32) return f.template call<8, 4>();
+  }
+  if (k < 16) {
+    if (E <= 16) return f.template call<16, 1>();
+    if (E <= 32) return f.template call<16, 2>();
+    if (E <= 64) return f.template call<16, 4>();
+    if (E <= 128) return f.template call<16, 8>();
+    if (E <= 256) return f.template call<16, 16>();
+  }
+  if (E <= 32) return f.template call<32, 1>();
+  if (E <= 64) return f.template call<32, 2>();
+  if (E <= 128) return f.template call<32, 4>();
+  if (E <= 256) return f.template call<32, 8>();
+  if (E <= 512) return f.template call<32, 16>();
+  return f.template call<32, 32>();
 }
 
 int64_t blocks_of(int64_t T, int per_warp) { return (T + kWarps * per_warp - 1) / (kWarps * per_warp); }
@@ -893,32 +984,30 @@ int64_t blocks_of(int64_t T, int per_warp) { return (T + kWarps * per_warp - 1) 
 struct Forward {
   const SelParams& p;
   cudaStream_t s;
-  template <class T, int G, int NV>
+  template <int G, int NV>
   cudaError_t call() const {
     const bool keys = p.bias != nullptr || (p.top < p.n && p.sum == 2);
     const int64_t blocks = blocks_of(p.T, 32 / G);
-    return keys ? launch_after(select_kernel<T, G, NV, true>, blocks, 32 * kWarps, 0, 1, s, p)
-                : launch_after(select_kernel<T, G, NV, false>, blocks, 32 * kWarps, 0, 1, s, p);
+    return keys ? launch_after(select_kernel<G, NV, true>, blocks, 32 * kWarps, 0, 1, s, p)
+                : launch_after(select_kernel<G, NV, false>, blocks, 32 * kWarps, 0, 1, s, p);
   }
 };
 
 struct Backward {
   const SelParams& p;
   cudaStream_t s;
-  template <class T, int G, int NV>
+  template <int G, int NV>
   cudaError_t call() const {
-    if (!p.sigmoid && !p.renorm) return launch<T, G, NV, true>();
-    return p.k <= 8 ? launch<T, 8, 1, false>() : p.k <= 16 ? launch<T, 16, 1, false>() : launch<T, 32, 1, false>();
+    if (!p.sigmoid && !p.renorm) return launch<G, NV, true>();
+    return p.k <= 8 ? launch<8, 1, false>() : p.k <= 16 ? launch<16, 1, false>() : launch<32, 1, false>();
   }
-  template <class T, int G, int NV, bool kDense>
+  template <int G, int NV, bool kDense>
   cudaError_t launch() const {
-    return launch_after(select_bwd_kernel<T, G, NV, kDense>, blocks_of(p.T, 32 / G), 32 * kWarps, 0, 1, s, p);
+    return launch_after(select_bwd_kernel<G, NV, kDense>, blocks_of(p.T, 32 / G), 32 * kWarps, 0, 1, s, p);
   }
 };
 
-}  // namespace
-
-cudaError_t launch_select(const Select& c, const void* logits, const float* bias, int32_t* idx, float* w,
+cudaError_t forward(const Select& c, const void* logits, const float* bias, int32_t* idx, float* w,
                           cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
   SelParams p = params_of(c);
@@ -927,12 +1016,12 @@ cudaError_t launch_select(const Select& c, const void* logits, const float* bias
   p.idx = idx;
   p.w = w;
   prof_mark(kKSelect, s, true);
-  const cudaError_t e = by_type(c, Forward{p, s});
+  const cudaError_t e = by_experts(c.E, c.k, Forward{p, s});
   prof_mark(kKSelect, s, false);
   return e;
 }
 
-cudaError_t launch_select_bwd(const Select& c, const void* logits, const int32_t* idx, const float* dw, void* dl,
+cudaError_t backward(const Select& c, const void* logits, const int32_t* idx, const float* dw, void* dl,
                               cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
   SelParams p = params_of(c);
@@ -941,9 +1030,11 @@ cudaError_t launch_select_bwd(const Select& c, const void* logits, const int32_t
   p.dw = dw;
   p.dl = dl;
   prof_mark(kKSelectBwd, s, true);
-  const cudaError_t e = by_type(c, Backward{p, s});
+  const cudaError_t e = by_experts(c.E, c.k, Backward{p, s});
   prof_mark(kKSelectBwd, s, false);
   return e;
 }
+
+}  // namespace
 
 }  // namespace moe

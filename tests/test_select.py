@@ -165,9 +165,13 @@ def test_masks(moe, score, dtype, groups):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,groups", [(8, dict()), (64, dict(groups=8, top=4, group_top=2)), (256, dict(groups=8, top=4, group_top=2)),
-                                      (120, dict(groups=5, top=2, group_top=2))])
-def test_ties_and_near_ties(moe, score, E, groups):
-    T, k = 200, 4
+                                      (120, dict(groups=5, top=2, group_top=2)), (32, dict(groups=16, top=11, group_top=2)),
+                                      (25, dict(groups=5, top=1, group_top=2)), (96, dict())])
+@pytest.mark.parametrize("k", [4, 13, 20])
+def test_ties_and_near_ties(moe, score, E, groups, k):
+    T = 200
+    if k > E // groups.get("groups", 1) * groups.get("top", 1):
+        pytest.skip("more slots than experts of the groups that stay")
     l = (rand((T, E), 3) * 2).round() / 4                       # equal logits in every row
     check(moe, l, None, k, score, renorm=1, **groups)
     check(moe, l, torch.zeros(E, device="cuda"), k, score, renorm=1, **groups)
