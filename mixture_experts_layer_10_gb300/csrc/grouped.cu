@@ -107,6 +107,7 @@ struct Shape {
   static constexpr int kThreads = 32 * (2 + kEpiWarps + kExtra);
   static constexpr size_t kSmem = 1024 + (size_t)(kStages + kRaw) * 2 * kHalf + kScales + 512 + sizeof(GroupTab);
   static_assert(kSmem <= 232448, "shared memory per block");
+  static_assert(kOp != kMx || 2 * kRows + kStages * kMxCols <= kTmemCols, "TMEM columns");
 };
 
 struct Params {

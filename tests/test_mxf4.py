@@ -359,3 +359,72 @@ def test_serving_chain(moe):
     rows64 = o.double()[at] * w.double()[..., None]
     ref, mass = rows64.sum(1), rows64.abs().sum(1)
     assert bool(((y.double() - ref).abs() <= 2.0 ** -8 * ref.abs() * 1.001 + 8 * 2.0 ** -24 * mass).all())
+
+
+def test_profiler_counts_the_kernels(moe):
+    rows, K, N, G = 64, 256, 64, 2
+    x = rand((rows, K), torch.bfloat16, 1)
+    l = rand((rows, 16), torch.float32, 2)
+    cfg, mc = moe.grouped_config(rows, K, N, G), moe.config(rows, K, 64, 16, 2)
+    ws, ws_layer = moe.grouped_workspace(cfg), moe.Buffers.allocate(mc).ws
+    sel = moe.select_config(rows, 16, 2, "sigmoid")
+    idx, w = torch.empty(rows, 2, dtype=torch.int32, device="cuda"), torch.empty(rows, 2, device="cuda")
+    q, s, Wq, Ws = operands(moe, rows, G, K, N)
+    moe.moe_profile_enable(True)
+    moe.moe_select(sel, l, None, idx, w)
+    moe.moe_select_bwd(sel, l, idx, w, torch.empty_like(l))
+    moe.moe_router_wgrad(mc, x, l, torch.empty(K, 16, device="cuda"), None, ws_layer)
+    quantise(moe, x)
+    moe.moe_grouped_mm_mxf4(cfg, dev_i32([0, 20]), dev_i32([20, rows]), q, s, Wq, Ws, torch.empty(rows, N, dtype=torch.bfloat16, device="cuda"), ws)
+    ran = {n: c for n, (ms, c) in moe.moe_profile_read().items() if c}
+    moe.moe_profile_enable(False)
+    assert ran == {"select": 1, "select_bwd": 1, "router_dlogits_rows": 1, "router_dwr": 1, "router_reduce": 1, "quantize_mxf4": 1,
+                   "grouped_mm_mxf4": 1}
+
+
+def test_offsets_past_32_bits(moe):
+    """Codes, scales' rows, weights and outputs behind the 2^32nd byte: the same bits as of those rows by themselves."""
+    n, K, N = 300, 8192, 72
+    rows = (1 << 20) + n                         # 4.3 GB of codes
+    head = rand((n, K), torch.bfloat16, 1)
+    q, s = quantise(moe, head)
+    W = rand((2, N, K), torch.bfloat16, 2)
+    Wq, Ws = quantise(moe, W)
+    codes = torch.zeros(rows, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(rows, stride(K), dtype=torch.uint8, device="cuda")
+    codes[-n:], scales[-n:] = q, s
+    wide = 4096                                  # y rows far apart: 8.6 GB
+    y = torch.full((rows, wide), 7.0, dtype=torch.bfloat16, device="cuda")
+    cfg = moe.grouped_config(rows, K, N, 2, out_stride=wide)
+    ws = moe.grouped_workspace(cfg)
+    moe.moe_grouped_mm_mxf4(cfg, dev_i32([rows - n, rows - 9]), dev_i32([rows - 9, rows]), codes, scales, Wq, Ws, y[:, :N], ws)
+    assert moe.moe_check_error(ws) == 0
+    ref, S = exact([0, n - 9], [n - 9, n], values(q, s), values(Wq, Ws))
+    check("y", y[-n:, :N], ref, S, K)
+    assert bool((y[: rows - n] == 7).all()) and bool((y[-n:, N:] == 7).all())
+    del codes, scales, y
+    G = 1024                                     # 4.8 GB of weights
+    big = torch.zeros(G, 2304, 2048, dtype=torch.uint8, device="cuda")
+    bs = torch.zeros(G, 2304, stride(4096), dtype=torch.uint8, device="cuda")
+    W = rand((1, 2304, 4096), torch.bfloat16, 3)
+    big[-1:], bs[-1:] = quantise(moe, W)
+    x = rand((40, 4096), torch.bfloat16, 4)
+    q, s = quantise(moe, x)
+    cfg = moe.grouped_config(40, 4096, 2304, G)
+    ws = moe.grouped_workspace(cfg)
+    y = torch.empty(40, 2304, dtype=torch.bfloat16, device="cuda")
+    cut = [0] * G + [40]
+    moe.moe_grouped_mm_mxf4(cfg, dev_i32(cut[:-1]), dev_i32(cut[1:]), q, s, big, bs, y, ws)
+    assert moe.moe_check_error(ws) == 0
+    ref, S = exact([0], [40], values(q, s), values(big[-1:], bs[-1:]))
+    check("y", y, ref, S, 4096)
+
+
+def test_quantiser_past_32_bits(moe):
+    rows, cols, n = (1 << 22) + 37, 544, 500     # 4.6 GB
+    v = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    v[-n:] = rand((n, cols), torch.bfloat16, 1)
+    codes, scales = quantise(moe, v)
+    q, s = quantise(moe, v[-n:].clone())
+    assert torch.equal(codes[-n:], q) and torch.equal(scales[-n:], s)
+    assert not bool(codes[: rows - n].any()) and not bool(scales[: rows - n].any())

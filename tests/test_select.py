@@ -338,6 +338,26 @@ def test_captured_and_on_streams(moe):
     assert torch.equal(idx[0], idx[1]) and torch.equal(w[0], w[1]) and torch.equal(dl, eager)
 
 
+@pytest.mark.parametrize("dtype,E", [("fp16", 300), ("fp32", 256)])
+def test_offsets_past_32_bits(moe, dtype, E):
+    """Tokens behind the 2^32nd byte of the logits: the same bits as of those tokens by themselves."""
+    T, n, k = (1 << 32) // (E * (2 if dtype == "fp16" else 4)) + 1000, 500, 5
+    l = torch.zeros(T, E, dtype=TYPES[dtype], device="cuda")
+    l[-n:] = rand((n, E), 1).to(l.dtype)
+    b, c = rand((E,), 2, 0.1), torch.zeros(T, k, device="cuda")
+    c[-n:] = rand((n, k), 3, 1.0)
+    for renorm in (0, 1):
+        out = []
+        for a, d in ((l, c), (l[-n:].clone(), c[-n:].clone())):
+            cfg = moe.select_config(len(a), E, k, renorm=renorm, dtype=l.dtype)
+            idx, w = torch.empty(len(a), k, dtype=torch.int32, device="cuda"), torch.empty(len(a), k, device="cuda")
+            dl = torch.empty_like(a)
+            moe.moe_select(cfg, a, b, idx, w)
+            moe.moe_select_bwd(cfg, a, idx, d, dl)
+            out.append([t[-n:] for t in (idx, w, dl)])
+        assert all(torch.equal(p, q) for p, q in zip(*out))
+
+
 @pytest.mark.parametrize("T,E,d", [(1, 8, 64), (33, 8, 128), (1000, 40, 192), (513, 64, 64), (2049, 128, 256), (300, 200, 64),
                                    (70, 256, 128)])
 def test_router_wgrad(moe, T, E, d):
