@@ -223,6 +223,10 @@ __device__ __forceinline__ float rcp_fast(float v) {   // of 1 and more
 }
 
 __device__ __forceinline__ float sigmoid32(float x) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
+// A sigmoid over e^low, low the smaller of 0 and the largest x of a sum: ratios that do not underflow with the sigmoids.
+__device__ __forceinline__ float sigmoid_over(float x, float low) {
+  return x >= 0.f ? sigmoid32(x) : __fdiv_rn(expf(x - low), 1.f + expf(x));
+}
 
 // ---- the same in 64 bits, for a token whose order is in doubt ---------------------------------------
 
@@ -457,7 +461,9 @@ __device__ __noinline__ bool select_rounds(const SelParams& p, int64_t row, Toke
     for (int i = NV - 1; i >= 0; --i)
       if (u[i] == v) il = i;
     const int e = __shfl_sync(0xffffffffu, e0 + il, owner);
-    if (kKeys && r > 0 && v > kMasked && near_by(value_of(before), value_of(v), tol)) doubt |= !same_key(p, row, expert, e);
+    // (at the border more keys may follow that are near: no looking further here)
+    if (kKeys && r > 0 && v > kMasked && near_by(value_of(before), value_of(v), tol))
+      doubt |= r == p.k || !same_key(p, row, expert, e);
     before = v;
     expert = e;
     if (r == p.k) break;
@@ -724,14 +730,19 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         }
       __syncwarp();
       if (kKeys) {
+        // from the first key to the first one, from the k-th on, that is far enough from the next: two that are near and not
+        // the same may stand the other way round, if only by what lies between them
+        uint32_t near = 0, unlike = 0;   // a bit a key, against the next (there are more than k)
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) {
           const int j = q * G + li;
-          // (there are more than k candidates)
-          if (j < p.k && near_by(token.top[j], token.top[j + 1], tol))
-            doubt |= !same_key(p, row, token.who[j], token.who[j + 1]);
+          const bool close = j + 1 < count && near_by(token.top[j], token.top[j + 1], tol);
+          const bool other = close && !same_key(p, row, token.who[j], token.who[j + 1]);
+          near |= (__ballot_sync(mask, close) & mine) >> (lane - li) << (q * G & 31);
+          unlike |= (__ballot_sync(mask, other) & mine) >> (lane - li) << (q * G & 31);
         }
-        doubt = (__ballot_sync(mask, doubt) & mine) != 0;
+        const int last = __ffs(~(near >> (p.k - 1))) + p.k - 2;   // (the last candidate's bit is 0)
+        doubt = (unlike & ((2u << last) - 1u)) != 0;
       }
     }
   }
@@ -780,13 +791,9 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
     s[q] = 0.f;
     if (q * G >= p.k) continue;
     const bool slot = q * G + li < p.k;
-    if (!p.renorm) {
-      s[q] = p.sigmoid ? sigmoid32(xs[q]) : expf(xs[q] - m) * rz;
-    } else if (p.sigmoid && M >= -40.f) {
-      s[q] = sigmoid32(xs[q]);
-    } else {   // (a sigmoid below e^-40 is the exponential to 2^-57)
-      s[q] = M == -INFINITY ? (xs[q] == -INFINITY ? 0.f : xs[q]) : expf(xs[q] - M);
-    }
+    if (!p.renorm) s[q] = p.sigmoid ? sigmoid32(xs[q]) : expf(xs[q] - m) * rz;
+    else if (M == -INFINITY) s[q] = xs[q] == -INFINITY ? 0.f : xs[q];   // (0 or NaN)
+    else s[q] = p.sigmoid ? sigmoid_over(xs[q], fminf(M, 0.f)) : expf(xs[q] - M);
     if (!slot) s[q] = 0.f;
     sum += s[q];
   }
@@ -872,8 +879,9 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 12 : 6) select_bwd_ker
     h[q] = 0.f;
     if (q * G >= p.k) continue;
     if (kDense) h[q] = __expf(xs[q] - m) * rz;
-    else if (p.sigmoid && !(p.renorm && M < -40.f)) h[q] = sigmoid32(xs[q]);
-    else h[q] = M == -INFINITY ? 0.f : expf(xs[q] - M);
+    else if (!p.renorm) h[q] = sigmoid32(xs[q]);
+    else if (M == -INFINITY) h[q] = 0.f;
+    else h[q] = p.sigmoid ? sigmoid_over(xs[q], fminf(M, 0.f)) : expf(xs[q] - M);
     if (e[q] < 0) h[q] = 0.f;
     sum += h[q];
   }

@@ -183,6 +183,12 @@ def test_ties_and_near_ties(moe, score, E, groups, k):
     l[1:] = l[0] + rand((T - 1, E), 5, 1e-6)
     p = scores64(l, score)[0]
     check(moe, l, (p.max() - p).float(), k, score, renorm=1, **groups)
+    # most logits equal and a few the least bit above them, at either end of the experts
+    l = torch.zeros(T, E, device="cuda")
+    l.scatter_(1, torch.randint(0, E, (T, 3), device="cuda", generator=torch.Generator("cuda").manual_seed(6)), 2.0 ** -24)
+    check(moe, l, torch.zeros(E, device="cuda"), k, score, renorm=1)
+    l[:, : E // 2] -= 1.0
+    check(moe, l, torch.zeros(E, device="cuda"), k, score, renorm=1)
     # scores far below the bias's last place: the order is the bias's, then theirs
     check(moe, l - 40, torch.ones(E, device="cuda"), k, score, renorm=1, **groups)
 
@@ -214,6 +220,16 @@ def test_far_logits(moe):
         for score in ("softmax", "sigmoid"):
             check(moe, l, None, 5, score, renorm=1, scale=16.0)
             check(moe, l, None, 5, score)
+
+
+def test_wide_logits(moe):
+    """Scores of one token that lie many powers of ten apart, some of them below the smallest number of 32 bits."""
+    for shift in (-60.0, -20.0, 0.0, 40.0):
+        l = rand((300, 24), 11, 40.0) + shift
+        for renorm in (0, 1):
+            for k in (3, 12):
+                check(moe, l, None, k, "sigmoid", renorm=renorm, scale=1.5)
+                check(moe, l, None, k, "softmax", renorm=renorm, scale=1.5)
 
 
 def test_nan_and_infinite_logits(moe):
