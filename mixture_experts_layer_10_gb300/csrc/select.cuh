@@ -366,6 +366,24 @@ __device__ __forceinline__ bool near_by(float hi, float lo, float by) {
   return hi < INFINITY && hi - lo <= by * fmaxf(1.f, fabsf(hi));
 }
 
+// Whether all of a token's experts that are not masked have one logit and one bias (a token of zeros, a router that has
+// learned nothing): all its keys are one number then, whatever its bits, and sums of as many of them are.
+template <int G, int NV>
+__device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0) {
+  const uint32_t mine = group_mask<G>(lane);
+  float lo = INFINITY, hi = -INFINITY, blo = INFINITY, bhi = -INFINITY;
+  for (int i = 0; i < NV && e0 + i < p.E; ++i) {
+    if (!(token.key(e0 + i) > -INFINITY)) continue;
+    const float x = logit(p, row + e0 + i), b = p.bias != nullptr ? p.bias[e0 + i] : 0.f;
+    lo = fminf(lo, x);
+    hi = fmaxf(hi, x);
+    blo = fminf(blo, b);
+    bhi = fmaxf(bhi, b);
+  }
+  __syncwarp(mine);
+  return -group_fmax<G>(-lo, mine) == group_fmax<G>(hi, mine) && -group_fmax<G>(-blo, mine) == group_fmax<G>(bhi, mine);
+}
+
 // How many groups come before this lane's, by scores in 64 bits of the keys that may be among a group's largest.
 // `least`: the smallest key that the group's score counts.
 template <int G, int NV>
@@ -461,9 +479,19 @@ __device__ __noinline__ bool select_rounds(const SelParams& p, int64_t row, Toke
     for (int i = NV - 1; i >= 0; --i)
       if (u[i] == v) il = i;
     const int e = __shfl_sync(0xffffffffu, e0 + il, owner);
-    // (at the border more keys may follow that are near: no looking further here)
-    if (kKeys && r > 0 && v > kMasked && near_by(value_of(before), value_of(v), tol))
-      doubt |= r == p.k || !same_key(p, row, expert, e);
+    if (kKeys && r > 0 && v > kMasked && near_by(value_of(before), value_of(v), tol)) {
+      if (r < p.k) {
+        doubt |= !same_key(p, row, expert, e);
+      } else {   // the border: of all keys that follow
+        uint32_t close = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) close |= u[i] > kMasked && near_by(value_of(before), value_of(u[i]), tol) ? 1u << i : 0u;
+        bool other = false;
+        for (; close != 0; close &= close - 1) other |= !same_key(p, row, expert, e0 + __ffs(close) - 1);
+        __syncwarp(mine);
+        doubt |= (__ballot_sync(mine, other) & mine) != 0;
+      }
+    }
     before = v;
     expert = e;
     if (r == p.k) break;
@@ -619,7 +647,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         const uint32_t last = __ballot_sync(mask, e0 < p.E && above == p.top - 1) & mine;
         const uint32_t next = __ballot_sync(mask, e0 < p.E && above == p.top) & mine;
         const float sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
-        if (near_by(sl, sn, 2.f * tol)) above = groups_above64<G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol);
+        if (near_by(sl, sn, 2.f * tol) && !flat<G, NV>(p, row, token, lane, e0))
+          above = groups_above64<G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol);
         __syncwarp();
       }
       if (above >= p.top) {
@@ -656,7 +685,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
       if (kKeys) {
         lo = -group_fmax<G>(-lo, mask);
         hi = group_fmax<G>(hi, mask);
-        if (near_by(lo, hi, 2.f * tol)) drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol);
+        if (near_by(lo, hi, 2.f * tol) && !flat<G, NV>(p, row, token, lane, e0))
+          drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol);
         __syncwarp();
       }
 #pragma unroll

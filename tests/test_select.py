@@ -193,6 +193,26 @@ def test_ties_and_near_ties(moe, score, E, groups, k):
     check(moe, l - 40, torch.ones(E, device="cuda"), k, score, renorm=1, **groups)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_flat_tokens(moe, score, dtype):
+    """Tokens whose logits are all one number (padding, an untrained router), some of their experts masked, one of them
+    the least bit larger: with equal biases, with biases, and with one bias the least bit larger."""
+    for E, k, groups in ((256, 8, dict(groups=8, top=4, group_top=2)), (256, 20, dict()), (64, 6, dict()), (40, 6, dict(groups=5, top=2, group_top=2)),
+                         (512, 10, dict(groups=64, top=9, group_top=2)), (1024, 32, dict())):
+        l = torch.zeros(64, E, device="cuda")
+        l[8:16] = 3.0
+        l[16:24, ::3] = -INF
+        l[24:40].scatter_(1, torch.randint(0, E, (16, 1), device="cuda", generator=torch.Generator("cuda").manual_seed(E)), 2.0 ** -20)
+        l[40:48] = rand((8, E), E)
+        l = l.to(TYPES[dtype])
+        b = torch.full((E,), 0.5, device="cuda")
+        for bias in (None, torch.zeros(E, device="cuda"), b, b + rand((E,), 1, 0.1)):
+            check(moe, l, bias, k, score, renorm=1, **groups)
+        b[E - 1] += 2.0 ** -24
+        check(moe, l, b, k, score, renorm=1, **groups)
+
+
 def test_large_biases(moe):
     l, b = rand((300, 64), 1), rand((64,), 2, 300.0)
     b[::2] = b[1::2]   # pairs with one bias: the scores decide
