@@ -9,11 +9,12 @@
 // fewer experts left than that, more than 32 candidates.  The slots' weights are then formed one slot a lane, from
 // the logits themselves.
 //
-// Measured: 65536 tokens of 256 experts, k = 8, 4 of 8 groups, sigmoid, bias, fp32 54 us, 10.6 of them to read and write
-// (91 with rounds, and 136 with every doubt settled for the whole token): issue of ~650 instructions a token, two
-// thirds on the ALU; 8192 of 8, k = 2, 2.4 us; 65536 of 256 in bf16 without groups 42 us, and with biases of 0, where
-// many keys are equal, 41.  16 lanes a token of 256 experts rather than 32: 56 and 71 us when that was tried.  The
-// gradient of the first 13.3 us, 5.5 TB/s, 10.9 to read and write.
+// Measured: 65536 tokens of 256 experts, k = 8, 4 of 8 groups, sigmoid, bias, fp32 58 us, 10.6 of them to read and write
+// (91 with rounds alone, 136 with every doubt settled for the whole token): issue of ~650 instructions a token, two
+// thirds on the ALU, and at the end of the kernel the last tokens in doubt; 8192 of 8, k = 2, 2.4 us; 65536 of 256 in bf16
+// without groups 44 us, with biases of 0, where many keys are equal, 42, and with all logits equal 132 (202 in
+// groups).  16 lanes a token of 256 experts rather than 32: 56 and 71 us when that was tried.  The gradient of the
+// first 13.3 us, 5.5 TB/s, 10.9 to read and write.
 //
 // Which expert wins must not hang on the rounding of a score, so the order is that of the keys in 64 bits:
 //   - without a bias and without sums of keys (groups scored by two) the order of the keys is the order of the
@@ -29,7 +30,7 @@
 // 2^-19 max(1, |key|) is what is asked for.  A softmax's sum of at most 32 + 5 rounded additions is
 // 2^-18.7 off in one direction for all experts, so twice as much is asked for there, and for sums of two keys.
 // The kernels are built once for fp32 logits (select_fp32.cu) and once for 16-bit ones (select_16.cu), which look up which
-// of the two types they have: types looked up in one build cost 10% (51 : 57 us, gradient 4.1 : 4.6), a build
+// of the two types they have: types looked up in one build cost 10% when that was tried (51 : 57 us, gradient 4.1 : 4.6), a build
 // for each of three types most of the time to compile.
 #pragma once
 
@@ -371,7 +372,18 @@ __device__ __forceinline__ bool near_by(float hi, float lo, float by) {
 template <int G, int NV>
 __device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0) {
   const uint32_t mine = group_mask<G>(lane);
+  // (first their keys in 32 bits, which are at hand: nearly always these differ)
   float lo = INFINITY, hi = -INFINITY, blo = INFINITY, bhi = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const float v = token.key(e0 + i);
+    hi = fmaxf(hi, v);
+    if (v > -INFINITY) lo = fminf(lo, v);
+  }
+  __syncwarp(mine);
+  if (-group_fmax<G>(-lo, mine) != group_fmax<G>(hi, mine)) return false;
+  lo = INFINITY;
+  hi = -INFINITY;
   for (int i = 0; i < NV && e0 + i < p.E; ++i) {
     if (!(token.key(e0 + i) > -INFINITY)) continue;
     const float x = logit(p, row + e0 + i), b = p.bias != nullptr ? p.bias[e0 + i] : 0.f;
@@ -385,10 +397,11 @@ __device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>&
 }
 
 // How many groups come before this lane's, by scores in 64 bits of the keys that may be among a group's largest.
-// `least`: the smallest key that the group's score counts.
+// `least`: the smallest key that the group's score counts; `above`: the answer of the scores in 32 bits.
 template <int G, int NV>
 __device__ __noinline__ int groups_above64(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, float m,
-                                           float least, float tol) {
+                                           float least, float tol, int above) {
+  if (flat<G, NV>(p, row, token, lane, e0)) return above;
   const uint32_t mine = group_mask<G>(lane);
   const int lanes = p.per / NV, g = e0 / p.per;
   const double total = softmax64<G, NV>(p, row, e0, m, mine);
@@ -403,7 +416,7 @@ __device__ __noinline__ int groups_above64(const SelParams& p, int64_t row, Toke
   __syncwarp(mine);
   for (int o = lanes / 2; o > 0; o >>= 1) top2_merge(a, b, __shfl_xor_sync(mine, a, o), __shfl_xor_sync(mine, b, o));
   const double s = p.sum == 2 && b > -INFINITY ? a + b : a;
-  int above = 0;
+  above = 0;
   for (int h = 0; h < p.n; ++h) {
     const double o = __shfl_sync(mine, s, h * lanes, G);
     above += h < g ? o >= s : o > s;
@@ -414,7 +427,8 @@ __device__ __noinline__ int groups_above64(const SelParams& p, int64_t row, Toke
 // The same for groups that do not fall on lanes, a group a lane: the groups that go, a bit each, those of this lane's.
 template <int G, int NV>
 __device__ __noinline__ uint64_t groups_dropped64(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, float m,
-                                                  float tol) {
+                                                  float tol, uint64_t drop) {
+  if (flat<G, NV>(p, row, token, lane, e0)) return drop;
   const uint32_t mine = group_mask<G>(lane);
   const int li = lane & (G - 1);
   const double total = softmax64<G, NV>(p, row, e0, m, mine);
@@ -437,7 +451,7 @@ __device__ __noinline__ uint64_t groups_dropped64(const SelParams& p, int64_t ro
     token.wide[g] = p.sum == 2 && b > -INFINITY ? a + b : a;
   }
   __syncwarp(mine);
-  uint64_t drop = 0;
+  drop = 0;
   for (int g = li; g < p.n; g += G) {
     const double s = token.wide[g];
     int above = 0;
@@ -647,8 +661,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         const uint32_t last = __ballot_sync(mask, e0 < p.E && above == p.top - 1) & mine;
         const uint32_t next = __ballot_sync(mask, e0 < p.E && above == p.top) & mine;
         const float sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
-        if (near_by(sl, sn, 2.f * tol) && !flat<G, NV>(p, row, token, lane, e0))
-          above = groups_above64<G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol);
+        if (near_by(sl, sn, 2.f * tol))
+          above = groups_above64<G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol, above);
         __syncwarp();
       }
       if (above >= p.top) {
@@ -685,8 +699,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
       if (kKeys) {
         lo = -group_fmax<G>(-lo, mask);
         hi = group_fmax<G>(hi, mask);
-        if (near_by(lo, hi, 2.f * tol) && !flat<G, NV>(p, row, token, lane, e0))
-          drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol);
+        if (near_by(lo, hi, 2.f * tol)) drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol, drop);
         __syncwarp();
       }
 #pragma unroll
