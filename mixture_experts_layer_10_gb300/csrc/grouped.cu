@@ -413,9 +413,9 @@ __device__ __forceinline__ void umma_commit_both(uint64_t* bar, int lead) {
 
 // Barriers (the same offsets in both CTAs; who uses which copy):
 //   full[s]     even CTA: the stage's operands of both CTAs are in place (TMA bytes; 8-bit integers: the
-//               warps that widened them)
+//               warps that widened them; 4-bit: the bytes, and the warps that brought the scales)
 //   empty[s]    stage free: committed to the even CTA, whose producer forwards it to the odd one when it
-//               refills the stage (8-bit integers: committed to both, the widening warps wait)
+//               refills the stage (8-bit integers, 4-bit: committed to both, whose warps wait too)
 //   tfull[a]    each CTA: accumulator a is complete
 //   tempty[a]   even CTA: both CTAs' epilogues have read it
 //   raw[s]      8-bit integers, own CTA: the bytes of a raw stage
