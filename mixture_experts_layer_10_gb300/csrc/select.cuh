@@ -725,7 +725,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
     const float sorted = NV > 1 ? sort_pairs<G>(best[0], best[1], li) : sort_lanes<G>(best[0], li);
     float bound = __shfl_sync(mask, sorted, p.k, G);
     rounds = !(fabsf(bound) < INFINITY);
-    if (kKeys) bound -= 2.f * tol * fmaxf(1.f, fabsf(bound));
+    // (not past the lowest number: masked experts, groups that go and lanes past the last expert have -inf and are none)
+    if (kKeys) bound = fmaxf(bound - 2.f * tol * fmaxf(1.f, fabsf(bound)), -FLT_MAX);
     uint32_t bits = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) bits |= key[i] >= bound ? 1u << i : 0u;
