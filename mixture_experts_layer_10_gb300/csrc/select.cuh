@@ -28,7 +28,8 @@
 // relatively; of a sigmoid, s (1 - s) |x| <= 0.23 of that counts, so s is off by less than 2^-21.6 and the sum
 // with the bias by 2^-24 of itself: two keys differ wrongly by less than 2^-20.5 + 2^-23 |key|, and
 // 2^-19 max(1, |key|) is what is asked for.  A softmax's sum of at most 32 + 5 rounded additions is
-// 2^-18.7 off in one direction for all experts, so twice as much is asked for there, and for sums of two keys.
+// 2^-18.7 off in one direction for all experts, so twice as much is asked for there.  A sum of two keys is off by as much as
+// both together and its own rounding, 2^-20.5 + 2^-22 times the larger magnitude of the two, however small it is itself.
 // The kernels are built once for fp32 logits (select_fp32.cu) and once for 16-bit ones (select_16.cu), which look up which
 // of the two types they have: types looked up in one build cost 10% when that was tried (51 : 57 us, gradient 4.1 : 4.6), a build
 // for each of three types most of the time to compile.
@@ -357,7 +358,7 @@ struct Token {
   int who[kMaxCand];
   union {
     double wide[kMaxExpertGroups];    // in 64 bits: candidates' keys, or scores
-    float scores[kMaxExpertGroups];   // of groups that do not fall on lanes
+    float scores[2][kMaxExpertGroups];   // of groups that do not fall on lanes, and what they may be off
   };
   __device__ __forceinline__ float& key(int e) { return keys[e + e / NV * kPad]; }
 };
@@ -365,6 +366,13 @@ struct Token {
 // Whether two keys, the larger one first, may stand the other way round.  (Infinities do not.)
 __device__ __forceinline__ bool near_by(float hi, float lo, float by) {
   return hi < INFINITY && hi - lo <= by * fmaxf(1.f, fabsf(hi));
+}
+
+// What the score of a group with the largest keys a >= b may be off: as much as these are, which their sum need not
+// show (1000 and -1000 add up to about nothing).
+__device__ __forceinline__ float score_off(const SelParams& p, float a, float b, float tol) {
+  const float most = p.sum == 2 && b > -INFINITY ? fmaxf(fabsf(a), fabsf(b)) : fabsf(a);
+  return tol * fmaxf(1.f, most);
 }
 
 // Whether all of a token's experts that are not masked have one logit and one bias (a token of zeros, a router that has
@@ -661,7 +669,11 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         const uint32_t last = __ballot_sync(mask, e0 < p.E && above == p.top - 1) & mine;
         const uint32_t next = __ballot_sync(mask, e0 < p.E && above == p.top) & mine;
         const float sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
-        if (near_by(sl, sn, 2.f * tol))
+        // no group may cross the border if none reaches the middle between the two at it.  (Where one of these is infinite,
+        // so are all on its side of the border, which no rounding moves; other infinite scores reach nowhere or NaN.)
+        const float cut = 0.5f * sl + 0.5f * sn, off = score_off(p, a, b, tol);
+        const bool reach = e0 < p.E && (above < p.top ? s - off <= cut : s + off >= cut);
+        if ((__ballot_sync(mask, reach) & mine) != 0 && sl < INFINITY && sn > -INFINITY)
           above = groups_above64<G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol, above);
         __syncwarp();
       }
@@ -680,26 +692,28 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
           b = fmaxf(b, fminf(a, v));
           a = fmaxf(a, v);
         }
-        token.scores[g] = p.sum == 2 && b > -INFINITY ? a + b : a;
+        token.scores[0][g] = p.sum == 2 && b > -INFINITY ? a + b : a;
+        token.scores[1][g] = score_off(p, a, b, tol);
       }
       __syncwarp();
-      float lo = INFINITY, hi = -INFINITY;   // the lowest score kept, the highest dropped
+      // how low those kept may reach, and how high those dropped (infinite ones as above)
+      float lo = INFINITY, hi = -INFINITY;
       uint64_t drop = 0;
       for (int g = li; g < p.n; g += G) {
-        const float s = token.scores[g];
+        const float s = token.scores[0][g], off = token.scores[1][g];
         int above = 0;
-        for (int h = 0; h < p.n; ++h) above += h < g ? token.scores[h] >= s : token.scores[h] > s;
+        for (int h = 0; h < p.n; ++h) above += h < g ? token.scores[0][h] >= s : token.scores[0][h] > s;
         if (above < p.top) {
-          lo = fminf(lo, s);
+          lo = fminf(lo, s - off);
         } else {
-          hi = fmaxf(hi, s);
+          hi = fmaxf(hi, s + off);
           drop |= (uint64_t)1 << g;
         }
       }
       if (kKeys) {
         lo = -group_fmax<G>(-lo, mask);
         hi = group_fmax<G>(hi, mask);
-        if (near_by(lo, hi, 2.f * tol)) drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol, drop);
+        if (lo <= hi && lo < INFINITY && hi > -INFINITY) drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol, drop);
         __syncwarp();
       }
 #pragma unroll

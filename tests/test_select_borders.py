@@ -26,3 +26,39 @@ def test_biases_of_the_lowest_value(moe, E, k, groups, score):
         l[-1, : E // 2] = -INF
         for renorm in (0, 1):
             check(moe, l, b, k, score, renorm=renorm, **groups)
+
+
+# groups that fall on lanes, and groups that do not
+LAYOUTS = [(256, dict(groups=8, top=4, group_top=2)), (120, dict(groups=5, top=2, group_top=2))]
+
+
+@pytest.mark.parametrize("per", [4, 5])
+def test_two_keys_that_cancel(moe, per):
+    """Biases of 1000 and -1000 are in a group's two largest keys, whose sum is about 1: in 32 bits each key has lost 2^-15,
+    and the sums of 1.000040 and 1.000031 are 1.0 and 1.000061."""
+    b = torch.full((2 * per,), -3000.0, device="cuda")
+    b[0::per], b[1::per] = 1000.0, -1000.0
+    l = torch.zeros(3, 2 * per, device="cuda")
+    s = torch.tensor([0.50002, 0.50002, 0.500031, 0.4999999], dtype=torch.float64)
+    l[1, [0, 1, per, per + 1]] = torch.logit(s).float().cuda()
+    check(moe, l, b, 2, "sigmoid", groups=2, top=1, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", LAYOUTS)
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e6, 1e9])
+def test_groups_with_large_biases_of_both_signs(moe, size, E, groups, score):
+    T, per = 3000, E // groups["groups"]
+    l = rand((T, E), int(size) % 1000 + E)
+    g = torch.Generator("cuda").manual_seed(E)
+    one = torch.full((E,), -size, device="cuda")
+    one[::per] = size                                             # one of every group above, the rest below
+    some = torch.where(torch.rand(E, device="cuda", generator=g) < 0.5, size, -size)
+    some[: 2 * per] = -size
+    some[per] = size                                              # (a group of one sign, one with a single large key)
+    few = torch.zeros(E, device="cuda")
+    few[per + 1 : 2 * per] = -size                                # a group of one expert and others switched off
+    few[2 * per : 3 * per] = -size                                # and of none else
+    for b in (one, some, few, one + rand((E,), 1, 0.1)):
+        check(moe, l, b, 6, score, renorm=1, **groups)
+    check(moe, l.bfloat16(), one, 6, score, renorm=1, **groups)
