@@ -368,8 +368,13 @@ __device__ __forceinline__ bool near_by(float hi, float lo, float by) {
   return hi < INFINITY && hi - lo <= by * fmaxf(1.f, fabsf(hi));
 }
 
-// What the score of a group with the largest keys a >= b may be off: as much as these are, which their sum need not
-// show (1000 and -1000 add up to about nothing).
+// The score of a group with the largest keys a >= b.  A sum of finite keys that 32 bits do not hold is the number next to
+// it that they do, so that it stays apart from infinite scores; among such sums the border is then in doubt.
+__device__ __forceinline__ float score_of(const SelParams& p, float a, float b) {
+  return p.sum == 2 && b > -INFINITY && a < INFINITY ? fminf(fmaxf(a + b, -FLT_MAX), FLT_MAX) : a;
+}
+// What it may be off: as much as these are, which their sum need not show
+// (1000 and -1000 add up to about nothing).
 __device__ __forceinline__ float score_off(const SelParams& p, float a, float b, float tol) {
   const float most = p.sum == 2 && b > -INFINITY ? fmaxf(fabsf(a), fabsf(b)) : fabsf(a);
   return tol * fmaxf(1.f, most);
@@ -658,7 +663,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         b = fmaxf(fmaxf(b, ob), fminf(a, oa));
         a = fmaxf(a, oa);
       }
-      const float s = p.sum == 2 && b > -INFINITY ? a + b : a;
+      const float s = score_of(p, a, b);
       const int g = e0 / p.per;   // (of a lane past the last expert: no group's)
       int above = 0;
       for (int h = 0; h < p.n; ++h) {
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
           b = fmaxf(b, fminf(a, v));
           a = fmaxf(a, v);
         }
-        token.scores[0][g] = p.sum == 2 && b > -INFINITY ? a + b : a;
+        token.scores[0][g] = score_of(p, a, b);
         token.scores[1][g] = score_off(p, a, b, tol);
       }
       __syncwarp();

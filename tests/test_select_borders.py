@@ -62,3 +62,41 @@ def test_groups_with_large_biases_of_both_signs(moe, size, E, groups, score):
     for b in (one, some, few, one + rand((E,), 1, 0.1)):
         check(moe, l, b, 6, score, renorm=1, **groups)
     check(moe, l.bfloat16(), one, 6, score, renorm=1, **groups)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("per", [8, 5])
+def test_sums_past_the_largest_number(moe, per, score):
+    """Groups whose two largest biases add up beyond fp32: by their sums all the same, before an infinite one and the masked
+    last."""
+    n = 8
+    l = rand((90, n * per), per)
+    l[5:9, :: 2] = -INF
+    b = torch.zeros(n * per, device="cuda")
+    top = b.view(n, per)
+    top[:] = -3.3e38
+    for sign in (1.0, -1.0):
+        for g, (x, y) in enumerate([(3.0, 0.5), (3.0, 1.0), (3.0, 3.0), (3.2, 3.1), (2.0, 1.0), (3.0, 3.0)]):
+            top[g, 0], top[g, 1] = sign * x * 1e38, sign * y * 1e38
+        for last in (LOWEST, -INF, INF, 0.0):
+            top[6] = last
+            top[7, 1:] = LOWEST     # a group of one and others switched off: its sum is below the lowest number, too
+            top[7, 0] = 0.0
+            for keep in (1, 2, 3, 5, 7):
+                check(moe, l, b, min(6, keep * per), score, renorm=1, groups=n, top=keep, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", LAYOUTS)
+def test_groups_switched_off_by_the_lowest_value(moe, E, groups, score):
+    """Two, one or no expert of a group left by biases of the lowest value, beside masked groups."""
+    n, per = groups["groups"], E // groups["groups"]
+    l, b = rand((200, E), E), rand((E,), 1, 0.1)
+    l[10:60, :per] = -INF
+    l[40:90, (n - 1) * per :] = -INF
+    l[100:, ::3] = -INF
+    b[2:per] = LOWEST
+    b[per + 1 : 2 * per] = LOWEST
+    b[2 * per : 4 * per] = LOWEST
+    for top in range(1, n):
+        check(moe, l, b, 6, score, renorm=1, **{**groups, "top": top})
