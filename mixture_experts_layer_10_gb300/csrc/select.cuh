@@ -381,9 +381,11 @@ __device__ __forceinline__ float score_off(const SelParams& p, float a, float b,
 }
 
 // Whether all of a token's experts that are not masked have one logit and one bias (a token of zeros, a router that has
-// learned nothing): all its keys are one number then, whatever its bits, and sums of as many of them are.
+// learned nothing): all its keys are one number then, whatever its bits, and so are sums of as many of them.  Where a
+// group's score is of one key and another's of two (`uneven`, in any lane), their order hangs on the key's sign, which its
+// 32 bits tell only of a key beyond its error, and on a sum that they hold.
 template <int G, int NV>
-__device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0) {
+__device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, bool uneven, float tol) {
   const uint32_t mine = group_mask<G>(lane);
   // (first their keys in 32 bits, which are at hand: nearly always these differ)
   float lo = INFINITY, hi = -INFINITY, blo = INFINITY, bhi = -INFINITY;
@@ -394,7 +396,9 @@ __device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>&
     if (v > -INFINITY) lo = fminf(lo, v);
   }
   __syncwarp(mine);
-  if (-group_fmax<G>(-lo, mine) != group_fmax<G>(hi, mine)) return false;
+  const float key = group_fmax<G>(hi, mine);
+  if (-group_fmax<G>(-lo, mine) != key) return false;
+  if ((__ballot_sync(mine, uneven) & mine) != 0 && !(fabsf(key) > tol && fabsf(key) <= FLT_MAX / 2)) return false;
   lo = INFINITY;
   hi = -INFINITY;
   for (int i = 0; i < NV && e0 + i < p.E; ++i) {
@@ -410,11 +414,15 @@ __device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>&
 }
 
 // How many groups come before this lane's, by scores in 64 bits of the keys that may be among a group's largest.
-// `least`: the smallest key that the group's score counts; `above`: the answer of the scores in 32 bits.
+// `least`: the smallest key that the group's score counts (-inf: it is of the other key alone); `above`: the answer of the
+// scores in 32 bits.
 template <int G, int NV>
 __device__ __noinline__ int groups_above64(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, float m,
                                            float least, float tol, int above) {
-  if (flat<G, NV>(p, row, token, lane, e0)) return above;
+  bool live = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) live |= token.key(e0 + i) > -INFINITY;
+  if (flat<G, NV>(p, row, token, lane, e0, live && least == -INFINITY, tol)) return above;
   const uint32_t mine = group_mask<G>(lane);
   const int lanes = p.per / NV, g = e0 / p.per;
   const double total = softmax64<G, NV>(p, row, e0, m, mine);
@@ -440,8 +448,8 @@ __device__ __noinline__ int groups_above64(const SelParams& p, int64_t row, Toke
 // The same for groups that do not fall on lanes, a group a lane: the groups that go, a bit each, those of this lane's.
 template <int G, int NV>
 __device__ __noinline__ uint64_t groups_dropped64(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, float m,
-                                                  float tol, uint64_t drop) {
-  if (flat<G, NV>(p, row, token, lane, e0)) return drop;
+                                                  float tol, bool uneven, uint64_t drop) {
+  if (flat<G, NV>(p, row, token, lane, e0, uneven, tol)) return drop;
   const uint32_t mine = group_mask<G>(lane);
   const int li = lane & (G - 1);
   const double total = softmax64<G, NV>(p, row, e0, m, mine);
@@ -690,6 +698,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
     } else {
       // groups that do not fall on lanes: through shared memory, a group a lane
       __syncwarp();
+      bool uneven = false;   // a score of one key among those of two
       for (int g = li; g < p.n; g += G) {
         float a = -INFINITY, b = -INFINITY;
         for (int e = g * p.per; e < (g + 1) * p.per; ++e) {
@@ -697,6 +706,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
           b = fmaxf(b, fminf(a, v));
           a = fmaxf(a, v);
         }
+        uneven |= p.sum == 2 && a > b && b == -INFINITY;
         token.scores[0][g] = score_of(p, a, b);
         token.scores[1][g] = score_off(p, a, b, tol);
       }
@@ -718,7 +728,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
       if (kKeys) {
         lo = -group_fmax<G>(-lo, mask);
         hi = group_fmax<G>(hi, mask);
-        if (lo <= hi && lo < INFINITY && hi > -INFINITY) drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol, drop);
+        if (lo <= hi && lo < INFINITY && hi > -INFINITY)
+          drop = groups_dropped64<G, NV>(p, row, token, lane, e0, m, tol, uneven, drop);
         __syncwarp();
       }
 #pragma unroll

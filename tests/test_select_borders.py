@@ -100,3 +100,25 @@ def test_groups_switched_off_by_the_lowest_value(moe, E, groups, score):
     b[2 * per : 4 * per] = LOWEST
     for top in range(1, n):
         check(moe, l, b, 6, score, renorm=1, **{**groups, "top": top})
+
+
+@pytest.mark.parametrize("E,n", [(64, 8), (256, 8), (40, 5), (120, 5), (1024, 64)])
+def test_flat_tokens_of_uneven_groups(moe, E, n):
+    """Tokens of one logit whose masks leave some groups a single expert: the score of those is one key, that of the others
+    two, also where 32 bits hold the key as 0, or as near to it as its error, of either sign."""
+    per = E // n
+    at = torch.arange(E, device="cuda")
+    for top in (1, 2, n - 1):
+        for x, b in ((-100.0, None), (-600.0, None), (0.0, None), (0.0, -0.5), (-100.0, 0.0), (1.0, -0.7310586), (1.0, -0.73105854),
+                     (-3.0, -0.04742587), (-3.0, -0.047425874), (12.0, -1.0), (3.0, 5.0)):
+            l = torch.full((8, E), x, device="cuda")
+            l[1, 1:per] = -INF                           # the first group has one expert
+            l[2, (at >= per) & (at % per != per - 1)] = -INF   # all but the first
+            l[3, at % (2 * per) >= 1] = -INF             # every other one, the rest none
+            l[4, at % per != 0] = -INF                   # all
+            l[5, (n - 1) * per + 1 :] = -INF             # the last
+            l[6, (at % (2 * per) >= 1) & (at % (2 * per) < per)] = -INF
+            bias = None if b is None else torch.full((E,), b, device="cuda")
+            check(moe, l, bias, min(4, top), "sigmoid", renorm=1, groups=n, top=top, group_top=2)
+            if b is not None:
+                check(moe, l, bias, min(4, top), "softmax", renorm=1, groups=n, top=top, group_top=2)
