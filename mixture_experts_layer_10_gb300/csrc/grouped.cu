@@ -58,6 +58,7 @@
 // 14336 to 512: four, 67 us).
 #include <algorithm>
 
+#include "clusters.cuh"
 #include "common.cuh"
 #include "grouped.cuh"
 #include "ptx.cuh"
@@ -1050,7 +1051,7 @@ Params params_of(const Grouped& c, const int32_t* begin, const int32_t* end, Hdr
   return p;
 }
 
-// How many clusters run at once.
+// How many clusters run at once (-1: clusters of several pairs cannot).
 template <int kOp, int kSplit = 1, int kTurn = 4>
 cudaError_t clusters_at_once(int* fit) {
   using S = Shape<kOp>;
@@ -1065,11 +1066,9 @@ cudaError_t clusters_at_once(int* fit) {
     cfg.blockDim = dim3(S::kThreads, 1, 1);
     cfg.dynamicSmemBytes = S::kSmem;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, grouped_kernel<kOp, kSplit, kTurn>, &cfg) != cudaSuccess || n <= 0) {
-      (void)cudaGetLastError();
-      n = num_sms() / kSize;
-    }
-    return std::min(n, num_sms() / kSize);
+    const bool ok = cudaOccupancyMaxActiveClusters(&n, grouped_kernel<kOp, kSplit, kTurn>, &cfg) == cudaSuccess;
+    if (!ok) (void)cudaGetLastError();
+    return clusters_that_fit(ok, n, num_sms(), kSize);
   });
 }
 
@@ -1196,13 +1195,15 @@ cudaError_t launch_grouped_mxf4(const Grouped& c, const int32_t* begin, const in
   // 42 at 384 rows of 64, 4096 x 1408; 23.8 : 22.2 at 384 rows of 64, 2048 x 1408.
   const int64_t tiles = most_row_tiles(c, kMxRows) * (p.nf + p.narrow);
   if ((p.depth + kMxWide - 1) / kMxWide >= kMxSplit) {
-    int fit = 0;
-    cudaError_t e = clusters_at_once<kMx, 4, 8>(&fit);
-    if (e == cudaSuccess && tiles <= fit) return launch<kMx, 4, 8>(p, tiles, kKGroupedMxf4, s);
-    if (e == cudaSuccess) e = clusters_at_once<kMx, 2, 8>(&fit);
-    if (e == cudaSuccess && tiles <= fit) return launch<kMx, 2, 8>(p, tiles, kKGroupedMxf4, s);
+    cudaError_t e = cudaSuccess;
+    const int pairs = pairs_per_tile(tiles, [&e](int n) {
+      int fit = -1;
+      if (e == cudaSuccess) e = n == 4 ? clusters_at_once<kMx, 4, 8>(&fit) : clusters_at_once<kMx, 2, 8>(&fit);
+      return fit;
+    });
     if (e != cudaSuccess) return e;
-    return launch<kMx, 1, 8>(p, tiles, kKGroupedMxf4, s);
+    if (pairs == 4) return launch<kMx, 4, 8>(p, tiles, kKGroupedMxf4, s);
+    return pairs == 2 ? launch<kMx, 2, 8>(p, tiles, kKGroupedMxf4, s) : launch<kMx, 1, 8>(p, tiles, kKGroupedMxf4, s);
   }
   return launch<kMx>(p, tiles, kKGroupedMxf4, s);
 }

@@ -104,7 +104,7 @@ struct SmemOnce {
   }
 };
 
-// A positive number of a device, found by the first call there (of several threads at once, by each of them:
+// A number of a device that is not 0, found by the first call there (of several threads at once, by each of them:
 // the answer is the same).
 struct IntOnce {
   std::atomic<int> found[64] = {};
