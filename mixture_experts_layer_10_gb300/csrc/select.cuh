@@ -368,22 +368,20 @@ __device__ __forceinline__ bool near_by(float hi, float lo, float by) {
   return hi < INFINITY && hi - lo <= by * fmaxf(1.f, fabsf(hi));
 }
 
-// The score of a group with the largest keys a >= b.  A sum of finite keys that 32 bits do not hold is the number next to
-// it that they do, so that it stays apart from infinite scores; among such sums the border is then in doubt.
-__device__ __forceinline__ float score_of(const SelParams& p, float a, float b) {
-  return p.sum == 2 && b > -INFINITY && a < INFINITY ? fminf(fmaxf(a + b, -FLT_MAX), FLT_MAX) : a;
-}
-// What it may be off: as much as these are, which their sum need not show
-// (1000 and -1000 add up to about nothing).
-__device__ __forceinline__ float score_off(const SelParams& p, float a, float b, float tol) {
-  const float most = p.sum == 2 && b > -INFINITY ? fmaxf(fabsf(a), fabsf(b)) : fabsf(a);
-  return tol * fmaxf(1.f, most);
+// The score of a group with the largest keys a >= b, halved where it is the sum of both (b: 0 if there is no second), so that
+// finite keys give a finite one; and what it may be off: as much as the keys are, which their sum need not show (1000 and
+// -1000 add up to about nothing).  Logits are taken as they are.
+template <bool kKeys>
+__device__ __forceinline__ float2 score_of(const SelParams& p, float a, float b, float tol) {
+  if (!kKeys) return make_float2(a, 0.f);
+  b = p.sum == 1 ? a : (b > -INFINITY ? b : 0.f);
+  return make_float2(fmaf(0.5f, a, 0.5f * b), tol * fmaxf(0.5f, fmaxf(fabsf(0.5f * a), fabsf(0.5f * b))));
 }
 
 // Whether all of a token's experts that are not masked have one logit and one bias (a token of zeros, a router that has
 // learned nothing): all its keys are one number then, whatever its bits, and so are sums of as many of them.  Where a
 // group's score is of one key and another's of two (`uneven`, in any lane), their order hangs on the key's sign, which its
-// 32 bits tell only of a key beyond its error, and on a sum that they hold.
+// 32 bits tell only of a key beyond its error.
 template <int G, int NV>
 __device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>& token, int lane, int e0, bool uneven, float tol) {
   const uint32_t mine = group_mask<G>(lane);
@@ -398,7 +396,7 @@ __device__ __noinline__ bool flat(const SelParams& p, int64_t row, Token<G, NV>&
   __syncwarp(mine);
   const float key = group_fmax<G>(hi, mine);
   if (-group_fmax<G>(-lo, mine) != key) return false;
-  if ((__ballot_sync(mine, uneven) & mine) != 0 && !(fabsf(key) > tol && fabsf(key) <= FLT_MAX / 2)) return false;
+  if ((__ballot_sync(mine, uneven) & mine) != 0 && !(fabsf(key) > tol)) return false;
   lo = INFINITY;
   hi = -INFINITY;
   for (int i = 0; i < NV && e0 + i < p.E; ++i) {
@@ -671,7 +669,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         b = fmaxf(fmaxf(b, ob), fminf(a, oa));
         a = fmaxf(a, oa);
       }
-      const float s = score_of(p, a, b);
+      const float2 score = score_of<kKeys>(p, a, b, tol);
+      const float s = score.x;
       const int g = e0 / p.per;   // (of a lane past the last expert: no group's)
       int above = 0;
       for (int h = 0; h < p.n; ++h) {
@@ -684,7 +683,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
         const float sl = __shfl_sync(mask, s, __ffs(last) - 1), sn = __shfl_sync(mask, s, __ffs(next) - 1);
         // no group may cross the border if none reaches the middle between the two at it.  (Where one of these is infinite,
         // so are all on its side of the border, which no rounding moves; other infinite scores reach nowhere or NaN.)
-        const float cut = 0.5f * sl + 0.5f * sn, off = score_off(p, a, b, tol);
+        const float cut = 0.5f * sl + 0.5f * sn, off = score.y;
         const bool reach = e0 < p.E && (above < p.top ? s - off <= cut : s + off >= cut);
         if ((__ballot_sync(mask, reach) & mine) != 0 && sl < INFINITY && sn > -INFINITY)
           above = groups_above64<G, NV>(p, row, token, lane, e0, m, p.sum == 2 ? b : a, tol, above);
@@ -707,8 +706,9 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 16 ? 8 : 4) select_kernel(c
           a = fmaxf(a, v);
         }
         uneven |= p.sum == 2 && a > b && b == -INFINITY;
-        token.scores[0][g] = score_of(p, a, b);
-        token.scores[1][g] = score_off(p, a, b, tol);
+        const float2 score = score_of<kKeys>(p, a, b, tol);
+        token.scores[0][g] = score.x;
+        token.scores[1][g] = score.y;
       }
       __syncwarp();
       // how low those kept may reach, and how high those dropped (infinite ones as above)

@@ -122,3 +122,16 @@ def test_flat_tokens_of_uneven_groups(moe, E, n):
             check(moe, l, bias, min(4, top), "sigmoid", renorm=1, groups=n, top=top, group_top=2)
             if b is not None:
                 check(moe, l, bias, min(4, top), "softmax", renorm=1, groups=n, top=top, group_top=2)
+
+
+@pytest.mark.parametrize("per", [8, 5])
+def test_groups_of_subnormal_logits(moe, per):
+    """Without biases groups go by their largest logits as they are, to the last bit of the smallest numbers."""
+    n, T = 8, 60
+    step = torch.finfo(torch.float32).smallest_normal * 2.0 ** -23
+    g = torch.Generator("cuda").manual_seed(per)
+    l = torch.randint(-5, 6, (T, n * per), device="cuda", generator=g).float() * step
+    assert bool((l != 0).any())
+    for score in ("softmax", "sigmoid"):
+        for top in (1, 4, 7):
+            check(moe, l, None, min(6, top * per), score, renorm=1, groups=n, top=top, group_top=1)
