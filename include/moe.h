@@ -378,7 +378,8 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
  * layer's softmax and top-k (sigmoid scores, a bias that balances the load, groups of experts, scaled
  * weights), on the logits of moe_route or of the caller's own router.  The layer's other calls take what it
  * gives: moe_dispatch the experts, moe_combine the weights; back through them, moe_select_bwd makes dlogits of
- * the weights' gradients, moe_combine_bwd the input gradient and moe_router_wgrad the router's.
+ * the weights' gradients, moe_combine_bwd the input gradient and moe_router_wgrad the router's (the layer's calls have
+ * limits of their own: 256 experts, 2^20 tokens).
  *
  * For every token, with logits l [E] and the bias b [E]:
  *   s_e     = softmax(l)_e or sigmoid(l_e)
@@ -387,9 +388,10 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
  *             top_groups best stay (a tie goes to the lower group)
  *   idx     = the k largest keys among the groups that stay, larger first (a tie goes to the lower expert)
  *   w_j     = s[idx_j], with renorm s[idx_j] / sum_m s[idx_m]; times scale
- * The order of experts and groups is that of keys formed in 64 bits, whatever the type of the logits, and where there
- * is no bias and no sum of two keys, that of the logits, which is the scores' own; weights and gradients are computed in 32 bits, and renormalised weights are finite and sum to scale however small the
- * scores.
+ * The order of experts and groups is that of keys formed, and added up, in 64 bits, whatever the type of the logits and the
+ * size of the biases (two that are nearer than 64 bits' own rounding go as they round), and where there is no bias and no
+ * sum of two keys, that of the logits, which is the scores' own.  Weights and gradients are computed in 32 bits, and
+ * renormalised weights are finite and sum to scale however small the scores.
  *
  * Masks.  A logit of -inf masks its expert, as do a NaN and a bias of -inf or NaN: it counts in no group's
  * score, a group of masked experts only comes last, and it is chosen only where its token has fewer than k others left

@@ -45,7 +45,8 @@
 // 5.1 TB/s.  Steps on the way, same size: scales copied by tcgen05.cp 644 us; written to TMEM from registers
 // 525; by two teams in turn 474; one barrier a stage for operands and scales 434; one elected thread issuing 374; scales
 // a sector at a time 365; no bank conflicts on their way, and two sectors at a time 332.  (Tried and not kept: four
-// stages, tiles of equal height, weights fetched to L2 ahead, eight epilogue warps, naps of 100 ns: the same or slower.)
+// stages, 362 when five took 374, but slower at small sizes; tiles of equal height, weights fetched to L2 ahead, eight
+// epilogue warps, naps of 100 ns: the same or slower.)
 //
 // Measured (graph replays on inputs larger than L2; 36 launches / after three seconds of them, when the power
 // cap has lowered the clock): y of 16384 rows, 8 groups, 4096 x 14336, bf16: 1.14 / 1.19 ms, 1.69 / 1.62
@@ -93,7 +94,7 @@ constexpr int mx_pieces(int turn) { return (turn / 2 * kMxHand + 128 * kMxTeams 
 constexpr int mx_stage(int turn) { return 8 * kMxHand + 128 / turn; }
 constexpr uint32_t kMxScales = 2 * 8 * mx_stage(8);   // two hand-overs
 constexpr int kAheadMx = 2;                  // 4-bit: such times that are on their way
-constexpr int kMxSplit = 16;                 // K blocks of a tile from which two or four pairs share them
+constexpr int kMxSplit = 16;                 // K blocks of a tile (columns: 3872) from which two or four pairs share them
 constexpr int kMxCols = 24;                  // their TMEM columns: 2 words x (4 + 8)
 
 template <int kOp>

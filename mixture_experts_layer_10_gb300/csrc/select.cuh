@@ -12,9 +12,10 @@
 // Measured: 65536 tokens of 256 experts, k = 8, 4 of 8 groups, sigmoid, bias, fp32 58 us, 10.6 of them to read and write
 // (91 with rounds alone, 136 with every doubt settled for the whole token): issue of ~650 instructions a token, two
 // thirds on the ALU, and at the end of the kernel the last tokens in doubt; 8192 of 8, k = 2, 2.4 us; 65536 of 256 in bf16
-// without groups 44 us, with biases of 0, where many keys are equal, 42, and with all logits equal 132 (202 in
-// groups).  16 lanes a token of 256 experts rather than 32: 56 and 71 us when that was tried.  The gradient of the
-// first 13.3 us, 5.5 TB/s, 10.9 to read and write.
+// without groups and without a bias 25 to 28 us, with one 41 to 59 (sigmoid, renormalised: 44; biases of 0, where many
+// keys are equal, 43), and with all logits equal 134 (200 in groups).  16 lanes a token of 256 experts rather than 32: 56
+// and 71 us when that was tried.  The gradient of the first 13.3 us where dlogits stay in L2, 5.5 TB/s, 19.8 where they
+// do not, 10.9 to read and write.
 //
 // Which expert wins must not hang on the rounding of a score, so the order is that of the keys in 64 bits:
 //   - without a bias and without sums of keys (groups scored by two) the order of the keys is the order of the
